@@ -330,3 +330,11 @@ def all_to_all_v_combine(windows, outputs, recv_counts, atomic="none", stream=No
     a = {"none": ATOMIC_NONE, "add": ATOMIC_ADD}[atomic] if isinstance(atomic, str) else atomic
     return ptoc_all_to_all_v_combine(windows, outputs, recv_counts, tr, size, a,
                                      dtype_code(outputs[0]), stream=stream)
+
+
+# the layer operators of include/ptoc_layers.h (they use the names above)
+from .layers import (  # noqa: E402,F401
+    CKPT_BLOCK, MOE_MAX_EXPERTS, MOE_MAX_TOKENS, MOE_MAX_TOP_K, NORM_MAX_COLS, Checkpoint8, MoeLayer, block_norm,
+    block_norm_backward, block_norm_backward_workspace, checkpoint8, ptoc_block_norm, ptoc_block_norm_backward,
+    ptoc_block_norm_backward_workspace, ptoc_block_norm_params, ptoc_block_norm_saved, ptoc_checkpoint8, ptoc_ckpt8,
+    ptoc_matrix, ptoc_moe_few_tokens, ptoc_moe_few_tokens_workspace, ptoc_moe_params, ptoc_restore8, restore8)

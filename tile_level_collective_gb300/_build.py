@@ -1,8 +1,9 @@
 """Build libptoc.so in-tree for sm_103a (GB300).
 
-Each .cu under csrc/ is compiled by nvcc in parallel into _build/, then linked
-into tile_level_collective_gb300/libptoc.so. No fast-math, no FMA contraction
-concerns (the kernels add, compare and select only). Run as
+Each .cu under csrc/ and its folders is compiled by nvcc in parallel into
+_build/, then linked into tile_level_collective_gb300/libptoc.so. No fast-math;
+where the order and rounding of every operation is part of the contract (the
+collectives' sums) the kernels say so with intrinsics. Run as
 ``python tile_level_collective_gb300/_build.py`` or through
 ``__graft_entry__.build()``.
 """
@@ -33,12 +34,12 @@ def nvcc():
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "**", "*.cu"), recursive=True))
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + [os.path.join(INCLUDE, "ptoc.h"), os.path.abspath(__file__)]
+    return sources() + [f for ext in ("*.h", "*.cuh") for f in glob.glob(os.path.join(CSRC, "**", ext), recursive=True)] \
+        + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date():

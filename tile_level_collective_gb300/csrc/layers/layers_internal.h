@@ -1,0 +1,91 @@
+// Parameter blocks and launchers of the layer operators (see ptoc_layers.h).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include "ptoc_internal.h"
+#include "ptoc_layers.h"
+
+namespace ptoc {
+
+struct Ckpt;
+
+struct Ckpt8Params {
+    void* x;
+    int64_t ld;
+    ptoc_ckpt8 ckpt;
+    int64_t rows, cols;
+    int32_t vec;                  // 16-byte aligned bases and pitches
+};
+
+// The element types of the norms' parameters are dtype, or binary32 where
+// param_f32 is set.
+struct NormCommon {
+    const void *post_weight, *pre_weight, *gate;
+    int64_t gate_rs, gate_cs;
+    int32_t post_norm, param_f32;
+    float residual_scale, branch_scale, eps, inv_cols;
+    int64_t rows, cols;
+    int32_t vec;
+};
+
+struct NormParams {
+    const void* part[kMaxRanks];
+    NormCommon c;
+    int64_t ld_part;
+    const void* x;
+    int64_t ld_x;
+    void *out, *normed, *block_out;      // normed and block_out may be null
+    int64_t ld_out, ld_normed, ld_block;
+    ptoc_ckpt8 block_ckpt, stream_ckpt;  // codes null: not written
+    float* rstd;                         // may be null
+    int32_t nparts;
+};
+
+struct NormBackParams {
+    NormCommon c;
+    const void *block, *stream;          // null: read from the checkpoint
+    int64_t ld_block, ld_stream;
+    ptoc_ckpt8 block_ckpt, stream_ckpt;
+    const float* rstd;
+    const void *dy, *du;                 // du may be null
+    int64_t ld_dy, ld_du;
+    void *d_residual, *d_block;
+    int64_t ld_dres, ld_dblk;
+    float *d_pre, *d_post, *d_gate;      // may be null
+    float* partial;                      // [kinds, grid, cols] column sums of each block, in the workspace
+    int32_t gate_kind;                   // GateKind of d_gate
+    int32_t grid;
+};
+
+enum GateKind : int { kGateNone = 0, kGateScalar = 1, kGateChannel = 2, kGateToken = 3, kGateElement = 4 };
+
+// Blocks of the backward pass: each keeps column sums of its rows, so the
+// workspace holds this many partial rows for each kind of column sum.
+int norm_backward_grid(int64_t rows, int64_t cols);
+constexpr int kNormColumnSums = 3;       // d_pre, d_post, d_gate
+
+cudaError_t launch_checkpoint8(const Ckpt8Params& p, int dtype, cudaStream_t s);
+cudaError_t launch_restore8(const Ckpt8Params& p, int dtype, cudaStream_t s);
+cudaError_t launch_block_norm(const NormParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_block_norm_backward(const NormBackParams& p, int dtype, cudaStream_t s);
+
+struct MoeParams {
+    const void *x, *router, *w_in, *w_out;
+    const float* bias;
+    void* y;
+    int64_t ld_x, ld_y;
+    int32_t* ids;                        // user outputs, may be null
+    float* weights;
+    char* ws;                            // workspace
+    int64_t hidden, inter;
+    int32_t tokens, experts, first, local, top_k;
+    int32_t router_f32, sigmoid, renormalize, vec;
+    float scale;
+};
+
+size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k);
+cudaError_t launch_moe_few(const MoeParams& p, int dtype, cudaStream_t s);
+
+}  // namespace ptoc

@@ -9,22 +9,12 @@
 #include <mutex>
 
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
+#include "host/host_checks.h"
 #include "ptoc.h"
 #include "ptoc_internal.h"
 
 namespace ptoc {
-
-// A named NVTX range around the host side of every entry point (checks and
-// launches), so that timeline tools show the library's calls by name. With
-// no tool attached a range costs a few nanoseconds.
-struct TraceRange {
-    explicit TraceRange(const char* name) { nvtxRangePushA(name); }
-    ~TraceRange() { nvtxRangePop(); }
-    TraceRange(const TraceRange&) = delete;
-    TraceRange& operator=(const TraceRange&) = delete;
-};
 
 // The documented switch PTOC_PDL=0 turns programmatic dependent launch off.
 bool programmatic_launch()
@@ -47,10 +37,6 @@ bool staged_reduction(int64_t bytes)
     if (e && strcmp(e, "bulk") == 0) return true;
     if (e && (strcmp(e, "regs") == 0 || strcmp(e, "tma") == 0)) return false;
     return bytes >= kStagedMinBytes;
-}
-
-namespace {
-int sm_count();
 }
 
 int32_t first_wave_prefetch(int64_t bytes)
@@ -82,17 +68,6 @@ bool tensor_form_selected()
 
 namespace {
 
-int elem_size(int dtype)
-{
-    switch (dtype) {
-    case PTOC_F32: case PTOC_I32: return 4;
-    case PTOC_F16: case PTOC_BF16: return 2;
-    default: return 0;
-    }
-}
-
-bool valid_dtype(int dtype) { return elem_size(dtype) != 0; }
-
 // op of TREDUCE: Sum / Max / Min ([TR] §1.3); Prod belongs to the allreduce
 // family only.
 ptoc_status check_op(int op)
@@ -108,24 +83,6 @@ ptoc_status check_op_allreduce(int op)
     return (op >= PTOC_SUM && op <= PTOC_PROD) ? PTOC_OK : PTOC_ERR_INVALID_ARG;
 }
 
-// Byte range [lo, hi) a buffer occupies.
-struct Range {
-    uintptr_t lo, hi;
-};
-
-bool overlap(const Range& a, const Range& b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
-
-// Footprint in bytes of a [rows, cols] box with pitch ld, or -1 on overflow.
-int64_t footprint(int64_t rows, int64_t cols, int64_t ld, int eb)
-{
-    if (rows == 0 || cols == 0) return 0;
-    const int64_t lim = INT64_MAX / 8;
-    if (rows > lim / (ld > 0 ? ld : 1)) return -1;
-    const int64_t elems = (rows - 1) * ld + cols;
-    if (elems > lim / eb) return -1;
-    return elems * eb;
-}
-
 // The widest vector (16, 8, 4 or 2 bytes) that every address and the pitch
 // allow, never narrower than one element (addresses are element-aligned).
 int pick_vector_bytes(uintptr_t addr_or, int64_t pitch_bytes, int eb)
@@ -137,6 +94,8 @@ int pick_vector_bytes(uintptr_t addr_or, int64_t pitch_bytes, int eb)
 }
 
 std::atomic<int> g_sm_count[kMaxDevices];
+
+}  // namespace
 
 int current_device()
 {
@@ -157,6 +116,8 @@ int sm_count()
     if (dev < kMaxDevices) g_sm_count[dev].store(c, std::memory_order_relaxed);
     return c;
 }
+
+namespace {
 
 // The 4-byte tile counters of the claiming exchanges come from one small
 // memory pool per device, created on first use, that never returns its memory
@@ -245,11 +206,7 @@ dim3 grid_for(int64_t ntiles)
     return dim3((unsigned)(ntiles < cap ? (ntiles > 0 ? ntiles : 1) : cap));
 }
 
-// cuTensorMapEncodeTiled, reached through the runtime's driver entry point
-// (the library links no driver library); null if the driver lacks it.
-using TensorMapEncoder = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+}  // namespace
 
 TensorMapEncoder tensor_map_encoder()
 {
@@ -264,6 +221,8 @@ TensorMapEncoder tensor_map_encoder()
     });
     return fn;
 }
+
+namespace {
 
 // A tensor map over the valid box of a slice: {valid_cols, valid_rows}
 // elements, rows ld * eb bytes apart, boxes of kTmaBoxCols x (4 KiB / row
@@ -359,18 +318,6 @@ cudaError_t launch_reduction(int dtype, ReduceParams& p, int op, int64_t rows, i
     return launch_reduce_regs(dtype, p, op, vb, grid_for(p.ntiles + p.tail_blocks), s);
 }
 
-ptoc_status check_group(const ptoc_group* g, bool need_root)
-{
-    if (!g || !g->tensors) return PTOC_ERR_INVALID_ARG;
-    if (g->nranks < 1 || g->nranks > kMaxRanks) return PTOC_ERR_INVALID_ARG;
-    if (need_root && (g->root < 0 || g->root >= g->nranks)) return PTOC_ERR_INVALID_ARG;
-    for (int r = 0; r < g->nranks; ++r)
-        if (!g->tensors[r]) return PTOC_ERR_INVALID_ARG;
-    return PTOC_OK;
-}
-
-bool aligned(const void* p, int eb) { return ((uintptr_t)p % (uintptr_t)eb) == 0; }
-
 // Shared checks of the window collectives (reduce_scatter, allgather,
 // allreduce, broadcast): group, dtype, sizes, alignment, disjoint windows.
 ptoc_status check_windows(const ptoc_group* w, int64_t rows, int64_t cols, int64_t ld, int dtype,
@@ -392,31 +339,6 @@ ptoc_status check_windows(const ptoc_group* w, int64_t rows, int64_t cols, int64
             if (overlap(ra, rb)) return PTOC_ERR_ALIAS;
         }
     *fp_out = fp;
-    return PTOC_OK;
-}
-
-// Shared checks of the pairwise exchanges over [target_rows, size] buffers
-// (all_to_all_v, all_to_all, the combine). `writes` are the spans the call
-// writes, `reads` the ones it only reads; outputs must not overlap anything,
-// inputs may overlap each other.
-struct Span {
-    const void* p;
-    uintptr_t bytes;
-};
-
-ptoc_status check_disjoint_outputs(const Span* writes, int nw, const Span* reads, int nr)
-{
-    for (int a = 0; a < nw; ++a) {
-        const Range ra{(uintptr_t)writes[a].p, (uintptr_t)writes[a].p + writes[a].bytes};
-        for (int b = a + 1; b < nw; ++b) {
-            const Range rb{(uintptr_t)writes[b].p, (uintptr_t)writes[b].p + writes[b].bytes};
-            if (overlap(ra, rb)) return PTOC_ERR_ALIAS;
-        }
-        for (int b = 0; b < nr; ++b) {
-            const Range rb{(uintptr_t)reads[b].p, (uintptr_t)reads[b].p + reads[b].bytes};
-            if (overlap(ra, rb)) return PTOC_ERR_ALIAS;
-        }
-    }
     return PTOC_OK;
 }
 
