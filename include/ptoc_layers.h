@@ -49,8 +49,9 @@ typedef struct {
  * block itself, is smaller); codes[i * ld_codes + j] = x / 2^e rounded to the
  * nearest integer, ties to even. The division is exact, so the codes do not
  * depend on how it is computed, and a restored value (code * 2^e) has at most
- * 7 significant bits: it is exact in every element type (f16: where it is in
- * range). A block that holds an infinity or a NaN has exponent byte 255 and
+ * 7 significant bits: it is exact in every element type where it is in that
+ * type's range (a value within 2^-7 of the largest float can round up to 2^128
+ * and come back as infinity). A block that holds an infinity or a NaN has exponent byte 255 and
  * is restored as NaN. ld_codes >= cols, ld_exps >= ceil(cols / 32). */
 typedef struct {
     int8_t* codes;
@@ -104,13 +105,12 @@ ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts, const pto
                             int64_t rows, int64_t cols, ptoc_dtype dtype, cudaStream_t stream);
 
 /* What the backward pass reads of the forward pass: a and s, each either as a
- * matrix of the element type or as an 8-bit checkpoint (exactly one non-null),
- * and the statistics rstd ([2, rows]). */
+ * matrix of the element type or as an 8-bit checkpoint (of a matrix and its
+ * checkpoint exactly one has a non-null address), and the statistics rstd
+ * ([2, rows]). */
 typedef struct {
-    const ptoc_matrix* block;
-    const ptoc_ckpt8* block_ckpt;
-    const ptoc_matrix* stream;
-    const ptoc_ckpt8* stream_ckpt;
+    ptoc_matrix block, stream;
+    ptoc_ckpt8 block_ckpt, stream_ckpt;
     const float* rstd;
 } ptoc_block_norm_saved;
 

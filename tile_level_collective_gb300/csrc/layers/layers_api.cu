@@ -243,8 +243,10 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
     const TraceRange trace("ptoc_block_norm_backward");
     ptoc_status st = check_box(rows, cols, dtype);
     if (st != PTOC_OK) return st;
-    if (!saved || !dy || !d_residual || !d_block || !saved->rstd) return PTOC_ERR_INVALID_ARG;
-    if (!saved->block == !saved->block_ckpt || !saved->stream == !saved->stream_ckpt) return PTOC_ERR_INVALID_ARG;
+    if (!saved || !dy || !d_residual || !d_block || (!saved->rstd && rows > 0)) return PTOC_ERR_INVALID_ARG;
+    const ptoc_block_norm_saved& sv = *saved;
+    // an empty tensor may have no address in either form
+    if ((sv.block.data && sv.block_ckpt.codes) || (sv.stream.data && sv.stream_ckpt.codes)) return PTOC_ERR_INVALID_ARG;
     const int eb = elem_size(dtype);
     Operands o;
     NormBackParams p;
@@ -253,15 +255,14 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
     if (st != PTOC_OK) return st;
     if ((d_post_weight && !params->post_norm) || (d_gate && !params->gate)) return PTOC_ERR_INVALID_ARG;
     p.gate_kind = d_gate ? gate_kind(params) : kGateNone;
-    if (saved->block) {
-        if (!same_matrix(saved->block, d_block)) o.matrix(false, saved->block, rows, cols, eb);
-    } else {
-        o.ckpt(false, saved->block_ckpt, rows, cols);
+    if (rows > 0 && cols > 0) {
+        if (sv.block_ckpt.codes) o.ckpt(false, &sv.block_ckpt, rows, cols);
+        else if (!same_matrix(&sv.block, d_block)) o.matrix(false, &sv.block, rows, cols, eb);
+        if (sv.stream_ckpt.codes) o.ckpt(false, &sv.stream_ckpt, rows, cols);
+        else o.matrix(false, &sv.stream, rows, cols, eb);
     }
-    if (saved->stream) o.matrix(false, saved->stream, rows, cols, eb);
-    else o.ckpt(false, saved->stream_ckpt, rows, cols);
     if (rows > INT64_MAX / 16) return PTOC_ERR_INVALID_ARG;
-    o.floats(false, saved->rstd, 2 * rows);
+    o.floats(false, sv.rstd, 2 * rows);
     o.matrix(false, dy, rows, cols, eb);
     if (du && !same_matrix(du, d_residual)) o.matrix(false, du, rows, cols, eb);
     o.matrix(true, d_residual, rows, cols, eb);
@@ -295,11 +296,13 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
         return PTOC_OK;
     }
     p.c.vec = o.vec;
-    if (saved->block) p.block = saved->block->data, p.ld_block = saved->block->ld;
-    else p.block_ckpt = *saved->block_ckpt;
-    if (saved->stream) p.stream = saved->stream->data, p.ld_stream = saved->stream->ld;
-    else p.stream_ckpt = *saved->stream_ckpt;
-    p.rstd = saved->rstd;
+    p.block = sv.block.data;
+    p.ld_block = sv.block.ld;
+    p.block_ckpt = sv.block_ckpt;
+    p.stream = sv.stream.data;
+    p.ld_stream = sv.stream.ld;
+    p.stream_ckpt = sv.stream_ckpt;
+    p.rstd = sv.rstd;
     p.dy = dy->data;
     p.ld_dy = dy->ld;
     if (du) p.du = du->data, p.ld_du = du->ld;

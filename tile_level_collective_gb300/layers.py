@@ -19,8 +19,9 @@ Outputs and workspaces belong to the caller; nothing is allocated in a call.
     layer(normed, y, workspace=layer.workspace(64))
 """
 import ctypes
+import struct
 
-from . import (F32, _addr, _done, _group, _lib, _rows_cols_ld, _same_layout, _stream, _vp, _i64, _G, dtype_code)
+from . import OK, F16, F32, BF16, PtocError, _addr, _done, _group, _lib, _stream, _vp, _i64
 
 CKPT_BLOCK = 32
 NORM_MAX_COLS = 32768
@@ -45,8 +46,8 @@ class ptoc_block_norm_params(ctypes.Structure):
 
 
 class ptoc_block_norm_saved(ctypes.Structure):
-    _fields_ = [("block", ctypes.POINTER(ptoc_matrix)), ("block_ckpt", ctypes.POINTER(ptoc_ckpt8)),
-                ("stream", ctypes.POINTER(ptoc_matrix)), ("stream_ckpt", ctypes.POINTER(ptoc_ckpt8)), ("rstd", _vp)]
+    _fields_ = [("block", ptoc_matrix), ("stream", ptoc_matrix), ("block_ckpt", ptoc_ckpt8),
+                ("stream_ckpt", ptoc_ckpt8), ("rstd", _vp)]
 
 
 class ptoc_moe_params(ctypes.Structure):
@@ -55,15 +56,14 @@ class ptoc_moe_params(ctypes.Structure):
                 ("renormalize", _i32), ("scale", _f32)]
 
 
-_M, _K = ctypes.POINTER(ptoc_matrix), ctypes.POINTER(ptoc_ckpt8)
-_N, _S, _E = (ctypes.POINTER(t) for t in (ptoc_block_norm_params, ptoc_block_norm_saved, ptoc_moe_params))
-_lib.ptoc_checkpoint8.argtypes = [_M, _K, _i64, _i64, ctypes.c_int, _vp]
-_lib.ptoc_restore8.argtypes = [_K, _M, _i64, _i64, ctypes.c_int, _vp]
-_lib.ptoc_block_norm.argtypes = [_G, _i64, _M, _N, _M, _M, _M, _K, _K, _vp, _i64, _i64, ctypes.c_int, _vp]
-_lib.ptoc_block_norm_backward.argtypes = [_S, _N, _M, _M, _M, _M, _vp, _vp, _vp, _vp, _size_t, _i64, _i64,
-                                          ctypes.c_int, _vp]
+# Structure arguments are declared as addresses: the C-name calls below pass
+# structures by reference, the conveniences pass their packed bytes.
+_lib.ptoc_checkpoint8.argtypes = [_vp, _vp, _i64, _i64, ctypes.c_int, _vp]
+_lib.ptoc_restore8.argtypes = [_vp, _vp, _i64, _i64, ctypes.c_int, _vp]
+_lib.ptoc_block_norm.argtypes = [_vp, _i64] + [_vp] * 8 + [_i64, _i64, ctypes.c_int, _vp]
+_lib.ptoc_block_norm_backward.argtypes = [_vp] * 10 + [_size_t, _i64, _i64, ctypes.c_int, _vp]
 _lib.ptoc_block_norm_backward_workspace.argtypes = [_i64, _i64]
-_lib.ptoc_moe_few_tokens.argtypes = [_M, _E, _M, _vp, _vp, _vp, _size_t, _i64, _i64, _i64, ctypes.c_int, _vp]
+_lib.ptoc_moe_few_tokens.argtypes = [_vp] * 6 + [_size_t, _i64, _i64, _i64, ctypes.c_int, _vp]
 _lib.ptoc_moe_few_tokens_workspace.argtypes = [_i64, _i64, _i64, _i32, _i32]
 for _f in ("ptoc_checkpoint8", "ptoc_restore8", "ptoc_block_norm", "ptoc_block_norm_backward", "ptoc_moe_few_tokens"):
     getattr(_lib, _f).restype = ctypes.c_int
@@ -122,24 +122,79 @@ def ptoc_moe_few_tokens_workspace(tokens, hidden, inter, experts, top_k):
 
 
 # ---- shape-inferring conveniences over torch tensors -------------------------------
+# They run for every layer of every step, and a small call's kernel is shorter
+# than a careless check of its arguments: each tensor's layout is read once,
+# and the C structures are packed as bytes.
 
-def _matrix(t):
-    """A 2-D tensor as a ptoc_matrix. A single row may have any row stride."""
-    rows, cols, ld = _rows_cols_ld(t)
-    return ptoc_matrix(t.data_ptr(), max(ld, cols) if rows <= 1 else ld)
+_matrix_bytes = struct.Struct("Pq").pack
+_ckpt_bytes = struct.Struct("PqPq").pack
+_params_bytes = struct.Struct("iiPPPqqfff4x").pack
+_saved_bytes = struct.Struct("PqPqPqPqPqPqP").pack
+assert struct.calcsize("iiPPPqqfff4x") == ctypes.sizeof(ptoc_block_norm_params)
+_group_bytes = struct.Struct("Pii").pack
+_array_types = {}
+_codes = {}
+_raw_stream = None
 
 
-def _like(t, ref, what):
-    if tuple(t.shape) != tuple(ref.shape) or t.dtype != ref.dtype or t.device != ref.device:
+def _torch_names():
+    """Fill what depends on torch, which the package imports on first use."""
+    import torch
+    global _raw_stream, _float32, _int32, _int8, _uint8
+    _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
+    _float32, _int32, _int8, _uint8 = torch.float32, torch.int32, torch.int8, torch.uint8
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _code(dtype):
+    if not _codes:
+        _torch_names()
+    code = _codes.get(dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % dtype)
+    return code
+
+
+def _stream_of(stream, device):
+    """The given stream, or torch's current one on the tensors' device."""
+    if stream is None and device.type == "cuda":
+        return _raw_stream(device.index)
+    return _stream(stream)
+
+
+def _call(status, where):
+    if status != OK:
+        raise PtocError(status, where)
+    return status
+
+
+def _pitch(t, what):
+    """The row pitch of a 2-D tensor. A single row may have any row stride."""
+    if t.dim() != 2:
+        raise ValueError("%s: expected a 2-D tensor" % what)
+    ld, one = t.stride()
+    rows, cols = t.shape
+    if one != 1 and cols > 1:
+        raise ValueError("%s: rows must be contiguous (stride(1) == 1)" % what)
+    return ld if rows > 1 or ld > cols else cols
+
+
+def _like(t, shape, dtype, device, what):
+    """A matrix argument of the activations' kind, packed for C; None stays None."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError("%s: needs the shape, dtype and device of the activations" % what)
+    return _matrix_bytes(t.data_ptr(), _pitch(t, what))
 
 
 def _packed(t, shape, dtype, device, what):
+    """The address of a packed tensor argument; None stays None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s: expected a packed %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
-    return t
+    return t.data_ptr()
 
 
 def _workspace(nbytes, device):
@@ -154,84 +209,91 @@ class Checkpoint8:
     def __init__(self, rows, cols, device="cuda"):
         import torch
         blocks = (cols + CKPT_BLOCK - 1) // CKPT_BLOCK
-        self.cols = cols
-        self.codes = torch.empty(rows, blocks * CKPT_BLOCK, dtype=torch.int8, device=device)[:, :cols]
-        self.exps = torch.empty(rows, blocks, dtype=torch.uint8, device=device)
+        self._hold(torch.empty(rows, blocks * CKPT_BLOCK, dtype=torch.int8, device=device)[:, :cols],
+                   torch.empty(rows, blocks, dtype=torch.uint8, device=device))
 
     @classmethod
     def of(cls, codes, exps, cols=None):
         """A checkpoint over given codes [rows, cols] and exponent bytes."""
         import torch
-        k = cls.__new__(cls)
-        k.cols = codes.shape[1] if cols is None else cols
+        cols = codes.shape[-1] if cols is None else cols
         if codes.dtype != torch.int8 or exps.dtype != torch.uint8 or codes.device != exps.device:
             raise ValueError("checkpoint: expected int8 codes and uint8 exponents on one device")
-        if tuple(codes.shape) != (codes.shape[0], k.cols) or \
-                tuple(exps.shape) != (codes.shape[0], (k.cols + CKPT_BLOCK - 1) // CKPT_BLOCK):
+        if codes.dim() != 2 or codes.shape[1] != cols or \
+                tuple(exps.shape) != (codes.shape[0], (cols + CKPT_BLOCK - 1) // CKPT_BLOCK):
             raise ValueError("checkpoint: expected codes [rows, cols] and exponents [rows, ceil(cols / 32)]")
-        k.codes, k.exps = codes, exps
+        k = cls.__new__(cls)
+        k._hold(codes, exps)
         return k
 
-    @property
-    def shape(self):
-        return tuple(self.codes.shape)
-
-    def c(self):
-        m, e = _matrix(self.codes), _matrix(self.exps)
-        return ptoc_ckpt8(m.data, m.ld, e.data, e.ld)
+    def _hold(self, codes, exps):
+        self.codes, self.exps = codes, exps
+        self.shape, self.device = codes.shape, codes.device
+        self.c = (codes.data_ptr(), _pitch(codes, "codes"), exps.data_ptr(), _pitch(exps, "exps"))
 
 
-def _ckpt(k, ref, what):
+def _ckpt(k, shape, device, what):
     if k is None:
         return None
-    if k.shape != tuple(ref.shape) or k.codes.device != ref.device:
+    if k.shape != shape or k.device != device:
         raise ValueError("%s: the checkpoint needs the shape and device of the activations" % what)
-    return k.c()
+    return _ckpt_bytes(*k.c)
+
+
+def _ckpt_call(call, x, ckpt, stream, what):
+    shape, device = x.shape, x.device
+    m = _matrix_bytes(x.data_ptr(), _pitch(x, what))
+    k = _ckpt(ckpt, shape, device, what)
+    code = _code(x.dtype)
+    a, b = (m, k) if what == "checkpoint8" else (k, m)
+    return _call(call(a, b, shape[0], shape[1], code, _stream_of(stream, device)), "ptoc_" + what)
 
 
 def checkpoint8(x, ckpt, stream=None):
     """ckpt = x [rows, cols] in 8 bits."""
-    return ptoc_checkpoint8(_matrix(x), _ckpt(ckpt, x, "checkpoint8"), x.shape[0], x.shape[1], dtype_code(x),
-                            stream=stream)
+    return _ckpt_call(_lib.ptoc_checkpoint8, x, ckpt, stream, "checkpoint8")
 
 
 def restore8(ckpt, x, stream=None):
     """x [rows, cols] = the values that the checkpoint holds."""
-    return ptoc_restore8(_ckpt(ckpt, x, "restore8"), _matrix(x), x.shape[0], x.shape[1], dtype_code(x), stream=stream)
+    return _ckpt_call(_lib.ptoc_restore8, x, ckpt, stream, "restore8")
 
 
 def _gate_strides(gate, rows, cols):
     """Row and column stride of a gate that broadcasts to [rows, cols]: a
     scalar, [cols], [1, cols], [rows, 1] or [rows, cols]."""
-    if gate.dim() > 2:
+    d = gate.dim()
+    if d > 2:
         raise ValueError("gate: expected at most 2 dimensions")
-    shape = (1,) * (2 - gate.dim()) + tuple(gate.shape)
-    stride = (0,) * (2 - gate.dim()) + tuple(gate.stride())
-    if shape[0] not in (1, rows) or shape[1] not in (1, cols):
-        raise ValueError("gate: shape %s does not broadcast to [%d, %d]" % (tuple(gate.shape), rows, cols))
-    rs = stride[0] if shape[0] > 1 else 0
-    cs = stride[1] if shape[1] > 1 else 0
-    if shape[0] > 1 and rs < 1 or cs not in (0, 1) or shape[1] > 1 and cs != 1:
+    shape, stride = gate.shape, gate.stride()
+    across = shape[d - 1] if d > 0 else 1
+    down = shape[0] if d > 1 else 1
+    if down not in (1, rows) or across not in (1, cols):
+        raise ValueError("gate: shape %s does not broadcast to [%d, %d]" % (tuple(shape), rows, cols))
+    rs = stride[0] if down > 1 else 0
+    cs = stride[d - 1] if across > 1 else 0
+    if down > 1 and rs < 1 or across > 1 and cs != 1:
         raise ValueError("gate: needs packed columns and its own rows")
     return rs, cs
 
 
-def _norm_params(ref, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps):
-    import torch
-    rows, cols = ref.shape
-    given = [t for t in (post_weight if post_norm else None, pre_weight, gate) if t is not None]
-    kind = given[0].dtype if given else ref.dtype
-    for t in given:
-        if t.dtype != kind or kind not in (ref.dtype, torch.float32) or t.device != ref.device:
-            raise ValueError("block_norm: weights and gate need one dtype (the activations' or float32) and their device")
-    for t, what in ((post_weight, "post_weight"), (pre_weight, "pre_weight")):
-        _packed(t, (cols,), t.dtype if t is not None else None, ref.device, what)
+def _norm_params(shape, dtype, device, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps):
+    rows, cols = shape
     if post_weight is not None and not post_norm:
         raise ValueError("block_norm: post_weight without the norm after the block")
+    kind = None
+    for t in (post_weight, pre_weight, gate):
+        if t is not None:
+            if kind is None:
+                kind = t.dtype
+            if t.dtype != kind or (kind != dtype and kind != _float32) or t.device != device:
+                raise ValueError("block_norm: weights and gate need one dtype (the activations' or float32) and their "
+                                 "device")
     rs, cs = _gate_strides(gate, rows, cols) if gate is not None else (0, 0)
-    return ptoc_block_norm_params(int(bool(post_norm)), dtype_code(given[0]) if given else dtype_code(ref),
-                                  _addr(post_weight), _addr(pre_weight), _addr(gate), rs, cs, residual_scale,
-                                  branch_scale, eps)
+    return _params_bytes(1 if post_norm else 0, _codes[dtype if kind is None else kind],
+                         _packed(post_weight, (cols,), kind, device, "post_weight") or 0,
+                         _packed(pre_weight, (cols,), kind, device, "pre_weight") or 0,
+                         0 if gate is None else gate.data_ptr(), rs, cs, residual_scale, branch_scale, eps)
 
 
 def block_norm(parts, residual, out, normed=None, *, post_norm=True, post_weight=None, pre_weight=None, gate=None,
@@ -240,18 +302,31 @@ def block_norm(parts, residual, out, normed=None, *, post_norm=True, post_weight
     """out = residual_scale * residual + branch_scale * gate * norm(sum of parts);
     normed = norm(out) * pre_weight. ``out`` may be ``residual``. ``gate``
     broadcasts to the activations; ``rstd`` is float32 [2, rows]."""
-    import torch
-    rows, cols, ld = _same_layout(parts, "block_norm")
-    if rows <= 1:
-        ld = max(ld, cols)
-    for t, what in ((residual, "residual"), (out, "out"), (normed, "normed"), (block_out, "block_out")):
-        if t is not None:
-            _like(t, parts[0], what)
-    _packed(rstd, (2, rows), torch.float32, out.device, "rstd")
-    p = _norm_params(out, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
-    return ptoc_block_norm(parts, ld, _matrix(residual), p, _matrix(out), None if normed is None else _matrix(normed),
-                           None if block_out is None else _matrix(block_out), _ckpt(block_ckpt, out, "block_ckpt"),
-                           _ckpt(stream_ckpt, out, "stream_ckpt"), rstd, rows, cols, dtype_code(out), stream=stream)
+    n = len(parts)
+    if n == 0:
+        raise ValueError("block_norm: expected at least one part")
+    first = parts[0]
+    shape, dtype, device, strides = first.shape, first.dtype, first.device, first.stride()
+    code = _code(dtype)
+    ld = _pitch(first, "parts")
+    rows, cols = shape
+    pointers = []
+    for t in parts:
+        if t is not first and (t.shape != shape or t.stride() != strides or t.dtype != dtype or t.device != device):
+            raise ValueError("block_norm: every part needs the same shape, strides, dtype and device")
+        pointers.append(t.data_ptr())
+    kind = _array_types.get(n)
+    if kind is None:
+        kind = _array_types[n] = ctypes.c_void_p * n
+    group = kind(*pointers)
+    p = _norm_params(shape, dtype, device, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
+    st = _lib.ptoc_block_norm(
+        _group_bytes(ctypes.addressof(group), n, 0), ld, _like(residual, shape, dtype, device, "residual"), p,
+        _like(out, shape, dtype, device, "out"), _like(normed, shape, dtype, device, "normed"),
+        _like(block_out, shape, dtype, device, "block_out"), _ckpt(block_ckpt, shape, device, "block_ckpt"),
+        _ckpt(stream_ckpt, shape, device, "stream_ckpt"), _packed(rstd, (2, rows), _float32, device, "rstd"), rows,
+        cols, code, _stream_of(stream, device))
+    return _call(st, "ptoc_block_norm")
 
 
 def block_norm_backward_workspace(rows, cols, device="cuda"):
@@ -268,35 +343,31 @@ def block_norm_backward(block, saved_stream, rstd, d_normed, d_residual, d_block
     the gradient that reaches the stream from later layers. ``d_block`` is the
     gradient of every part. Weight and gate gradients are float32, the gate's
     in the gate's shape."""
-    import torch
-    ref = d_normed
-    rows, cols, _ = _rows_cols_ld(ref)
-    for t, what in ((d_residual, "d_residual"), (d_block, "d_block"), (d_stream, "d_stream")):
-        if t is not None:
-            _like(t, ref, what)
-    _packed(rstd, (2, rows), torch.float32, ref.device, "rstd")
-    for t, what in ((d_pre_weight, "d_pre_weight"), (d_post_weight, "d_post_weight")):
-        _packed(t, (cols,), torch.float32, ref.device, what)
-    if d_gate is not None:
-        if gate is None:
-            raise ValueError("block_norm_backward: d_gate without a gate")
-        _packed(d_gate, gate.shape, torch.float32, ref.device, "d_gate")
-    p = _norm_params(ref, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
-    s = ptoc_block_norm_saved()
-    keep = []
-    for t, what in ((block, "block"), (saved_stream, "stream")):
+    shape, dtype, device = d_normed.shape, d_normed.dtype, d_normed.device
+    code = _code(dtype)
+    dy = _like(d_normed, shape, dtype, device, "d_normed")
+    rows, cols = shape
+    if d_gate is not None and gate is None:
+        raise ValueError("block_norm_backward: d_gate without a gate")
+    p = _norm_params(shape, dtype, device, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
+    held = [(0, 0), (0, 0), (0, 0, 0, 0), (0, 0, 0, 0)]           # block, stream, their checkpoints
+    for i, (t, what) in enumerate(((block, "block"), (saved_stream, "stream"))):
         if isinstance(t, Checkpoint8):
-            keep.append(_ckpt(t, ref, what))
-            setattr(s, what + "_ckpt", ctypes.pointer(keep[-1]))
+            _ckpt(t, shape, device, what)
+            held[2 + i] = t.c
         else:
-            _like(t, ref, what)
-            keep.append(_matrix(t))
-            setattr(s, what, ctypes.pointer(keep[-1]))
-    s.rstd = rstd.data_ptr()
-    return ptoc_block_norm_backward(s, p, _matrix(d_normed), None if d_stream is None else _matrix(d_stream),
-                                    _matrix(d_residual), _matrix(d_block), d_pre_weight, d_post_weight, d_gate,
-                                    workspace, workspace.numel() * workspace.element_size(), rows, cols,
-                                    dtype_code(ref), stream=stream)
+            _like(t, shape, dtype, device, what)
+            held[i] = (t.data_ptr(), _pitch(t, what))
+    s = _saved_bytes(*held[0], *held[1], *held[2], *held[3],
+                     _packed(rstd, (2, rows), _float32, device, "rstd") or 0)
+    st = _lib.ptoc_block_norm_backward(
+        s, p, dy, _like(d_stream, shape, dtype, device, "d_stream"),
+        _like(d_residual, shape, dtype, device, "d_residual"), _like(d_block, shape, dtype, device, "d_block"),
+        _packed(d_pre_weight, (cols,), _float32, device, "d_pre_weight"),
+        _packed(d_post_weight, (cols,), _float32, device, "d_post_weight"),
+        _packed(d_gate, None if gate is None else gate.shape, _float32, device, "d_gate"), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), rows, cols, code, _stream_of(stream, device))
+    return _call(st, "ptoc_block_norm_backward")
 
 
 class MoeLayer:
@@ -307,42 +378,45 @@ class MoeLayer:
 
     def __init__(self, router, w_in, w_out, top_k, *, bias=None, first_expert=0, score="softmax", renormalize=True,
                  scale=1.0):
-        import torch
         if w_in.dim() != 3 or w_out.dim() != 3 or router.dim() != 2:
             raise ValueError("MoeLayer: expected router [experts, hidden], w_in [local, 2 * inter, hidden] and "
                              "w_out [local, hidden, inter]")
         local, hidden, inter = w_out.shape
-        device = w_in.device
-        _packed(w_in, (local, 2 * inter, hidden), w_in.dtype, device, "w_in")
-        _packed(w_out, (local, hidden, inter), w_in.dtype, device, "w_out")
-        if router.dtype not in (w_in.dtype, torch.float32):
+        dtype, device = w_in.dtype, w_in.device
+        self.code = _code(dtype)
+        _packed(w_in, (local, 2 * inter, hidden), dtype, device, "w_in")
+        _packed(w_out, (local, hidden, inter), dtype, device, "w_out")
+        if router.dtype not in (dtype, _float32):
             raise ValueError("MoeLayer: the router needs the experts' dtype or float32")
         _packed(router, (router.shape[0], hidden), router.dtype, device, "router")
-        _packed(bias, (router.shape[0],), torch.float32, device, "bias")
+        _packed(bias, (router.shape[0],), _float32, device, "bias")
         if score not in SCORES:
             raise ValueError("MoeLayer: score is one of %s" % sorted(SCORES))
         self.router, self.w_in, self.w_out, self.bias = router, w_in, w_out, bias
+        self.dtype, self.device = dtype, device
         self.hidden, self.inter, self.experts, self.top_k = hidden, inter, router.shape[0], top_k
-        self.params = ptoc_moe_params(_addr(router), _addr(bias), _addr(w_in), _addr(w_out), dtype_code(router),
+        self.params = ptoc_moe_params(_addr(router), _addr(bias), _addr(w_in), _addr(w_out), _code(router.dtype),
                                       self.experts, first_expert, local, top_k, SCORES[score], int(bool(renormalize)),
                                       scale)
 
     def workspace(self, tokens):
         """A workspace tensor for calls of up to `tokens` tokens."""
         n = ptoc_moe_few_tokens_workspace(tokens, self.hidden, self.inter, self.experts, self.top_k)
-        return _workspace(n, self.w_in.device)
+        return _workspace(n, self.device)
 
     def __call__(self, x, y, *, ids=None, weights=None, workspace, stream=None):
         """y [tokens, hidden] = the held experts' part of the layer's output
         for x; ids (int32) and weights (float32) [tokens, top_k] are optional
         outputs."""
-        import torch
-        tokens, hidden, _ = _rows_cols_ld(x)
-        if hidden != self.hidden or x.dtype != self.w_in.dtype or x.device != self.w_in.device:
-            raise ValueError("MoeLayer: x needs the weights' width, dtype and device")
-        _like(y, x, "y")
-        _packed(ids, (tokens, self.top_k), torch.int32, x.device, "ids")
-        _packed(weights, (tokens, self.top_k), torch.float32, x.device, "weights")
-        return ptoc_moe_few_tokens(_matrix(x), self.params, _matrix(y), ids, weights, workspace,
-                                   workspace.numel() * workspace.element_size(), tokens, hidden, self.inter,
-                                   dtype_code(x), stream=stream)
+        shape, dtype, device = x.shape, self.dtype, self.device
+        m = _like(x, shape, dtype, device, "x")
+        tokens, hidden = shape
+        if hidden != self.hidden:
+            raise ValueError("MoeLayer: x needs the weights' width")
+        choice = (tokens, self.top_k)
+        st = _lib.ptoc_moe_few_tokens(
+            m, ctypes.byref(self.params), _like(y, shape, dtype, device, "y"),
+            _packed(ids, choice, _int32, device, "ids"), _packed(weights, choice, _float32, device, "weights"),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), tokens, hidden, self.inter, self.code,
+            _stream_of(stream, device))
+        return _call(st, "ptoc_moe_few_tokens")
