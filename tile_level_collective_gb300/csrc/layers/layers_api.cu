@@ -32,7 +32,7 @@ struct Operands {
             ok = false;
             return;
         }
-        if (((uintptr_t)p | (uintptr_t)(ld * eb)) & (uintptr_t)(word - 1)) vec = false;
+        if (((uintptr_t)p | (uintptr_t)(rows > 1 ? ld * eb : 0)) & (uintptr_t)(word - 1)) vec = false;
         add(write, p, footprint(rows, cols, ld, eb));
     }
     void matrix(bool write, const ptoc_matrix* m, int64_t nrows, int64_t cols, int eb)
@@ -202,7 +202,7 @@ extern "C" ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts
     Span part_reads[kMaxRanks];
     for (int r = 0; r < parts->nranks; ++r) {
         if ((!parts->tensors[r] && fp > 0) || !aligned(parts->tensors[r], eb)) return PTOC_ERR_INVALID_ARG;
-        if (((uintptr_t)parts->tensors[r] | (uintptr_t)(ld_parts * eb)) & 15u) o.vec = false;
+        if (((uintptr_t)parts->tensors[r] | (uintptr_t)(rows > 1 ? ld_parts * eb : 0)) & 15u) o.vec = false;
         part_reads[r] = Span{parts->tensors[r], (uintptr_t)fp};
         p.part[r] = parts->tensors[r];
     }
@@ -349,9 +349,10 @@ extern "C" ptoc_status ptoc_moe_few_tokens(const ptoc_matrix* x, const ptoc_moe_
         return PTOC_ERR_UNSUPPORTED;
     const int eb = elem_size(dtype);
     Operands o;
-    o.matrix(true, y, tokens, hidden, eb);
+    o.rows(true, y->data, y->ld, tokens, hidden, eb, 1);
     o.matrix(false, x, tokens, hidden, eb);
-    o.rows(false, q.router, hidden, q.experts, hidden, elem_size(q.router_dtype), 1);
+    if ((hidden | inter) & 7) o.vec = false;
+    o.rows(false, q.router, hidden, q.experts, hidden, elem_size(q.router_dtype), 16);
     // 2 * inter * local_experts and hidden * local_experts are below 2^41
     o.rows(false, q.w_in, hidden, 2 * inter * q.local_experts, hidden, eb, 16);
     o.rows(false, q.w_out, inter, hidden * q.local_experts, inter, eb, 16);

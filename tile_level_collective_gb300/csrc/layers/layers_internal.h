@@ -87,5 +87,7 @@ struct MoeParams {
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k);
 cudaError_t launch_moe_few(const MoeParams& p, int dtype, cudaStream_t s);
+// The waits of the mixture-of-experts kernel that gave up since the last call.
+cudaError_t take_stage_faults_moe(uint32_t* count);
 
 }  // namespace ptoc

@@ -1,0 +1,88 @@
+// Pieces that both forms of the mixture-of-experts layer use.
+#pragma once
+
+#include "layers/layers_common.cuh"
+#include "layers/layers_internal.h"
+
+namespace ptoc {
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Floats in an order that unsigned comparison keeps, all above 1, which stands
+// for NaN; 0 is left for "not there" and "taken".
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    if (v != v) return 1u;
+    if (v == 0.0f) v = 0.0f;               // -0 ties with +0
+    const uint32_t u = __float_as_uint(v);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// One warp chooses for one token: top_k rounds of the largest key, lowest
+// index first among equals. Lane l holds experts l, 32 + l, ... in registers
+// (L of them). ids and weights are written by lane k for round k.
+template <int L>
+__device__ __forceinline__ void choose_experts(const MoeParams& m, const float* logits, int32_t* ids, float* weights)
+{
+    const int lane = threadIdx.x & 31, n = m.experts;
+    float v[L];
+    float top = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const int e = j * 32 + lane;
+        v[j] = e < n ? logits[e] : -INFINITY;
+        top = fmaxf(top, v[j]);
+    }
+    if (!m.sigmoid) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (j * 32 + lane < n) total += expf(v[j] - top);
+        total = warp_sum(total);
+    }
+    auto score = [&](float x) { return m.sigmoid ? 1.0f / (1.0f + expf(-x)) : expf(x - top) / total; };
+    uint32_t key[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const int e = j * 32 + lane;
+        float k = v[j];
+        if (e < n && (m.sigmoid || m.bias)) k = m.bias ? score(k) + m.bias[e] : score(k);
+        key[j] = e < n ? ordered(k) : 0u;
+    }
+    float sum = 0.0f, mine = 0.0f;
+    int id = 0;
+    for (int k = 0; k < m.top_k; ++k) {
+        uint32_t best = 0;
+        int at = INT32_MAX;
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (key[j] > best) best = key[j], at = j * 32 + lane;
+        const uint32_t high = __reduce_max_sync(0xffffffffu, best);
+        at = __reduce_min_sync(0xffffffffu, best == high ? at : INT32_MAX);
+#pragma unroll
+        for (int j = 0; j < L; ++j)
+            if (at == j * 32 + lane) key[j] = 0u;
+        const float w = score(logits[at]);
+        sum += w;
+        if (lane == k) mine = w, id = at;
+    }
+    if (lane < m.top_k) {
+        if (m.renormalize) mine /= sum;
+        ids[lane] = id;
+        weights[lane] = mine * m.scale;
+    }
+}
+
+cudaError_t launch_moe_plain(const MoeParams& m, int dtype, cudaStream_t s);
+size_t moe_plain_workspace(int64_t tokens, int64_t inter, int experts, int top_k);
+// The tensor-core form; false where its tensor maps do not apply.
+bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_t* e);
+size_t moe_tensor_workspace(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k);
+
+}  // namespace ptoc

@@ -1,12 +1,12 @@
-// A mixture-of-experts layer for a few tokens, in its plain form: router dot
-// products, the choice, the gated first product and the weighted second one,
-// one launch each, a warp per output row.
+// A mixture-of-experts layer for a few tokens, in its plain form, for rows
+// that the tensor-core form's copies cannot address: router dot products, the
+// choice, the gated first product and the weighted second one, one launch
+// each, a warp per output row.
 //
 // Bound by HBM: the chosen experts' 3 * inter * hidden weights are read once,
 // and nothing else is large. A warp streams one row (or a gate and an up row)
 // of weights and multiplies it with every token that chose the expert.
-#include "layers/layers_common.cuh"
-#include "layers/layers_internal.h"
+#include "layers/moe_common.cuh"
 
 namespace ptoc {
 
@@ -39,13 +39,6 @@ struct MoePlainParams {
     MoePlan w;
 };
 
-__device__ __forceinline__ float warp_sum(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
 template <class T>
 __device__ __forceinline__ float param_at(const void* p, bool f32, int64_t i)
 {
@@ -69,63 +62,18 @@ __global__ void __launch_bounds__(kBlock) moe_router_kernel(const MoePlainParams
     if (lane == 0) p.w.logits[dot] = sum;
 }
 
-// Floats in an order that unsigned comparison keeps; a NaN is the lowest.
-__device__ __forceinline__ uint32_t ordered(float v)
-{
-    if (v != v) return 0u;
-    if (v == 0.0f) v = 0.0f;               // -0 ties with +0
-    const uint32_t u = __float_as_uint(v);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
-// One warp per token: top_k rounds of the largest key, lowest index first
-// among equals, each below the previous one in (key, index) order.
+// One warp per token.
+template <int L>
 __global__ void __launch_bounds__(32) moe_choose_kernel(const MoePlainParams p)
 {
     pdl_enter();
-    const int t = blockIdx.x, lane = threadIdx.x, n = p.m.experts;
-    const float* logits = p.w.logits + (int64_t)t * n;
-    float top = -INFINITY, total = 0.0f;
-    if (!p.m.sigmoid) {
-        for (int e = lane; e < n; e += 32) top = fmaxf(top, logits[e]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        for (int e = lane; e < n; e += 32) total += expf(logits[e] - top);
-        total = warp_sum(total);
-    }
-    auto score = [&](int e) { return p.m.sigmoid ? 1.0f / (1.0f + expf(-logits[e])) : expf(logits[e] - top) / total; };
-    auto key = [&](int e) {
-        if (!p.m.sigmoid && !p.m.bias) return ordered(logits[e]);
-        return ordered(p.m.bias ? score(e) + p.m.bias[e] : score(e));
-    };
-    uint32_t last_key = 0xffffffffu;
-    int last = -1;
-    float sum = 0.0f, mine = 0.0f;
-    int id = 0;
-    for (int k = 0; k < p.m.top_k; ++k) {
-        uint32_t best = 0;
-        int at = INT32_MAX;
-        for (int e = lane; e < n; e += 32) {
-            const uint32_t u = key(e);
-            const bool left = u < last_key || (u == last_key && e > last);
-            if (left && (at == INT32_MAX || u > best)) best = u, at = e;
-        }
-        const uint32_t high = __reduce_max_sync(0xffffffffu, at == INT32_MAX ? 0u : best);
-        at = __reduce_min_sync(0xffffffffu, at != INT32_MAX && best == high ? at : INT32_MAX);
-        last_key = high;
-        last = at;
-        const float w = score(at);
-        sum += w;
-        if (lane == k) mine = w, id = at;
-    }
-    if (lane < p.m.top_k) {
-        if (p.m.renormalize) mine /= sum;
-        mine *= p.m.scale;
-        const int i = t * p.m.top_k + lane;
-        p.w.ids[i] = id;
-        p.w.weights[i] = mine;
-        if (p.m.ids) p.m.ids[i] = id;
-        if (p.m.weights) p.m.weights[i] = mine;
+    const int t = blockIdx.x, i = t * p.m.top_k + threadIdx.x;
+    int32_t* ids = p.w.ids + t * p.m.top_k;
+    choose_experts<L>(p.m, p.w.logits + (int64_t)t * p.m.experts, ids, p.w.weights + t * p.m.top_k);
+    __syncwarp();
+    if (threadIdx.x < p.m.top_k) {
+        if (p.m.ids) p.m.ids[i] = p.w.ids[i];
+        if (p.m.weights) p.m.weights[i] = p.w.weights[i];
     }
 }
 
@@ -209,7 +157,9 @@ cudaError_t launch_plain(const MoePlainParams& p, cudaStream_t s)
 {
     const int dots = p.m.tokens * p.m.experts;
     cudaError_t e = launch_kernel(moe_router_kernel<T>, dim3((dots + kWarps - 1) / kWarps), kBlock, 0, s, p);
-    if (e == cudaSuccess) e = launch_kernel(moe_choose_kernel, dim3(p.m.tokens), 32, 0, s, p);
+    if (e == cudaSuccess)
+        e = p.m.experts <= 128 ? launch_kernel(moe_choose_kernel<4>, dim3(p.m.tokens), 32, 0, s, p)
+                               : launch_kernel(moe_choose_kernel<32>, dim3(p.m.tokens), 32, 0, s, p);
     const dim3 in((unsigned)((p.m.inter + kWarps - 1) / kWarps), p.m.local);
     if (e == cudaSuccess) e = launch_kernel(moe_in_kernel<T>, in, kBlock, 0, s, p);
     const dim3 out((unsigned)((p.m.hidden + kWarps - 1) / kWarps));
@@ -219,19 +169,33 @@ cudaError_t launch_plain(const MoePlainParams& p, cudaStream_t s)
 
 }  // namespace
 
-size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k)
+size_t moe_plain_workspace(int64_t tokens, int64_t inter, int experts, int top_k)
 {
     size_t off[4];
     return plan_bytes(tokens, inter, experts, top_k, off);
 }
 
-cudaError_t launch_moe_few(const MoeParams& m, int dtype, cudaStream_t s)
+cudaError_t launch_moe_plain(const MoeParams& m, int dtype, cudaStream_t s)
 {
     size_t off[4];
     plan_bytes(m.tokens, m.inter, m.experts, m.top_k, off);
     MoePlainParams p{m, MoePlan{(float*)(m.ws + off[0]), (int32_t*)(m.ws + off[1]), (float*)(m.ws + off[2]),
                                 (float*)(m.ws + off[3])}};
     return dtype == PTOC_F16 ? launch_plain<__half>(p, s) : launch_plain<__nv_bfloat16>(p, s);
+}
+
+size_t moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k)
+{
+    const size_t a = moe_plain_workspace(tokens, inter, experts, top_k);
+    const size_t b = moe_tensor_workspace(tokens, hidden, inter, experts, top_k);
+    return a > b ? a : b;
+}
+
+cudaError_t launch_moe_few(const MoeParams& m, int dtype, cudaStream_t s)
+{
+    cudaError_t e = cudaSuccess;
+    if (m.vec && launch_moe_tensor(m, dtype, s, &e)) return e;
+    return launch_moe_plain(m, dtype, s);
 }
 
 }  // namespace ptoc

@@ -1,0 +1,657 @@
+// A mixture-of-experts layer for up to 64 tokens in one cooperative launch on
+// the tensor cores.
+//
+// Bound by HBM: the active experts' 3 * inter * hidden weights, read once.
+// The kernel is therefore one stream of weight tiles through shared memory
+// (tensor-map copies, a ring of stages deep enough to cover the latency of
+// HBM) into tcgen05.mma, whose 128 rows are rows of weights and whose N = 16
+// to 64 columns are all the call's tokens, padded to 16: an expert multiplies
+// every token, and the epilogue keeps those that chose it. The tensor cores
+// are nearly idle at any N; gathering tokens would save nothing that is short.
+//
+//   phase 0  logits in binary32 on the CUDA cores           | grid barrier
+//   routing  every block chooses for every token (the same bits everywhere)
+//   phase 1  tiles of 64 gate rows and the matching 64 up rows x hidden;
+//            epilogue: h[expert][token] = w * silu(gate) * up in the
+//            activations' type, zero for tokens that did not choose the
+//            expert                                         | grid barrier
+//   phase 2  tiles of 128 output columns x (inter of every active expert):
+//            the sum over experts stays in the accumulator
+//
+// Work is split evenly in units of one 64-deep stage: block c takes the
+// stages [c, c + 1) * total / blocks, in tile order, so that a tile may be
+// spread over several blocks. Those write binary32 partial tiles; the block
+// that arrives last (a counter per tile) adds them in the order of the blocks,
+// so the sum does not depend on who is last. Nobody waits for another block
+// but at the two grid barriers, and the weights of phase 2's first stages are
+// on their way before the second one.
+#include <cooperative_groups.h>
+
+#include "host/host_checks.h"
+#include "layers/moe_common.cuh"
+#include "reduce_forms.cuh"
+
+namespace ptoc {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kDepth = 64;                  // one stage: 64 elements (128 bytes, one swizzle row) of K
+constexpr int kTileRows = 128;
+constexpr int kTileBytes = kTileRows * kDepth * 2;
+constexpr int kThreads = 256;               // warp 0 copies, warp 1 multiplies, warps 4 to 7 drain
+constexpr int kEpilogue = 128;
+constexpr int kMaxStages = 12;
+constexpr int kRouterTokens = 8, kRouterExperts = 2;
+
+struct MoeTensorParams {
+    CUtensorMap w_in, w_out, x, h;
+    MoeParams m;
+    float* logits;                          // [tokens, experts]
+    char* act;                              // [active, N, inter] activations (the h map)
+    float* partial;                         // [2 * grid][tokens][128] binary32 partial tiles
+    uint32_t* arrived;                      // tiles of phase 1, then of phase 2
+    int64_t counters;
+    int64_t in_counters;                    // those of phase 1
+    uint64_t wait_ns;
+};
+
+// ---- shared memory ----------------------------------------------------------------
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_empty[2], drained;
+    uint32_t tmem;
+    int32_t active;                         // active local experts
+    int32_t fault;                          // a bounded wait gave up
+    int32_t last;                           // this block finishes the tile
+    int32_t ids[PTOC_MOE_MAX_TOKENS * PTOC_MOE_MAX_TOP_K];
+    float weights[PTOC_MOE_MAX_TOKENS * PTOC_MOE_MAX_TOP_K];
+    int16_t expert[PTOC_MOE_MAX_EXPERTS];   // the active local experts, ascending
+    float row_weight[PTOC_MOE_MAX_TOKENS];  // of the epilogue's expert; 0 where not chosen
+    int32_t chosen[PTOC_MOE_MAX_TOKENS];
+    union {
+        float up[16][64];                   // the epilogue's exchange of up rows
+        float dots[kThreads / 32][kRouterExperts * kRouterTokens];
+        uint32_t bits[PTOC_MOE_MAX_EXPERTS / 32];
+    };
+};
+
+constexpr size_t kSharedHead = (sizeof(Shared) + 1023) / 1024 * 1024;
+// bytes of dynamic shared memory: the head, the ring, and room to align it
+constexpr size_t shared_bytes(int stages, int n) { return kSharedHead + 1024 + (size_t)stages * (kTileBytes + n * kDepth * 2); }
+constexpr size_t kSharedMost = 227 * 1024;
+template <int N>
+constexpr int kRing = (int)((kSharedMost - kSharedHead - 1024) / (kTileBytes + N * kDepth * 2)) < kMaxStages
+                          ? (int)((kSharedMost - kSharedHead - 1024) / (kTileBytes + N * kDepth * 2))
+                          : kMaxStages;
+
+// ---- tensor-core and copy instructions ------------------------------------------------
+
+// A K-major operand of 128-byte rows in the 128-byte swizzle: groups of 8 rows
+// are 1024 bytes apart.
+__device__ __forceinline__ uint64_t operand(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+           (uint64_t)2 << 61;
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, uint32_t accumulate)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(kind), "r"(accumulate)
+                 : "memory");
+}
+
+// The barrier completes when every mma issued so far by this thread has.
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[16])
+{
+    uint32_t u[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+                   "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+}
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// A box of a 2-D tensor map at column x (a multiple of 64 elements) and row y.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpilogue) : "memory"); }
+
+// ---- the split of the work ----------------------------------------------------------
+
+// `total` stages, `depth` of them to a tile, over `blocks` blocks.
+struct Split {
+    uint32_t total, depth;
+    uint32_t blocks;                        // at most `total`: every one has work
+    __device__ Split(uint32_t tiles, uint32_t d, uint32_t grid)
+        : total(tiles * d), depth(d), blocks(tiles * d < grid ? tiles * d : grid) {}
+    __device__ uint32_t begin(uint32_t c) const { return c >= blocks ? total : (uint32_t)((uint64_t)c * total / blocks); }
+    // the block that holds stage x: the largest c with begin(c) <= x
+    __device__ uint32_t owner(uint32_t x) const { return (uint32_t)((((uint64_t)x + 1) * blocks - 1) / total); }
+};
+
+// A bounded wait on a barrier of this block; false once any wait gave up.
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, uint64_t bound_ns)
+{
+    if (stage_ready(smem_u32(bar), parity)) return true;
+    if (*(volatile int32_t*)&sh.fault) return false;
+    if (stage_wait(smem_u32(bar), parity, globaltimer_ns() + bound_ns, bound_ns)) return true;
+    if (atomicExch(&sh.fault, 1) == 0) atomicAdd(&g_stage_faults, 1u);
+    return false;
+}
+
+// The same wait by the epilogue's threads, which go on or stop together.
+__device__ __forceinline__ bool epilogue_wait(Shared& sh, uint64_t* bar, uint32_t parity, uint64_t bound_ns)
+{
+    uint32_t all;
+    asm volatile("{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.and.pred q, 1, %2, p; selp.u32 %0, 1, 0, q; }"
+                 : "=r"(all)
+                 : "r"((uint32_t)wait(sh, bar, parity, bound_ns)), "n"(kEpilogue)
+                 : "memory");
+    return all != 0;
+}
+
+// ---- phase 0 ----------------------------------------------------------------------
+
+template <class T>
+__device__ __forceinline__ void load_router8(const void* base, bool f32, int64_t i, float (&v)[8])
+{
+    if (f32) {
+        const float4 a = *(const float4*)((const float*)base + i), b = *(const float4*)((const float*)base + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        Raw8<T> r;
+        const uint4 a = *(const uint4*)((const T*)base + i);
+        r.w.w[0] = a.x, r.w.w[1] = a.y, r.w.w[2] = a.z, r.w.w[3] = a.w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = r.at(j);
+    }
+}
+
+// Dot products of kRouterExperts experts with kRouterTokens tokens per block
+// and turn; the warps share the row and their sums are added in order.
+template <class T>
+__device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& sh)
+{
+    const MoeParams& m = p.m;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int groups = (m.tokens + kRouterTokens - 1) / kRouterTokens;
+    const int units = (m.experts + kRouterExperts - 1) / kRouterExperts * groups;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int e0 = u / groups * kRouterExperts, t0 = u % groups * kRouterTokens;
+        float sum[kRouterExperts][kRouterTokens] = {};
+        for (int64_t i = threadIdx.x * 8; i < m.hidden; i += kThreads * 8) {
+            float r[kRouterExperts][8];
+#pragma unroll
+            for (int e = 0; e < kRouterExperts; ++e)
+                load_router8<T>(m.router, m.router_f32, (int64_t)min(e0 + e, m.experts - 1) * m.hidden + i, r[e]);
+#pragma unroll
+            for (int t = 0; t < kRouterTokens; ++t) {
+                if (t0 + t >= m.tokens) break;
+                float x[8];
+                load_router8<T>(m.x, false, (t0 + t) * m.ld_x + i, x);
+#pragma unroll
+                for (int e = 0; e < kRouterExperts; ++e)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) sum[e][t] += r[e][j] * x[j];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kRouterExperts; ++e)
+#pragma unroll
+            for (int t = 0; t < kRouterTokens; ++t) {
+                const float v = warp_sum(sum[e][t]);
+                if (lane == 0) sh.dots[warp][e * kRouterTokens + t] = v;
+            }
+        __syncthreads();
+        if (threadIdx.x < kRouterExperts * kRouterTokens) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) v += sh.dots[w][threadIdx.x];
+            const int e = e0 + threadIdx.x / kRouterTokens, t = t0 + threadIdx.x % kRouterTokens;
+            if (e < m.experts && t < m.tokens) p.logits[t * m.experts + e] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// The choice of every token, and the list of active local experts.
+__device__ __forceinline__ void route(const MoeTensorParams& p, Shared& sh)
+{
+    const MoeParams& m = p.m;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int t = warp; t < m.tokens; t += kThreads / 32) {
+        int32_t* ids = sh.ids + t * m.top_k;
+        float* w = sh.weights + t * m.top_k;
+        if (m.experts <= 128) choose_experts<4>(m, p.logits + t * m.experts, ids, w);
+        else choose_experts<32>(m, p.logits + t * m.experts, ids, w);
+    }
+    if (threadIdx.x < PTOC_MOE_MAX_EXPERTS / 32) sh.bits[threadIdx.x] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < m.tokens * m.top_k; i += kThreads) {
+        const int local = sh.ids[i] - m.first;
+        if (local >= 0 && local < m.local) atomicOr(&sh.bits[local >> 5], 1u << (local & 31));
+        if (blockIdx.x == 0) {
+            if (m.ids) m.ids[i] = sh.ids[i];
+            if (m.weights) m.weights[i] = sh.weights[i];
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t mine = sh.bits[lane];
+        int before = __popc(mine), all = before;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, all, o);
+            if (lane >= o) all += v;
+        }
+        before = all - before;
+        for (; mine; mine &= mine - 1) sh.expert[before++] = (int16_t)(lane * 32 + __ffs(mine) - 1);
+        if (lane == 31) sh.active = all;
+    }
+    __syncthreads();
+}
+
+// ---- the kernel -------------------------------------------------------------------
+
+template <class T, int N>
+__global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_constant__ MoeTensorParams p)
+{
+    extern __shared__ unsigned char raw[];
+    Shared& sh = *(Shared*)raw;
+    const uint32_t ring = (smem_u32(raw) + (uint32_t)kSharedHead + 1023u) & ~1023u;
+    constexpr uint32_t kStage = kTileBytes + N * kDepth * 2;
+    constexpr uint32_t kStages = kRing<N>;
+    constexpr uint32_t kTmem = 2 * N <= 32 ? 32 : 2 * N <= 64 ? 64 : 128;
+    // f32 accumulator, both operands T, both K-major, 128 x N
+    constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0u : 1u;
+    constexpr uint32_t kKind = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N >> 3) << 17 | (kTileRows >> 4) << 24;
+    const MoeParams& m = p.m;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const cg::grid_group grid = cg::this_grid();
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < kStages; ++s) bar_init(&sh.full[s], 1), bar_init(&sh.empty[s], 1);
+        for (int b = 0; b < 2; ++b) bar_init(&sh.acc_full[b], 1), bar_init(&sh.acc_empty[b], kEpilogue);
+        bar_init(&sh.drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        sh.fault = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                     "n"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < p.counters; i += (int64_t)gridDim.x * kThreads)
+        p.arrived[i] = 0;
+    router_logits<T>(p, sh);
+    grid.sync();
+    fence_after();
+    route(p, sh);
+
+    const uint32_t active = (uint32_t)sh.active;
+    const uint32_t in_depth = (uint32_t)((m.hidden + kDepth - 1) / kDepth);
+    const uint32_t out_depth = (uint32_t)((m.inter + kDepth - 1) / kDepth);
+    const uint32_t in_tiles = (uint32_t)((m.inter + 63) / 64);
+    const uint32_t out_tiles = (uint32_t)((m.hidden + kTileRows - 1) / kTileRows);
+    const Split in(active * in_tiles, in_depth, gridDim.x), out(out_tiles, active * out_depth, gridDim.x);
+    const uint32_t tmem = sh.tmem;
+
+    if (active == 0) {                      // nothing is held here: rows of zeros
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < m.tokens * m.hidden;
+             i += (int64_t)gridDim.x * kThreads)
+            ((T*)m.y)[i / m.hidden * m.ld_y + i % m.hidden] = from_f32<T>(0.0f);
+    }
+
+    // the roles' places in the ring and in the two accumulators, kept over both phases
+    uint32_t turn = 0, acc = 0;
+    for (int phase = 1; phase <= 2 && active > 0; ++phase) {
+        const Split& split = phase == 1 ? in : out;
+        const uint32_t first = split.begin(blockIdx.x), last = split.begin(blockIdx.x + 1);
+        // Copies of stage x: the weights' tile, then the tokens' rows of the same depth.
+        auto weights = [&](uint32_t x, uint32_t slot) {
+            const uint32_t tile = x / split.depth, d = x - tile * split.depth;
+            const uint32_t dst = ring + slot * kStage;
+            uint64_t* bar = &sh.full[slot];
+            bar_expect(bar, kStage);
+            if (phase == 1) {
+                const uint32_t a = tile / in_tiles, i0 = (tile - a * in_tiles) * 64;
+                const int row = (int)(sh.expert[a] * 2 * m.inter + i0);
+                copy_box(dst, &p.w_in, (int)d * kDepth, row, bar);
+                copy_box(dst + kTileBytes / 2, &p.w_in, (int)d * kDepth, row + (int)m.inter, bar);
+            } else {
+                const uint32_t a = d / out_depth, k = d - a * out_depth;
+                copy_box(dst, &p.w_out, (int)k * kDepth, (int)(sh.expert[a] * m.hidden) + (int)tile * kTileRows, bar);
+            }
+        };
+        auto tokens = [&](uint32_t x, uint32_t slot) {
+            const uint32_t d = x % split.depth;
+            const uint32_t dst = ring + slot * kStage + kTileBytes;
+            if (phase == 1) {
+                copy_box(dst, &p.x, (int)d * kDepth, 0, &sh.full[slot]);
+            } else {
+                const uint32_t a = d / out_depth, k = d - a * out_depth;
+                copy_box(dst, &p.h, (int)k * kDepth, (int)(a * N), &sh.full[slot]);
+            }
+        };
+        if (phase == 2) {
+            // the first weights do not wait for the other blocks
+            const uint32_t ahead = min(kStages, last - first);
+            uint32_t sent = 0;
+            if (warp == 0) {
+                if (lane == 0)
+                    for (; sent < ahead; ++sent) {
+                        const uint32_t u = turn + sent;
+                        if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
+                        weights(first + sent, u % kStages);
+                    }
+                __syncwarp();
+            }
+            grid.sync();
+            if (warp == 0 && lane == 0) {
+                asm volatile("fence.proxy.async;" ::: "memory");     // h was written with ordinary stores
+                for (uint32_t s = 0; s < sent; ++s) tokens(first + s, (turn + s) % kStages);
+                for (uint32_t x = first + sent; x < last; ++x) {
+                    const uint32_t u = turn + (x - first);
+                    if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
+                    weights(x, u % kStages);
+                    tokens(x, u % kStages);
+                }
+            }
+        } else if (warp == 0 && lane == 0) {
+            for (uint32_t x = first; x < last; ++x) {
+                const uint32_t u = turn + (x - first);
+                if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
+                weights(x, u % kStages);
+                tokens(x, u % kStages);
+            }
+        }
+
+        if (warp == 1 && lane == 0) {
+            uint32_t at = acc;
+            bool ok = true;
+            for (uint32_t x = first; x < last && ok;) {
+                // one segment: this block's stages of one tile
+                const uint32_t end = min(last, (x / split.depth + 1) * split.depth);
+                const uint32_t b = at & 1, d = tmem + b * N;
+                if (!wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns)) break;
+                fence_after();
+                for (const uint32_t from = x; x < end; ++x) {
+                    const uint32_t u = turn + (x - first), slot = u % kStages;
+                    ok = wait(sh, &sh.full[slot], u / kStages & 1, p.wait_ns);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t a = ring + slot * kStage;
+#pragma unroll
+                    for (int k = 0; k < kDepth / 16; ++k)
+                        mma(d, operand(a + k * 32), operand(a + kTileBytes + k * 32), kKind, x > from || k > 0);
+                    commit(&sh.empty[slot]);
+                }
+                if (ok) commit(&sh.acc_full[b]);
+                ++at;
+            }
+        }
+
+        if (warp >= 4) {
+            const int row = threadIdx.x - 128;                       // of the tile
+            uint32_t at = acc;
+            // One tile's sums of 16 tokens, complete, of this thread's row.
+            auto finish = [&](uint32_t tile, int n0, float (&v)[16]) {
+                if (phase == 1) {
+                    const uint32_t a = tile / in_tiles;
+                    const int64_t i = (tile - a * in_tiles) * 64 + (row & 63);
+                    if (row >= 64)
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) sh.up[n][row - 64] = v[n];
+                    epilogue_sync();
+                    if (row < 64 && i < m.inter)
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) {
+                            const int t = n0 + n;
+                            if (t >= m.tokens) break;
+                            // a token that did not choose the expert has h = 0, whatever the sums hold
+                            const float h = sh.chosen[t] ? sh.row_weight[t] * (v[n] / (1.0f + expf(-v[n]))) * sh.up[n][row]
+                                                         : 0.0f;
+                            ((T*)p.act)[((int64_t)a * N + t) * m.inter + i] = from_f32<T>(h);
+                        }
+                    epilogue_sync();
+                } else {
+                    const int64_t col = (int64_t)tile * kTileRows + row;
+                    if (col < m.hidden)
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (n0 + n < m.tokens) ((T*)m.y)[(n0 + n) * m.ld_y + col] = from_f32<T>(v[n]);
+                }
+            };
+            for (uint32_t x = first; x < last;) {
+                const uint32_t tile = x / split.depth, head = tile * split.depth;
+                const uint32_t end = min(last, head + split.depth);
+                const bool whole = x == head && end == head + split.depth;
+                const uint32_t b = at & 1;
+                if (phase == 1) {
+                    const int expert = m.first + sh.expert[tile / in_tiles];
+                    if (row < m.tokens) {
+                        int hit = 0;
+                        float w = 0.0f;
+                        for (int k = 0; k < m.top_k; ++k)
+                            if (sh.ids[row * m.top_k + k] == expert) hit = 1, w = sh.weights[row * m.top_k + k];
+                        sh.chosen[row] = hit;
+                        sh.row_weight[row] = w;
+                    }
+                }
+                if (!epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns)) break;
+                fence_after();
+                const uint32_t d = tmem + b * N + ((uint32_t)(warp & 3) << 21);
+                float* mine = p.partial + (2 * (int64_t)blockIdx.x + (x == head)) * m.tokens * kTileRows + row;
+#pragma unroll 1
+                for (int n0 = 0; n0 < N && n0 < m.tokens; n0 += 16) {
+                    float v[16];
+                    load_columns(d + n0, v);
+                    if (whole) finish(tile, n0, v);
+                    else
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (n0 + n < m.tokens) mine[(n0 + n) * kTileRows] = v[n];
+                }
+                fence_before();
+                bar_arrive(&sh.acc_empty[b]);
+                if (!whole) {
+                    const uint32_t c0 = split.owner(head), c1 = split.owner(head + split.depth - 1);
+                    __threadfence();
+                    epilogue_sync();
+                    if (row == 0) {
+                        uint32_t* counter = p.arrived + (phase == 1 ? 0 : p.in_counters) + tile;
+                        sh.last = atomicAdd(counter, 1u) == c1 - c0;
+                        __threadfence();
+                    }
+                    epilogue_sync();
+                    if (sh.last) {
+#pragma unroll 1
+                        for (int n0 = 0; n0 < N && n0 < m.tokens; n0 += 16) {
+                            float v[16] = {};
+                            for (uint32_t c = c0; c <= c1; ++c) {
+                                const float* part =
+                                    p.partial + (2 * (int64_t)c + (c == c0)) * m.tokens * kTileRows + n0 * kTileRows + row;
+#pragma unroll
+                                for (int n = 0; n < 16; ++n)
+                                    if (n0 + n < m.tokens) v[n] += __ldcg(part + n * kTileRows);
+                            }
+                            finish(tile, n0, v);
+                        }
+                    }
+                }
+                x = end;
+                ++at;
+            }
+            if (phase == 1) asm volatile("fence.proxy.async;" ::: "memory");   // h is read by tensor-map copies
+        }
+        __syncwarp();
+        // every role advances by the same stages and segments
+        turn += last - first;
+        if (last > first) acc += (last - 1) / split.depth - first / split.depth + 1;
+    }
+
+    __syncthreads();
+    if (sh.fault) {
+        // a wait gave up: let what is in flight land before the memory is given back
+        if (threadIdx.x < kStages) {
+            const uint64_t until = globaltimer_ns() + kStageWaitNs;
+            for (uint32_t q = 0; q < 2; ++q) stage_wait(smem_u32(&sh.full[threadIdx.x]), q, until, kStageWaitNs);
+        }
+        if (warp == 1 && lane == 0) {
+            commit(&sh.drained);
+            stage_wait(smem_u32(&sh.drained), 0, globaltimer_ns() + kStageWaitNs, kStageWaitNs);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmem) : "memory");
+    }
+}
+
+// ---- host side --------------------------------------------------------------------
+
+struct TensorPlan {
+    size_t logits, act, partial, arrived, bytes;
+    int64_t in_counters, counters;
+};
+
+constexpr int kGrid = 152;                  // one block per SM; the workspace is sized for it
+
+int padded_tokens(int64_t tokens) { return (int)((tokens + 15) / 16 * 16); }
+
+TensorPlan tensor_plan(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k)
+{
+    const int64_t most = tokens * top_k < experts ? tokens * top_k : experts;
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    TensorPlan t;
+    t.in_counters = most * ((inter + 63) / 64);
+    t.counters = t.in_counters + (hidden + kTileRows - 1) / kTileRows;
+    size_t at = 0;
+    t.logits = at, at += up((size_t)tokens * experts * 4);
+    t.act = at, at += up((size_t)most * padded_tokens(tokens) * inter * 2);
+    t.partial = at, at += up((size_t)2 * kGrid * tokens * kTileRows * 4);
+    t.arrived = at, at += up((size_t)t.counters * 4);
+    t.bytes = at;
+    return t;
+}
+
+bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f16)
+{
+    const TensorMapEncoder enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {kDepth, (cuuint32_t)box_rows};
+    const cuuint32_t steps[2] = {1, 1};
+    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+               const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class T, int N>
+cudaError_t launch(MoeTensorParams& p, cudaStream_t s)
+{
+    const size_t smem = shared_bytes(kRing<N>, N);
+    const void* kernel = (const void*)moe_tensor_kernel<T, N>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    void* args[] = {(void*)&p};
+    const int sms = sm_count();
+    return cudaLaunchCooperativeKernel(kernel, dim3((unsigned)(sms < kGrid ? sms : kGrid)), dim3(kThreads), args, smem,
+                                       s);
+}
+
+template <class T>
+cudaError_t launch_for(MoeTensorParams& p, cudaStream_t s)
+{
+    switch (padded_tokens(p.m.tokens)) {
+    case 16: return launch<T, 16>(p, s);
+    case 32: return launch<T, 32>(p, s);
+    case 48: return launch<T, 48>(p, s);
+    default: return launch<T, 64>(p, s);
+    }
+}
+
+}  // namespace
+
+size_t moe_tensor_workspace(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k)
+{
+    return tensor_plan(tokens, hidden, inter, experts, top_k).bytes;
+}
+
+bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_t* e)
+{
+    // tensor-map coordinates are int32
+    if ((int64_t)m.local * 2 * m.inter > INT32_MAX || (int64_t)m.local * m.hidden > INT32_MAX) return false;
+    const TensorPlan t = tensor_plan(m.tokens, m.hidden, m.inter, m.experts, m.top_k);
+    const int64_t in_tiles = (m.inter + 63) / 64, most = t.in_counters / in_tiles;
+    // and stages are counted in 32 bits
+    if (most * in_tiles * ((m.hidden + kDepth - 1) / kDepth) > INT32_MAX ||
+        (m.hidden + kTileRows - 1) / kTileRows * most * ((m.inter + kDepth - 1) / kDepth) > INT32_MAX)
+        return false;
+    const int n = padded_tokens(m.tokens);
+    const bool f16 = dtype == PTOC_F16;
+    MoeTensorParams p;
+    memset(&p, 0, sizeof(p));
+    p.m = m;
+    p.logits = (float*)(m.ws + t.logits);
+    p.act = m.ws + t.act;
+    p.partial = (float*)(m.ws + t.partial);
+    p.arrived = (uint32_t*)(m.ws + t.arrived);
+    p.counters = t.counters;
+    p.in_counters = t.in_counters;
+    p.wait_ns = copy_wait_ns();
+    if (!encode_rows(&p.w_in, m.w_in, m.local * 2 * m.inter, m.hidden, m.hidden, 64, f16) ||
+        !encode_rows(&p.w_out, m.w_out, m.local * m.hidden, m.inter, m.inter, kTileRows, f16) ||
+        !encode_rows(&p.x, m.x, m.tokens, m.hidden, m.tokens > 1 ? m.ld_x : m.hidden, n, f16) ||
+        !encode_rows(&p.h, p.act, most * n, m.inter, m.inter, n, f16))
+        return false;
+    *e = f16 ? launch_for<__half>(p, s) : launch_for<__nv_bfloat16>(p, s);
+    return true;
+}
+
+cudaError_t take_stage_faults_moe(uint32_t* count) { return take_stage_faults(count); }
+
+}  // namespace ptoc

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include "host/host_checks.h"
+#include "layers/layers_internal.h"
 #include "ptoc.h"
 #include "ptoc_internal.h"
 
@@ -842,7 +843,7 @@ extern "C" ptoc_status ptoc_wait_faults(uint32_t* count)
     if (!count) return PTOC_ERR_INVALID_ARG;
     uint32_t total = 0;
     cudaError_t (*const take[])(uint32_t*) = {take_stage_faults_f32, take_stage_faults_i32, take_stage_faults_f16,
-                                               take_stage_faults_bf16};
+                                               take_stage_faults_bf16, take_stage_faults_moe};
     for (auto f : take) {
         uint32_t v = 0;
         if (f(&v) != cudaSuccess) return PTOC_ERR_CUDA;
