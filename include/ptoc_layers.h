@@ -60,7 +60,9 @@ typedef struct {
     int64_t ld_exps;
 } ptoc_ckpt8;
 
-/* ptoc_checkpoint8 - x [rows, cols] -> out. x and out must not overlap. */
+/* ptoc_checkpoint8 - x [rows, cols] -> out. x and out must not overlap. Both
+ * calls take up to 2^31 - 1 pieces of 256 columns (rows * ceil(cols / 256)),
+ * else PTOC_ERR_UNSUPPORTED. */
 ptoc_status ptoc_checkpoint8(const ptoc_matrix* x, const ptoc_ckpt8* out, int64_t rows, int64_t cols,
                              ptoc_dtype dtype, cudaStream_t stream);
 

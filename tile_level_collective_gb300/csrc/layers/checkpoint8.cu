@@ -11,28 +11,43 @@ namespace ptoc {
 
 namespace {
 
-// Work unit u: 256 columns (one warp) of row u / units_per_row.
+constexpr int kUnits = 4;            // work units whose loads a warp issues together
+
+// Work unit u: 256 columns of row u / units_per_row, held by one warp. A block
+// takes kUnits * 8 neighbouring units, its warps in turn.
 template <class T, bool V, bool RESTORE>
 __global__ void __launch_bounds__(kBlock) ckpt8_kernel(const Ckpt8Params p)
 {
     pdl_enter();
-    const int64_t per_row = (p.cols + 255) / 256;
-    const int64_t unit = (int64_t)blockIdx.x * (kBlock / 32) + (threadIdx.x >> 5);
-    if (unit >= p.rows * per_row) return;
-    const int64_t row = unit / per_row;
-    const int64_t c = (unit - row * per_row) * 32 + (threadIdx.x & 31);
-    const uint32_t mask = chunk_mask<V>(c, p.cols);
+    const uint32_t per_row = (uint32_t)((p.cols + 255) / 256), units = (uint32_t)p.rows * per_row;
+    const uint32_t unit0 = blockIdx.x * (kUnits * kBlock / 32) + (threadIdx.x >> 5);
     const Ckpt k{p.ckpt.codes, p.ckpt.exps, p.ckpt.ld_codes, p.ckpt.ld_exps};
-    T* x = (T*)p.x + row * p.ld;
-    float v[8];
-    if constexpr (RESTORE) {
-        ckpt_load8<V>(k, row, c, mask, v);
-        store8<T, V>(x, c, mask, v);
-    } else {
-        const Raw8<T> r = load8<T, V>(x, c, mask);
+    int64_t row[kUnits], c[kUnits];
+    uint32_t mask[kUnits];
+    Raw8<T> raw[kUnits];
+    CkptRaw<V> codes[kUnits];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r.at(j);
-        ckpt_store8<V>(k, row, c, mask, v);
+    for (int q = 0; q < kUnits; ++q) {
+        const uint32_t unit = unit0 + q * (kBlock / 32);
+        const uint32_t r = unit / per_row;
+        row[q] = r;
+        c[q] = (int64_t)(unit - r * per_row) * 32 + (threadIdx.x & 31);
+        mask[q] = unit < units ? chunk_mask<V>(c[q], p.cols) : 0u;
+        if constexpr (RESTORE) codes[q] = ckpt_load8<V>(k, row[q], c[q], mask[q]);
+        else raw[q] = load8<T, V>((const T*)p.x + row[q] * p.ld, c[q], mask[q]);
+    }
+#pragma unroll
+    for (int q = 0; q < kUnits; ++q) {
+        if (unit0 + q * (kBlock / 32) >= units) break;         // the whole warp
+        float v[8];
+        if constexpr (RESTORE) {
+            ckpt_values<V>(codes[q], 1.0f, v);
+            store8<T, V>((T*)p.x + row[q] * p.ld, c[q], mask[q], v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = raw[q].at(j);
+            ckpt_store8<V>(k, row[q], c[q], mask[q], v);
+        }
     }
 }
 
@@ -40,7 +55,8 @@ template <class T, bool RESTORE>
 cudaError_t launch(const Ckpt8Params& p, cudaStream_t s)
 {
     const int64_t units = p.rows * ((p.cols + 255) / 256);
-    const dim3 grid((unsigned)((units + kBlock / 32 - 1) / (kBlock / 32)));
+    const int64_t per_block = kUnits * kBlock / 32;
+    const dim3 grid((unsigned)((units + per_block - 1) / per_block));
     return p.vec ? launch_kernel(ckpt8_kernel<T, true, RESTORE>, grid, kBlock, 0, s, p)
                  : launch_kernel(ckpt8_kernel<T, false, RESTORE>, grid, kBlock, 0, s, p);
 }

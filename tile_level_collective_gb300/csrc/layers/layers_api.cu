@@ -87,15 +87,15 @@ ptoc_status ckpt8_call(const ptoc_matrix* x, const ptoc_ckpt8* k, int64_t rows, 
     const ptoc_status al = o.disjoint();
     if (al != PTOC_OK) return al;
     if (rows == 0 || cols == 0) return PTOC_OK;
-    // 8 work units of 256 columns to a block of the launch
-    if (rows > ((int64_t)INT32_MAX * 8) / ((cols + 255) / 256)) return PTOC_ERR_UNSUPPORTED;
+    // work units of 256 columns are counted in 32 bits
+    if (rows > INT32_MAX / ((cols + 255) / 256)) return PTOC_ERR_UNSUPPORTED;
     Ckpt8Params p;
     p.x = x->data;
     p.ld = x->ld;
     p.ckpt = *k;
     p.rows = rows;
     p.cols = cols;
-    p.vec = o.vec;
+    p.vec = o.vec && cols % 8 == 0;
     return status_of(restore ? launch_restore8(p, dtype, stream) : launch_checkpoint8(p, dtype, stream));
 }
 
@@ -212,7 +212,7 @@ extern "C" ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts
     if (st != PTOC_OK) return st;
     if (cols > PTOC_NORM_MAX_COLS) return PTOC_ERR_UNSUPPORTED;
     if (rows == 0 || cols == 0) return PTOC_OK;
-    p.c.vec = o.vec;
+    p.c.vec = o.vec && cols % 8 == 0;
     p.nparts = parts->nranks;
     p.ld_part = ld_parts;
     p.x = x->data;
@@ -230,7 +230,7 @@ extern "C" ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts
 extern "C" size_t ptoc_block_norm_backward_workspace(int64_t rows, int64_t cols)
 {
     if (rows <= 0 || cols <= 0 || cols > PTOC_NORM_MAX_COLS) return 0;
-    return (size_t)norm_backward_grid(rows, cols) * (size_t)cols * kNormColumnSums * sizeof(float);
+    return (size_t)norm_backward_grid(rows, cols) * (2 * (size_t)cols + 1) * sizeof(float);
 }
 
 extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* saved,
@@ -295,7 +295,7 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
         if (gate_bytes && cudaMemsetAsync(d_gate, 0, gate_bytes, stream) != cudaSuccess) return PTOC_ERR_CUDA;
         return PTOC_OK;
     }
-    p.c.vec = o.vec;
+    p.c.vec = o.vec && cols % 8 == 0;
     p.block = sv.block.data;
     p.ld_block = sv.block.ld;
     p.block_ckpt = sv.block_ckpt;
@@ -313,6 +313,7 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
     p.d_pre = d_pre_weight;
     p.d_post = d_post_weight;
     p.d_gate = d_gate;
+    p.need_q = d_post_weight || p.gate_kind == kGateChannel;
     p.partial = (float*)workspace;
     p.grid = norm_backward_grid(rows, cols);
     return status_of(launch_block_norm_backward(p, dtype, stream));

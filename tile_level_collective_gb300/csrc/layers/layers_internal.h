@@ -54,17 +54,17 @@ struct NormBackParams {
     void *d_residual, *d_block;
     int64_t ld_dres, ld_dblk;
     float *d_pre, *d_post, *d_gate;      // may be null
-    float* partial;                      // [kinds, grid, cols] column sums of each block, in the workspace
+    float* partial;                      // the blocks' column sums: [2][grid, cols], then [grid] scalars
     int32_t gate_kind;                   // GateKind of d_gate
+    int32_t need_q;                      // the second column sum is asked for
     int32_t grid;
 };
 
 enum GateKind : int { kGateNone = 0, kGateScalar = 1, kGateChannel = 2, kGateToken = 3, kGateElement = 4 };
 
-// Blocks of the backward pass: each keeps column sums of its rows, so the
-// workspace holds this many partial rows for each kind of column sum.
+// Blocks of the backward pass: each leaves two partial rows of column sums
+// and a scalar in the workspace.
 int norm_backward_grid(int64_t rows, int64_t cols);
-constexpr int kNormColumnSums = 3;       // d_pre, d_post, d_gate
 
 cudaError_t launch_checkpoint8(const Ckpt8Params& p, int dtype, cudaStream_t s);
 cudaError_t launch_restore8(const Ckpt8Params& p, int dtype, cudaStream_t s);
