@@ -16,11 +16,6 @@ namespace ptoc {
 
 namespace {
 
-// What follows the sum of the parts, for one row in registers: a (the sum) and
-// x (raw) of C chunks. gw is the weight of the norm after the block times
-// branch_scale and the gate where that varies along the columns; `scale` is
-// the rest. wpre is the weight of the norm before the next block.
-
 template <class T>
 __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
 {
@@ -28,26 +23,29 @@ __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
     return k.param_f32 ? ((const float*)k.gate)[row * k.gate_rs] : to_f32(((const T*)k.gate)[row * k.gate_rs]);
 }
 
-// The columns' factor of the norm after the block.
-template <class T, bool V>
-__device__ __forceinline__ void column_factor(const NormCommon& k, int64_t row, int64_t c, uint32_t mask, float* gw)
+// The columns' factor of the norm after the block: its weight, times
+// branch_scale * gate where the gate varies along the columns.
+template <class T, int G>
+__device__ __forceinline__ F8 column_factor(const NormCommon& k, int64_t row, uint32_t col, uint32_t mask)
 {
-    load_param8<T, V>(k.post_weight, k.param_f32, c, mask, gw);
+    F8 w = load_param8<T, G>(k.post_weight, k.param_f32, col, mask);
     if (k.gate_cs) {
-        float g[8];
         const char* base = (const char*)k.gate + row * k.gate_rs * (k.param_f32 ? 4 : (int)sizeof(T));
-        load_param8<T, V>(base, k.param_f32, c, mask, g);
+        const F8 g = load_param8<T, G>(base, k.param_f32, col, mask);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) gw[j] *= k.branch_scale * g[j];
+        for (int j = 0; j < 4; ++j) w.p[j] = mul2(w.p[j], mul2(both(k.branch_scale), g.p[j]));
     }
+    return w;
 }
 
-// KEEP: the column factors are in gw and wpre for all rows; else they are
-// loaded for each row.
-template <class T, bool V, int C, bool KEEP>
-__device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, float (&a)[C][8], const Raw8<T> (&x)[C],
-                                           const uint32_t (&mask)[C], const float (&gw)[KEEP ? C : 1][8],
-                                           const float (&wpre)[KEEP ? C : 1][8], float (*slots)[32], int& turn)
+// What follows the sum of the parts, for one row in registers: a (the sum) and
+// x of C chunks. KEEP: the column factors are in gw and wpre for all rows;
+// else they are loaded for each row.
+template <class T, int G, int C, bool KEEP>
+__device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 (&a)[C], const Raw8<T, G> (&x)[C],
+                                           const uint32_t (&col)[C], const uint32_t (&mask)[C],
+                                           const F8 (&gw)[KEEP ? C : 1], const F8 (&wpre)[KEEP ? C : 1],
+                                           float (*slots)[32], int& turn)
 {
     const NormCommon& k = p.c;
     const Ckpt bc{p.block_ckpt.codes, p.block_ckpt.exps, p.block_ckpt.ld_codes, p.block_ckpt.ld_exps};
@@ -55,41 +53,43 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, flo
     const float row_gate = k.gate_cs ? 1.0f : k.branch_scale * gate_of_row<T>(k, row);
     float ra = 1.0f;
     if (k.post_norm) {
-        float sum[1] = {0.0f};
+        Pair sum = 0;
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum[0] += a[i][j] * a[i][j];
-        block_sum(sum, slots[turn]);
+            for (int j = 0; j < 4; ++j) sum = fma2(a[i].p[j], a[i].p[j], sum);
+        float total[1] = {sum_of(sum)};
+        block_sum(total, slots[turn]);
         turn ^= 1;
-        ra = 1.0f / sqrtf(sum[0] * k.inv_cols + k.eps);
+        ra = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     }
-    const float scale = ra * row_gate;
-    float sq[1] = {0.0f};
+    const Pair scale = both(ra * row_gate), keep = both(k.residual_scale);
+    Pair sq = 0;
+    Raw8<T, G> s[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-        if (p.block_out) store8<T, V>((T*)p.block_out + row * p.ld_block, c, mask[i], a[i]);
-        if (bc.codes) ckpt_store8<V>(bc, row, c, mask[i], a[i]);
-        float w[8];
-        if constexpr (!KEEP) column_factor<T, V>(k, row, c, mask[i], w);
+        if (p.block_out) store8<T, G>((T*)p.block_out + row * p.ld_block, col[i], mask[i], a[i]);
+        if (bc.codes) ckpt_store8<G>(bc, row, col[i], mask[i], a[i]);
+        F8 w;
+        if constexpr (!KEEP) w = column_factor<T, G>(k, row, col[i], mask[i]);
+        const F8 r = x[i].expand();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            a[i][j] = k.residual_scale * x[i].at(j) + a[i][j] * scale * (KEEP ? gw[KEEP ? i : 0][j] : w[j]);
-            sq[0] += a[i][j] * a[i][j];
+        for (int j = 0; j < 4; ++j) {
+            const Pair n = mul2(mul2(a[i].p[j], scale), KEEP ? gw[KEEP ? i : 0].p[j] : w.p[j]);
+            a[i].p[j] = fma2(keep, r.p[j], n);
+            sq = fma2(a[i].p[j], a[i].p[j], sq);
         }
-        store8<T, V>((T*)p.out + row * p.ld_out, c, mask[i], a[i]);
-        if (sc.codes) {
-            float v[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = to_f32(from_f32<T>(a[i][j]));
-            ckpt_store8<V>(sc, row, c, mask[i], v);
-        }
+        s[i] = round8<T, G>(a[i]);
+        store8<T, G>((T*)p.out + row * p.ld_out, col[i], mask[i], s[i]);
     }
+    if (sc.codes)
+#pragma unroll
+        for (int i = 0; i < C; ++i) ckpt_store8<G>(sc, row, col[i], mask[i], s[i].expand());
     if (!p.normed && !p.rstd) return;
-    block_sum(sq, slots[turn]);
+    float total[1] = {sum_of(sq)};
+    block_sum(total, slots[turn]);
     turn ^= 1;
-    const float r = 1.0f / sqrtf(sq[0] * k.inv_cols + k.eps);
+    const float r = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     if (p.rstd && threadIdx.x == 0) {
         p.rstd[row] = ra;
         p.rstd[k.rows + row] = r;
@@ -97,34 +97,33 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, flo
     if (!p.normed) return;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-        float w[8];
-        if constexpr (!KEEP) load_param8<T, V>(k.pre_weight, k.param_f32, c, mask[i], w);
+        F8 w;
+        if constexpr (!KEEP) w = load_param8<T, G>(k.pre_weight, k.param_f32, col[i], mask[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = a[i][j] * r * (KEEP ? wpre[KEEP ? i : 0][j] : w[j]);
-        store8<T, V>((T*)p.normed + row * p.ld_normed, c, mask[i], w);
+        for (int j = 0; j < 4; ++j) a[i].p[j] = mul2(mul2(a[i].p[j], both(r)), KEEP ? wpre[KEEP ? i : 0].p[j] : w.p[j]);
+        store8<T, G>((T*)p.normed + row * p.ld_normed, col[i], mask[i], a[i]);
     }
 }
 
-// Rows of 16-byte aligned words, through the threads' queues of K items.
-// COLUMNS: the column factors are kept in registers (they do not depend on
-// the row, and two chunks leave room for them).
+// Rows of 16-byte aligned words, through the threads' queues of K items. KEEP:
+// the column factors stay in registers (they do not depend on the row, and two
+// chunks leave room for them).
 template <class T, int C, int K, bool KEEP>
 __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(const NormParams p)
 {
+    constexpr int G = kVector<T>;
     pdl_enter();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float slots[2][32];
     int turn = 0;                           // block_sum's slots in turn
     const NormCommon& k = p.c;
-    Queue<C, (int)sizeof(T) / 2, K> queue(smem);
-    uint32_t mask[C];
-    float gw[KEEP ? C : 1][8], wpre[KEEP ? C : 1][8];
+    Queue<T, C, K> queue(smem);
+    uint32_t col[C], mask[C];
+    F8 gw[KEEP ? C : 1], wpre[KEEP ? C : 1];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-        mask[i] = chunk_mask<true>(c, k.cols);
-        if (!mask[i]) queue.clear(i);
+        col[i] = first_col<G>(i);
+        mask[i] = runs_below<G>(col[i], k.cols);
     }
     // the item to copy next: source `src` (nparts: the residual) of row `ahead`
     int64_t ahead = blockIdx.x;
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     auto push = [&] {
         if (ahead < k.rows) {
             const T* row = src < p.nparts ? (const T*)p.part[src] + ahead * p.ld_part : (const T*)p.x + ahead * p.ld_x;
-            queue.template copy_row<T>(row, mask);
+            queue.copy_row(row, col, mask);
             if (++src > p.nparts) src = 0, ahead += gridDim.x;
         }
         queue.next();
@@ -142,70 +141,78 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     if constexpr (KEEP)
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-            column_factor<T, true>(k, 0, c, mask[i], gw[i]);
-            load_param8<T, true>(k.pre_weight, k.param_f32, c, mask[i], wpre[i]);
+            gw[i] = column_factor<T, G>(k, 0, col[i], mask[i]);
+            wpre[i] = load_param8<T, G>(k.pre_weight, k.param_f32, col[i], mask[i]);
         }
     for (int64_t row = blockIdx.x; row < k.rows; row += gridDim.x) {
-        float a[C][8];
-        Raw8<T> x[C];
-        for (int r = 0; r < p.nparts; ++r) {
+        F8 a[C];
+        Raw8<T, G> x[C];
+        queue.wait();
+#pragma unroll
+        for (int i = 0; i < C; ++i) a[i] = queue.chunk(i).expand();
+        push();
+        for (int r = 1; r < p.nparts; ++r) {
             queue.wait();
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const Raw8<T> w = queue.template chunk<T>(i);
+                const F8 w = queue.chunk(i).expand();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) a[i][j] = r == 0 ? w.at(j) : __fadd_rn(a[i][j], w.at(j));
+                for (int j = 0; j < 4; ++j) a[i].p[j] = add2(a[i].p[j], w.p[j]);
             }
             push();
         }
         queue.wait();
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = queue.template chunk<T>(i);
+        for (int i = 0; i < C; ++i) x[i] = queue.chunk(i);
         push();
-        finish_row<T, true, C, KEEP>(p, row, a, x, mask, gw, wpre, slots, turn);
+        finish_row<T, G, C, KEEP>(p, row, a, x, col, mask, gw, wpre, slots, turn);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // Rows at any address: element-wide accesses, the next row's by other blocks.
 template <class T, int C>
-__global__ void __launch_bounds__(1024) block_norm_kernel(const NormParams p)
+__global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_kernel(const NormParams p)
 {
     pdl_enter();
     __shared__ float slots[2][32];
     int turn = 0;
     const NormCommon& k = p.c;
-    uint32_t mask[C];
+    uint32_t col[C], mask[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) mask[i] = chunk_mask<false>((int64_t)i * blockDim.x + threadIdx.x, k.cols);
+    for (int i = 0; i < C; ++i) {
+        col[i] = first_col<1>(i);
+        mask[i] = runs_below<1>(col[i], k.cols);
+    }
     for (int64_t row = blockIdx.x; row < k.rows; row += gridDim.x) {
-        float a[C][8];
-        Raw8<T> x[C];
+        F8 a[C];
+        Raw8<T, 1> x[C];
 #pragma unroll
-        for (int i = 0; i < C; ++i)
-            x[i] = load8<T, false>((const T*)p.x + row * p.ld_x, (int64_t)i * blockDim.x + threadIdx.x, mask[i]);
-        for (int r = 0; r < p.nparts; ++r) {
-            Raw8<T> w[C];
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-                w[i] = load8<T, false>((const T*)p.part[r] + row * p.ld_part, (int64_t)i * blockDim.x + threadIdx.x,
-                                       mask[i]);
-#pragma unroll
-            for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[i][j] = r == 0 ? w[i].at(j) : __fadd_rn(a[i][j], w[i].at(j));
+        for (int i = 0; i < C; ++i) {
+            x[i] = load8<T, 1>((const T*)p.x + row * p.ld_x, col[i], mask[i]);
+            a[i] = load8<T, 1>((const T*)p.part[0] + row * p.ld_part, col[i], mask[i]).expand();
         }
-        const float none[1][8] = {};
-        finish_row<T, false, C, false>(p, row, a, x, mask, none, none, slots, turn);
+        for (int r = 1; r < p.nparts; ++r) {
+            Raw8<T, 1> w[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) w[i] = load8<T, 1>((const T*)p.part[r] + row * p.ld_part, col[i], mask[i]);
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const F8 f = w[i].expand();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) a[i].p[j] = add2(a[i].p[j], f.p[j]);
+            }
+        }
+        const F8 none[1] = {};
+        finish_row<T, 1, C, false>(p, row, a, x, col, mask, none, none, slots, turn);
     }
 }
 
 template <class T, int C, int K>
 cudaError_t launch_queue(const NormParams& p, cudaStream_t s)
 {
-    const int64_t chunks = p.c.cols / 8;
-    const unsigned threads = (unsigned)((chunks + 32 * C - 1) / (32 * C)) * 32;
+    const int64_t groups = (p.c.cols + 255) / 256;           // warps' worth of chunks
+    const unsigned threads = (unsigned)((groups + C - 1) / C) * 32;
     const size_t smem = (size_t)K * threads * C * sizeof(T) * 8;
     // one wave: the registers and the queues of 512 threads of two chunks fill an SM
     const int64_t per_sm = C == 2 ? (512 / threads < 16 ? 512 / threads : 16) : 1;
@@ -227,10 +234,9 @@ cudaError_t launch(const NormParams& p, cudaStream_t s)
         if (p.c.cols <= 8192) return launch_queue<T, 2, kItems>(p, s);
         return launch_queue<T, 4, kItems / 4>(p, s);
     }
-    const int64_t groups = (p.c.cols + 255) / 256;           // warps' worth of chunks
+    const int64_t groups = (p.c.cols + 255) / 256;
     const dim3 grid((unsigned)(p.c.rows < INT32_MAX ? p.c.rows : INT32_MAX));
-    if (groups <= 32) return launch_kernel(block_norm_kernel<T, 1>, grid, (unsigned)groups * 32, 0, s, p);
-    if (groups <= 64) return launch_kernel(block_norm_kernel<T, 2>, grid, (unsigned)((groups + 1) / 2) * 32, 0, s, p);
+    if (groups <= 32) return launch_kernel(block_norm_kernel<T, 2>, grid, (unsigned)((groups + 1) / 2) * 32, 0, s, p);
     return launch_kernel(block_norm_kernel<T, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
 }
 

@@ -29,215 +29,239 @@ __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
     return k.param_f32 ? ((const float*)k.gate)[row * k.gate_rs] : to_f32(((const T*)k.gate)[row * k.gate_rs]);
 }
 
-template <class T, bool V>
-__device__ __forceinline__ void gate8(const NormCommon& k, int64_t row, int64_t c, uint32_t mask, float* g)
+template <class T, int G>
+__device__ __forceinline__ F8 gate8(const NormCommon& k, int64_t row, uint32_t col, uint32_t mask)
 {
-    load_param8<T, V>((const char*)k.gate + row * k.gate_rs * (k.param_f32 ? 4 : (int)sizeof(T)), k.param_f32, c, mask, g);
+    return load_param8<T, G>((const char*)k.gate + row * k.gate_rs * (k.param_f32 ? 4 : (int)sizeof(T)), k.param_f32,
+                             col, mask);
 }
 
 // Where the per-column parameters of chunk i come from: f32 copies that the
 // thread keeps in shared memory (KEEP), or memory.
-template <class T, bool V, bool KEEP>
+template <class T, int G, int C, bool KEEP>
 struct Columns {
     const NormCommon& k;
-    const float* kept;            // [2][C][2][threads] float4: wpre, then gw
-    __device__ __forceinline__ void pre(int i, int64_t c, uint32_t mask, float* w) const
+    const uint32_t (&col)[C];
+    const uint32_t (&mask)[C];
+    uint32_t kept;                          // [2][C][2][threads] 16-byte words: wpre, then the factor
+
+    __device__ __forceinline__ F8 pre(int i) const
     {
-        if constexpr (KEEP) read(2 * i, w);
-        else load_param8<T, V>(k.pre_weight, k.param_f32, c, mask, w);
+        if constexpr (KEEP) return read(2 * i);
+        return load_param8<T, G>(k.pre_weight, k.param_f32, col[i], mask[i]);
     }
     // the weight of the norm after the block, times branch_scale * gate for a gate of columns
-    __device__ __forceinline__ void factor(int i, int C, int64_t c, uint32_t mask, float* w) const
+    __device__ __forceinline__ F8 factor(int i) const
     {
-        if constexpr (KEEP) read(2 * (C + i), w);
-        else load_factor(c, mask, w);
+        if constexpr (KEEP) return read(2 * (C + i));
+        return load_factor(i);
     }
-    __device__ __forceinline__ void load_factor(int64_t c, uint32_t mask, float* w) const
+    __device__ __forceinline__ F8 load_factor(int i) const
     {
-        load_param8<T, V>(k.post_weight, k.param_f32, c, mask, w);
+        F8 w = load_param8<T, G>(k.post_weight, k.param_f32, col[i], mask[i]);
         if (k.gate_cs && !k.gate_rs) {
-            float g[8];
-            gate8<T, V>(k, 0, c, mask, g);
+            const F8 g = gate8<T, G>(k, 0, col[i], mask[i]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) w[j] *= k.branch_scale * g[j];
+            for (int j = 0; j < 4; ++j) w.p[j] = mul2(w.p[j], mul2(both(k.branch_scale), g.p[j]));
         }
+        return w;
     }
-    __device__ __forceinline__ void read(int slot, float* w) const
+    __device__ __forceinline__ uint32_t word(int n) const { return kept + (uint32_t)(n * 16) * blockDim.x; }
+    __device__ __forceinline__ F8 read(int n) const
     {
-        const float4* p = (const float4*)kept + (int64_t)slot * blockDim.x + threadIdx.x;
-        const float4 a = p[0], b = p[blockDim.x];
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        F8 f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(f.p[2 * h]), "=l"(f.p[2 * h + 1]) : "r"(word(n + h))
+                         : "memory");
+        return f;
     }
-    static __device__ __forceinline__ void keep(float* kept, int slot, const float* w)
+    __device__ __forceinline__ void keep(int n, const F8& f) const
     {
-        float4* p = (float4*)kept + (int64_t)slot * blockDim.x + threadIdx.x;
-        p[0] = make_float4(w[0], w[1], w[2], w[3]);
-        p[blockDim.x] = make_float4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(word(n + h)), "l"(f.p[2 * h]), "l"(f.p[2 * h + 1])
+                         : "memory");
     }
 };
 
-// One row. Loader gives, chunk by chunk and in this order: stream(i, factor),
-// dy(i), du(i) (if p.du), block(i, factor).
-template <class T, bool V, int C, bool KEEP, class Loader>
-__device__ __forceinline__ void back_row(const NormBackParams& p, int64_t row, Loader& in, const uint32_t (&mask)[C],
-                                         const Columns<T, V, KEEP>& cols, float (&sum_pre)[C][8], float (&sum_q)[C][8],
+// One row. The loader gives, chunk by chunk and in this order: the stream
+// times a factor, dy, du (if p.du), the block output times a factor.
+template <class T, int G, int C, bool KEEP, class Loader>
+__device__ __forceinline__ void back_row(const NormBackParams& p, int64_t row, Loader& in,
+                                         const Columns<T, G, C, KEEP>& cols, F8 (&sum_pre)[C], F8 (&sum_q)[C],
                                          float& sum_scalar, float (*slots)[32], int& turn)
 {
     const NormCommon& k = p.c;
+    const uint32_t (&col)[C] = cols.col;
+    const uint32_t (&mask)[C] = cols.mask;
     const float ra = k.post_norm ? p.rstd[row] : 1.0f, r = p.rstd[k.rows + row];
     const bool by_column = k.gate_cs != 0, by_element = by_column && k.gate_rs != 0;
     const float g_row = by_column ? 1.0f : gate_of_row<T>(k, row);
-    float st[C][8], up[C][8];
-    float dot[1] = {0.0f};
+    F8 st[C], up[C];
+    Pair dot = 0;
     in.begin_stream();
 #pragma unroll
-    for (int i = 0; i < C; ++i) in.stream(i, r, st[i]);
+    for (int i = 0; i < C; ++i) st[i] = in.stream(i, r);
     in.end();
-    in.begin();
+    in.begin_matrix(p.dy, p.ld_dy);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const Raw8<T> dy = in.matrix(i, p.dy, p.ld_dy);
-        float w[8];
-        cols.pre(i, (int64_t)i * blockDim.x + threadIdx.x, mask[i], w);
+        const F8 dy = in.matrix(i).expand(), w = cols.pre(i);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            up[i][j] = w[j] * dy.at(j);
-            sum_pre[i][j] += dy.at(j) * st[i][j];
-            dot[0] += up[i][j] * st[i][j];
+        for (int j = 0; j < 4; ++j) {
+            up[i].p[j] = mul2(w.p[j], dy.p[j]);
+            sum_pre[i].p[j] = fma2(dy.p[j], st[i].p[j], sum_pre[i].p[j]);
+            dot = fma2(up[i].p[j], st[i].p[j], dot);
         }
     }
     in.end();
-    block_sum(dot, slots[turn]);
+    float total[1] = {sum_of(dot)};
+    block_sum(total, slots[turn]);
     turn ^= 1;
-    const float m = dot[0] * k.inv_cols;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) up[i][j] = r * (up[i][j] - m * st[i][j]);
+    // up becomes ds
+    const Pair m = both(-total[0] * k.inv_cols), r2 = both(r);
     if (p.du) {
-        in.begin();
+        in.begin_matrix(p.du, p.ld_du);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const Raw8<T> du = in.matrix(i, p.du, p.ld_du);
+            const F8 du = in.matrix(i).expand();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) up[i][j] += du.at(j);
+            for (int j = 0; j < 4; ++j) up[i].p[j] = fma2(r2, fma2(m, st[i].p[j], up[i].p[j]), du.p[j]);
         }
         in.end();
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) up[i].p[j] = mul2(r2, fma2(m, st[i].p[j], up[i].p[j]));
     }
-    // up holds ds; st becomes ah
+    // st becomes ah
     in.begin_block();
 #pragma unroll
-    for (int i = 0; i < C; ++i) in.block(i, ra, st[i]);
+    for (int i = 0; i < C; ++i) st[i] = in.block(i, ra);
     in.end();
-    const float q_row = by_column ? 1.0f : (k.gate_rs ? g_row : 1.0f);       // a gate that varies by row goes into Q
-    float dots[1] = {0.0f};
+    const bool q_scaled = !by_column && k.gate_rs;       // a gate that varies by row goes into Q
+    dot = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-        float w[8];
+        F8 w;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = k.residual_scale * up[i][j];
-        store8<T, V>((T*)p.d_residual + row * p.ld_dres, c, mask[i], w);
-        cols.factor(i, C, c, mask[i], w);
+        for (int j = 0; j < 4; ++j) w.p[j] = mul2(both(k.residual_scale), up[i].p[j]);
+        store8<T, G>((T*)p.d_residual + row * p.ld_dres, col[i], mask[i], w);
+        w = cols.factor(i);
         if (by_element) {
-            float g[8];
-            gate8<T, V>(k, row, c, mask[i], g);
-            if (p.gate_kind == kGateElement)
+            const F8 g = gate8<T, G>(k, row, col[i], mask[i]);
+            if (p.gate_kind == kGateElement) {
+                F8 d;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (mask[i] >> j & 1)
-                        p.d_gate[row * k.cols + col_of<V>(c, j)] = k.branch_scale * (up[i][j] * (st[i][j] * w[j]));
+                for (int j = 0; j < 4; ++j)
+                    d.p[j] = mul2(both(k.branch_scale), mul2(up[i].p[j], mul2(st[i].p[j], w.p[j])));
+                // packed rows of floats, whose alignment follows the number of columns
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                sum_q[i][j] += g[j] * up[i][j] * st[i][j];
-                w[j] *= k.branch_scale * g[j];
+                for (int j = 0; j < 8; ++j) {
+                    float v[2];
+                    split(d.p[j / 2], v[0], v[1]);
+                    if (mask[i] >> (j / G) & 1) p.d_gate[row * k.cols + col[i] + j / G * 32 * G + j % G] = v[j & 1];
+                }
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum_q[i].p[j] = fma2(mul2(g.p[j], up[i].p[j]), st[i].p[j], sum_q[i].p[j]);
+                w.p[j] = mul2(w.p[j], mul2(both(k.branch_scale), g.p[j]));
+            }
+        } else if (q_scaled) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum_q[i].p[j] = fma2(mul2(both(g_row), up[i].p[j]), st[i].p[j], sum_q[i].p[j]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum_q[i][j] += q_row * up[i][j] * st[i][j];
+            for (int j = 0; j < 4; ++j) sum_q[i].p[j] = fma2(up[i].p[j], st[i].p[j], sum_q[i].p[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            up[i][j] *= w[j];
-            dots[0] += up[i][j] * st[i][j];
+        for (int j = 0; j < 4; ++j) {
+            up[i].p[j] = mul2(up[i].p[j], w.p[j]);
+            dot = fma2(up[i].p[j], st[i].p[j], dot);
         }
     }
+    total[0] = sum_of(dot);
     const bool row_gate = p.gate_kind == kGateToken || p.gate_kind == kGateScalar;
     if (k.post_norm || row_gate) {
-        block_sum(dots, slots[turn]);
+        block_sum(total, slots[turn]);
         turn ^= 1;
     }
     if (row_gate) {
-        const float d = k.branch_scale * dots[0];
+        const float d = k.branch_scale * total[0];
         if (p.gate_kind == kGateToken && threadIdx.x == 0) p.d_gate[row] = d;
         sum_scalar += d;
     }
-    const float m2 = k.post_norm ? dots[0] * k.inv_cols : 0.0f;
-    const float f = ra * (by_column ? 1.0f : k.branch_scale * g_row);
+    const Pair m2 = both(k.post_norm ? -total[0] * k.inv_cols : 0.0f);
+    const Pair f = both(ra * (by_column ? 1.0f : k.branch_scale * g_row));
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = f * (up[i][j] - m2 * st[i][j]);
-        store8<T, V>((T*)p.d_block + row * p.ld_dblk, (int64_t)i * blockDim.x + threadIdx.x, mask[i], v);
+        for (int j = 0; j < 4; ++j) up[i].p[j] = mul2(f, fma2(m2, st[i].p[j], up[i].p[j]));
+        store8<T, G>((T*)p.d_block + row * p.ld_dblk, col[i], mask[i], up[i]);
     }
 }
 
 // This block's partial rows of the column sums.
-template <bool V, int C>
-__device__ __forceinline__ void store_sums(const NormBackParams& p, const uint32_t (&mask)[C],
-                                           const float (&sum_pre)[C][8], const float (&sum_q)[C][8], float sum_scalar)
+template <int G, int C>
+__device__ __forceinline__ void store_sums(const NormBackParams& p, const uint32_t (&col)[C], const uint32_t (&mask)[C],
+                                           const F8 (&sum_pre)[C], const F8 (&sum_q)[C], float sum_scalar)
 {
     const int64_t cols = p.c.cols, plane = (int64_t)gridDim.x * cols;
     float* mine = p.partial + (int64_t)blockIdx.x * cols;
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-        if (p.d_pre) store8<float, V>(mine, c, mask[i], sum_pre[i]);
-        if (p.need_q) store8<float, V>(mine + plane, c, mask[i], sum_q[i]);
-    }
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float a[2], b[2];
+            split(sum_pre[i].p[j / 2], a[0], a[1]);
+            split(sum_q[i].p[j / 2], b[0], b[1]);
+            if (mask[i] >> (j / G) & 1) {
+                float* at = mine + col[i] + j / G * 32 * G + j % G;
+                if (p.d_pre) at[0] = a[j & 1];
+                if (p.need_q) at[plane] = b[j & 1];
+            }
+        }
     if (p.gate_kind == kGateScalar && threadIdx.x == 0) p.partial[2 * plane + blockIdx.x] = sum_scalar;
 }
 
 // Chunks from the thread's queue, in the order of the items: stream, dy, du, block.
 template <class T, int C, int K>
 struct QueueLoader {
+    static constexpr int G = kVector<T>;
     const NormBackParams& p;
-    Queue<C, (int)sizeof(T) / 2, K> queue;
+    Queue<T, C, K> queue;
+    const uint32_t (&col)[C];
     const uint32_t (&mask)[C];
     int64_t ahead;                          // the row of the item to copy next
     int item;
-    uint32_t s_exp[C], a_exp[C], s_next[C], a_next[C];   // exponent bytes of this row and the next
+    static constexpr int kRuns = 8 / G;
+    uint32_t s_exp[C * kRuns], a_exp[C * kRuns], s_next[C * kRuns], a_next[C * kRuns];   // exponent bytes of this row and the next
 
-    __device__ __forceinline__ QueueLoader(const NormBackParams& q, void* smem, const uint32_t (&m)[C])
-        : p(q), queue(smem), mask(m), ahead(blockIdx.x), item(0)
+    __device__ __forceinline__ QueueLoader(const NormBackParams& q, void* smem, const uint32_t (&c)[C],
+                                           const uint32_t (&m)[C])
+        : p(q), queue(smem), col(c), mask(m), ahead(blockIdx.x), item(0)
     {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            if (!mask[i]) queue.clear(i);
 #pragma unroll 1
         for (int k = 0; k < K; ++k) push();
         exponents(blockIdx.x);
-    }
-    __device__ __forceinline__ void codes(const ptoc_ckpt8& k)
-    {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-            queue.copy8(i, k.codes + ahead * k.ld_codes + ((int64_t)i * blockDim.x + threadIdx.x) * 8, mask[i] != 0);
     }
     __device__ __forceinline__ void push()
     {
         if (ahead < p.c.rows) {
             if (item == 0) {
-                if (p.stream) queue.template copy_row<T>((const T*)p.stream + ahead * p.ld_stream, mask);
-                else codes(p.stream_ckpt);
+                if (p.stream) queue.copy_row((const T*)p.stream + ahead * p.ld_stream, col, mask);
+                else queue.copy_codes(p.stream_ckpt.codes + ahead * p.stream_ckpt.ld_codes, col, mask);
             } else if (item == 1) {
-                queue.template copy_row<T>((const T*)p.dy + ahead * p.ld_dy, mask);
+                queue.copy_row((const T*)p.dy + ahead * p.ld_dy, col, mask);
             } else if (item == 2) {
-                queue.template copy_row<T>((const T*)p.du + ahead * p.ld_du, mask);
+                queue.copy_row((const T*)p.du + ahead * p.ld_du, col, mask);
             } else {
-                if (p.block) queue.template copy_row<T>((const T*)p.block + ahead * p.ld_block, mask);
-                else codes(p.block_ckpt);
+                if (p.block) queue.copy_row((const T*)p.block + ahead * p.ld_block, col, mask);
+                else queue.copy_codes(p.block_ckpt.codes + ahead * p.block_ckpt.ld_codes, col, mask);
             }
             item += item == 1 && !p.du ? 2 : 1;
             if (item == 4) item = 0, ahead += gridDim.x;
@@ -248,42 +272,45 @@ struct QueueLoader {
     __device__ __forceinline__ void exponents(int64_t row)
     {
         const bool in = row < p.c.rows;
+        const uint8_t* s = p.stream ? nullptr : p.stream_ckpt.exps + row * p.stream_ckpt.ld_exps;
+        const uint8_t* a = p.block ? nullptr : p.block_ckpt.exps + row * p.block_ckpt.ld_exps;
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int64_t b = ((int64_t)i * blockDim.x + threadIdx.x) >> 2;
-            s_next[i] = a_next[i] = 0;
-            if (!p.stream) s_next[i] = load1_if(p.stream_ckpt.exps + row * p.stream_ckpt.ld_exps + b, in && mask[i]);
-            if (!p.block) a_next[i] = load1_if(p.block_ckpt.exps + row * p.block_ckpt.ld_exps + b, in && mask[i]);
-        }
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int q = 0; q < kRuns; ++q) {
+                const bool on = in && (mask[i] >> q & 1);
+                const uint32_t b = (col[i] + q * 32 * G) >> 5;
+                s_next[i * kRuns + q] = s && on ? s[b] : 0u;
+                a_next[i * kRuns + q] = a && on ? a[b] : 0u;
+            }
     }
     __device__ __forceinline__ void row(int64_t r)
     {
 #pragma unroll
-        for (int i = 0; i < C; ++i) s_exp[i] = s_next[i], a_exp[i] = a_next[i];
+        for (int i = 0; i < C * kRuns; ++i) s_exp[i] = s_next[i], a_exp[i] = a_next[i];
         exponents(r + gridDim.x);
     }
-    __device__ __forceinline__ void begin() { queue.wait(); }
     __device__ __forceinline__ void begin_stream() { queue.wait(); }
     __device__ __forceinline__ void begin_block() { queue.wait(); }
+    __device__ __forceinline__ void begin_matrix(const void*, int64_t) { queue.wait(); }
     __device__ __forceinline__ void end() { push(); }
-    __device__ __forceinline__ Raw8<T> matrix(int i, const void*, int64_t) const { return queue.template chunk<T>(i); }
-    __device__ __forceinline__ void saved(int i, bool whole, uint32_t byte, float factor, float* v) const
+    __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i); }
+    __device__ __forceinline__ F8 saved(int i, bool whole, const uint32_t* bytes, float factor) const
     {
         if (whole) {
-            const Raw8<T> w = queue.template chunk<T>(i);
+            F8 f = queue.chunk(i).expand();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = w.at(j) * factor;
-        } else {
-            const Words<4> w = queue.read(i, 0);
-            CkptRaw<true> k;
-            k.w[0] = w.w[0];
-            k.w[1] = w.w[1];
-            k.byte = byte;
-            ckpt_values<true>(k, factor, v);
+            for (int j = 0; j < 4; ++j) f.p[j] = mul2(f.p[j], both(factor));
+            return f;
         }
+        CkptRaw<G> k;
+        queue.codes(i, k.w);
+#pragma unroll
+        for (int q = 0; q < kRuns; ++q) k.byte[q] = bytes[i * kRuns + q];
+        return ckpt_values<G>(k, factor);
     }
-    __device__ __forceinline__ void stream(int i, float f, float* v) const { saved(i, p.stream, s_exp[i], f, v); }
-    __device__ __forceinline__ void block(int i, float f, float* v) const { saved(i, p.block, a_exp[i], f, v); }
+    __device__ __forceinline__ F8 stream(int i, float f) const { return saved(i, p.stream, s_exp, f); }
+    __device__ __forceinline__ F8 block(int i, float f) const { return saved(i, p.block, a_exp, f); }
 };
 
 constexpr int kQueueThreads = 512;
@@ -291,94 +318,94 @@ constexpr int kQueueThreads = 512;
 template <class T, int K>
 __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(const NormBackParams p)
 {
-    constexpr int C = 2;
+    constexpr int C = 2, G = kVector<T>;
     pdl_enter();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ float slots[2][32];
     int turn = 0;                           // block_sum's slots in turn
-    uint32_t mask[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) mask[i] = chunk_mask<true>((int64_t)i * blockDim.x + threadIdx.x, p.c.cols);
-    float* kept = (float*)smem;
-    QueueLoader<T, C, K> in(p, smem + (size_t)blockDim.x * C * 2 * 32, mask);
-    const Columns<T, true, false> memory{p.c, nullptr};
-    const Columns<T, true, true> cols{p.c, kept};
+    uint32_t col[C], mask[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t c = (int64_t)i * blockDim.x + threadIdx.x;
-        float w[8];
-        memory.pre(i, c, mask[i], w);
-        cols.keep(kept, 2 * i, w);
-        memory.load_factor(c, mask[i], w);
-        cols.keep(kept, 2 * (C + i), w);
+        col[i] = first_col<G>(i);
+        mask[i] = runs_below<G>(col[i], p.c.cols);
     }
-    float sum_pre[C][8] = {}, sum_q[C][8] = {};
+    QueueLoader<T, C, K> in(p, smem + (size_t)blockDim.x * C * 2 * 32, col, mask);
+    const Columns<T, G, C, true> cols{p.c, col, mask, (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16};
+    const Columns<T, G, C, false> memory{p.c, col, mask, 0};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        cols.keep(2 * i, memory.pre(i));
+        cols.keep(2 * (C + i), memory.load_factor(i));
+    }
+    F8 sum_pre[C] = {}, sum_q[C] = {};
     float sum_scalar = 0.0f;
     for (int64_t row = blockIdx.x; row < p.c.rows; row += gridDim.x) {
         in.row(row);
-        back_row<T, true, C, true>(p, row, in, mask, cols, sum_pre, sum_q, sum_scalar, slots, turn);
+        back_row<T, G, C, true>(p, row, in, cols, sum_pre, sum_q, sum_scalar, slots, turn);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    store_sums<true, C>(p, mask, sum_pre, sum_q, sum_scalar);
+    store_sums<G, C>(p, col, mask, sum_pre, sum_q, sum_scalar);
 }
 
 // Chunks straight from memory, for rows at any address and very wide ones.
-template <class T, bool V, int C>
+template <class T, int G, int C>
 struct DirectLoader {
     const NormBackParams& p;
+    const uint32_t (&col)[C];
     const uint32_t (&mask)[C];
     int64_t row;
-    CkptRaw<V> codes[C];
-    Raw8<T> whole[C];
+    CkptRaw<G> codes[C];
+    Raw8<T, G> whole[C];
 
-    __device__ __forceinline__ int64_t chunk(int i) const { return (int64_t)i * blockDim.x + threadIdx.x; }
-    __device__ __forceinline__ void begin() {}
     __device__ __forceinline__ void end() {}
     __device__ __forceinline__ void fetch(const void* m, int64_t ld, const ptoc_ckpt8& k)
     {
         const Ckpt c{k.codes, k.exps, k.ld_codes, k.ld_exps};
+        if (m) begin_matrix(m, ld);
+        else
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            if (m) whole[i] = load8<T, V>((const T*)m + row * ld, chunk(i), mask[i]);
-            else codes[i] = ckpt_load8<V>(c, row, chunk(i), mask[i]);
-        }
+            for (int i = 0; i < C; ++i) codes[i] = ckpt_load8<G>(c, row, col[i], mask[i]);
     }
     __device__ __forceinline__ void begin_stream() { fetch(p.stream, p.ld_stream, p.stream_ckpt); }
     __device__ __forceinline__ void begin_block() { fetch(p.block, p.ld_block, p.block_ckpt); }
-    __device__ __forceinline__ Raw8<T> matrix(int i, const void* m, int64_t ld) const
+    __device__ __forceinline__ void begin_matrix(const void* m, int64_t ld)
     {
-        return load8<T, V>((const T*)m + row * ld, chunk(i), mask[i]);
-    }
-    __device__ __forceinline__ void saved(int i, bool matrix, float factor, float* v) const
-    {
-        if (matrix) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = whole[i].at(j) * factor;
-        } else {
-            ckpt_values<V>(codes[i], factor, v);
-        }
+        for (int i = 0; i < C; ++i) whole[i] = load8<T, G>((const T*)m + row * ld, col[i], mask[i]);
     }
-    __device__ __forceinline__ void stream(int i, float f, float* v) const { saved(i, p.stream, f, v); }
-    __device__ __forceinline__ void block(int i, float f, float* v) const { saved(i, p.block, f, v); }
+    __device__ __forceinline__ const Raw8<T, G>& matrix(int i) const { return whole[i]; }
+    __device__ __forceinline__ F8 saved(int i, bool matrix, float factor) const
+    {
+        if (!matrix) return ckpt_values<G>(codes[i], factor);
+        F8 f = whole[i].expand();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f.p[j] = mul2(f.p[j], both(factor));
+        return f;
+    }
+    __device__ __forceinline__ F8 stream(int i, float f) const { return saved(i, p.stream, f); }
+    __device__ __forceinline__ F8 block(int i, float f) const { return saved(i, p.block, f); }
 };
 
-template <class T, bool V, int C>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormBackParams p)
+template <class T, int G, int C>
+__global__ void __launch_bounds__(C == 2 ? 512 : 1024) norm_backward_kernel(const NormBackParams p)
 {
     pdl_enter();
     __shared__ float slots[2][32];
     int turn = 0;
-    uint32_t mask[C];
+    uint32_t col[C], mask[C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) mask[i] = chunk_mask<V>((int64_t)i * blockDim.x + threadIdx.x, p.c.cols);
-    const Columns<T, V, false> cols{p.c, nullptr};
-    float sum_pre[C][8] = {}, sum_q[C][8] = {};
+    for (int i = 0; i < C; ++i) {
+        col[i] = first_col<G>(i);
+        mask[i] = runs_below<G>(col[i], p.c.cols);
+    }
+    const Columns<T, G, C, false> cols{p.c, col, mask, 0};
+    F8 sum_pre[C] = {}, sum_q[C] = {};
     float sum_scalar = 0.0f;
     for (int64_t row = blockIdx.x; row < p.c.rows; row += gridDim.x) {
-        DirectLoader<T, V, C> in{p, mask, row};
-        back_row<T, V, C, false>(p, row, in, mask, cols, sum_pre, sum_q, sum_scalar, slots, turn);
+        DirectLoader<T, G, C> in{p, col, mask, row};
+        back_row<T, G, C, false>(p, row, in, cols, sum_pre, sum_q, sum_scalar, slots, turn);
     }
-    store_sums<V, C>(p, mask, sum_pre, sum_q, sum_scalar);
+    store_sums<G, C>(p, col, mask, sum_pre, sum_q, sum_scalar);
 }
 
 // Sums of the partial rows: a block takes 32 columns of one kind; its 8 warps
@@ -440,20 +467,18 @@ cudaError_t launch(const NormBackParams& p, cudaStream_t s)
     const int64_t groups = (p.c.cols + 255) / 256;
     cudaError_t e;
     if (p.c.vec && p.c.cols <= kQueueCols) {
-        const unsigned threads = (unsigned)((p.c.cols + 511) / 512) * 32;
+        const unsigned threads = (unsigned)((groups + 1) / 2) * 32;
         const size_t per_thread = 2 * (2 * 32 + (size_t)kItems<T> * sizeof(T) * 8);
         auto kernel = norm_backward_queue_kernel<T, kItems<T>>;
         e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)(per_thread * kQueueThreads));
         if (e == cudaSuccess) e = launch_kernel(kernel, grid, threads, per_thread * threads, s, p);
     } else if (p.c.vec) {
-        e = launch_kernel(norm_backward_kernel<T, true, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
-    } else if (groups <= 32) {
-        e = launch_kernel(norm_backward_kernel<T, false, 1>, grid, (unsigned)groups * 32, 0, s, p);
-    } else if (groups <= 64) {
-        e = launch_kernel(norm_backward_kernel<T, false, 2>, grid, (unsigned)((groups + 1) / 2) * 32, 0, s, p);
+        e = launch_kernel(norm_backward_kernel<T, kVector<T>, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
+    } else if (p.c.cols <= kQueueCols) {
+        e = launch_kernel(norm_backward_kernel<T, 1, 2>, grid, (unsigned)((groups + 1) / 2) * 32, 0, s, p);
     } else {
-        e = launch_kernel(norm_backward_kernel<T, false, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
+        e = launch_kernel(norm_backward_kernel<T, 1, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
     }
     if (e != cudaSuccess) return e;
     if (!p.d_pre && !p.need_q && p.gate_kind != kGateScalar) return cudaSuccess;

@@ -15,39 +15,32 @@ constexpr int kUnits = 4;            // work units whose loads a warp issues tog
 
 // Work unit u: 256 columns of row u / units_per_row, held by one warp. A block
 // takes kUnits * 8 neighbouring units, its warps in turn.
-template <class T, bool V, bool RESTORE>
+template <class T, int G, bool RESTORE>
 __global__ void __launch_bounds__(kBlock) ckpt8_kernel(const Ckpt8Params p)
 {
     pdl_enter();
     const uint32_t per_row = (uint32_t)((p.cols + 255) / 256), units = (uint32_t)p.rows * per_row;
     const uint32_t unit0 = blockIdx.x * (kUnits * kBlock / 32) + (threadIdx.x >> 5);
     const Ckpt k{p.ckpt.codes, p.ckpt.exps, p.ckpt.ld_codes, p.ckpt.ld_exps};
-    int64_t row[kUnits], c[kUnits];
-    uint32_t mask[kUnits];
-    Raw8<T> raw[kUnits];
-    CkptRaw<V> codes[kUnits];
+    int64_t row[kUnits];
+    uint32_t col[kUnits], mask[kUnits];
+    Raw8<T, G> raw[kUnits];
+    CkptRaw<G> codes[kUnits];
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
         const uint32_t unit = unit0 + q * (kBlock / 32);
         const uint32_t r = unit / per_row;
         row[q] = r;
-        c[q] = (int64_t)(unit - r * per_row) * 32 + (threadIdx.x & 31);
-        mask[q] = unit < units ? chunk_mask<V>(c[q], p.cols) : 0u;
-        if constexpr (RESTORE) codes[q] = ckpt_load8<V>(k, row[q], c[q], mask[q]);
-        else raw[q] = load8<T, V>((const T*)p.x + row[q] * p.ld, c[q], mask[q]);
+        col[q] = (unit - r * per_row) * 256 + (threadIdx.x & 31) * G;
+        mask[q] = unit < units ? runs_below<G>(col[q], p.cols) : 0u;
+        if constexpr (RESTORE) codes[q] = ckpt_load8<G>(k, row[q], col[q], mask[q]);
+        else raw[q] = load8<T, G>((const T*)p.x + row[q] * p.ld, col[q], mask[q]);
     }
 #pragma unroll
     for (int q = 0; q < kUnits; ++q) {
         if (unit0 + q * (kBlock / 32) >= units) break;         // the whole warp
-        float v[8];
-        if constexpr (RESTORE) {
-            ckpt_values<V>(codes[q], 1.0f, v);
-            store8<T, V>((T*)p.x + row[q] * p.ld, c[q], mask[q], v);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = raw[q].at(j);
-            ckpt_store8<V>(k, row[q], c[q], mask[q], v);
-        }
+        if constexpr (RESTORE) store8<T, G>((T*)p.x + row[q] * p.ld, col[q], mask[q], ckpt_values<G>(codes[q], 1.0f));
+        else ckpt_store8<G>(k, row[q], col[q], mask[q], raw[q].expand());
     }
 }
 
@@ -57,8 +50,8 @@ cudaError_t launch(const Ckpt8Params& p, cudaStream_t s)
     const int64_t units = p.rows * ((p.cols + 255) / 256);
     const int64_t per_block = kUnits * kBlock / 32;
     const dim3 grid((unsigned)((units + per_block - 1) / per_block));
-    return p.vec ? launch_kernel(ckpt8_kernel<T, true, RESTORE>, grid, kBlock, 0, s, p)
-                 : launch_kernel(ckpt8_kernel<T, false, RESTORE>, grid, kBlock, 0, s, p);
+    return p.vec ? launch_kernel(ckpt8_kernel<T, kVector<T>, RESTORE>, grid, kBlock, 0, s, p)
+                 : launch_kernel(ckpt8_kernel<T, 1, RESTORE>, grid, kBlock, 0, s, p);
 }
 
 template <bool RESTORE>

@@ -95,7 +95,7 @@ ptoc_status ckpt8_call(const ptoc_matrix* x, const ptoc_ckpt8* k, int64_t rows, 
     p.ckpt = *k;
     p.rows = rows;
     p.cols = cols;
-    p.vec = o.vec && cols % 8 == 0;
+    p.vec = o.vec && cols % (16 / elem_size(dtype)) == 0;
     return status_of(restore ? launch_restore8(p, dtype, stream) : launch_checkpoint8(p, dtype, stream));
 }
 
@@ -212,7 +212,7 @@ extern "C" ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts
     if (st != PTOC_OK) return st;
     if (cols > PTOC_NORM_MAX_COLS) return PTOC_ERR_UNSUPPORTED;
     if (rows == 0 || cols == 0) return PTOC_OK;
-    p.c.vec = o.vec && cols % 8 == 0;
+    p.c.vec = o.vec && cols % (16 / eb) == 0;
     p.nparts = parts->nranks;
     p.ld_part = ld_parts;
     p.x = x->data;
@@ -295,7 +295,7 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
         if (gate_bytes && cudaMemsetAsync(d_gate, 0, gate_bytes, stream) != cudaSuccess) return PTOC_ERR_CUDA;
         return PTOC_OK;
     }
-    p.c.vec = o.vec && cols % 8 == 0;
+    p.c.vec = o.vec && cols % (16 / eb) == 0;
     p.block = sv.block.data;
     p.ld_block = sv.block.ld;
     p.block_ckpt = sv.block_ckpt;

@@ -29,177 +29,218 @@ __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2hal
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// ---- 8 columns per thread --------------------------------------------------------
-// A row is cut into chunks of 8 columns; chunk c is held by one thread. With V
-// (bases and pitches 16-byte aligned, a multiple of 8 columns) a chunk is 8
-// neighbouring columns, moved as 16-byte words. Otherwise 32 neighbouring
-// chunks, one per lane of a warp, cover their 256 columns with lane-contiguous
-// elements (column 32 j + lane), so that element-wide accesses still coalesce.
-// Either way 32 columns that share an exponent lie in one warp: 4 lanes (V),
-// or element j of all lanes. Loads and stores are predicated, not branched
-// around, so that those of several chunks can be in flight together.
+// ---- pairs of floats ------------------------------------------------------------------
+// The kernels below issue several instructions per element and are close to
+// the issue rate, so their arithmetic is written on pairs (one instruction for
+// two binary32 operations, each rounded as usual).
 
-template <bool V>
-__device__ __forceinline__ int64_t col_of(int64_t c, int j)
+using Pair = unsigned long long;
+
+__device__ __forceinline__ Pair pair(float lo, float hi)
 {
-    if constexpr (V) return c * 8 + j;
-    else return (c & ~(int64_t)31) * 8 + j * 32 + (c & 31);
+    Pair r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-
-// Elements of chunk c that lie below `cols`, as a bit mask (V: all or none).
-template <bool V>
-__device__ __forceinline__ uint32_t chunk_mask(int64_t c, int64_t cols)
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ void split(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ float sum_of(Pair p)
 {
-    if constexpr (V) return c * 8 < cols ? 0xffu : 0u;
-    const int64_t left = cols - col_of<V>(c, 0);        // element j is in if 32 j < left
-    return left <= 0 ? 0u : left > 7 * 32 ? 0xffu : (1u << ((left + 31) / 32)) - 1u;
+    float a, b;
+    split(p, a, b);
+    return a + b;
 }
-
-__device__ __forceinline__ Words<4> load16_if(const void* p, bool on)
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c)
 {
-    Words<4> r;
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %5, 0;\n"
-                 "mov.u32 %0, 0; mov.u32 %1, 0; mov.u32 %2, 0; mov.u32 %3, 0;\n"
-                 "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4]; }"
-                 : "=&r"(r.w[0]), "=&r"(r.w[1]), "=&r"(r.w[2]), "=&r"(r.w[3]) : "l"(p), "r"((uint32_t)on) : "memory");
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b)
+{
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b)
+{
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 
-__device__ __forceinline__ Words<2> load8_if(const void* p, bool on)
-{
-    Words<2> r;
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %3, 0; mov.u32 %0, 0; mov.u32 %1, 0;\n"
-                 "@p ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2]; }"
-                 : "=&r"(r.w[0]), "=&r"(r.w[1]) : "l"(p), "r"((uint32_t)on) : "memory");
-    return r;
-}
+// Eight columns in binary32.
+struct F8 {
+    Pair p[4];
+};
 
-__device__ __forceinline__ uint32_t load4_if(const void* p, bool on)
-{
-    uint32_t r;
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; mov.u32 %0, 0; @p ld.global.u32 %0, [%1]; }"
-                 : "=&r"(r) : "l"(p), "r"((uint32_t)on) : "memory");
-    return r;
-}
+// ---- 8 columns per thread ----------------------------------------------------------------
+// A row is cut into groups of 256 columns, one per warp; a lane holds 8 of
+// them (chunk c = 32 * group + lane) as 8 / G runs of G neighbouring columns:
+// G = 8, one 16-byte word of 16-bit elements; G = 4, two words of binary32;
+// G = 1, element-wide accesses, for rows at any address and of any length. Run
+// q of lane l starts at column 32 * G * q + G * l of the group, so that a warp
+// always touches neighbouring words, and 32 columns that share an exponent lie
+// in one run of neighbouring lanes. G > 1 needs 16-byte aligned bases and
+// pitches and a multiple of G columns.
 
-__device__ __forceinline__ uint32_t load2_if(const void* p, bool on)
-{
-    uint32_t r;
-    asm volatile("{ .reg .pred p; .reg .u16 h; setp.ne.u32 p, %2, 0; mov.u16 h, 0; @p ld.global.u16 h, [%1];\n"
-                 "cvt.u32.u16 %0, h; }"
-                 : "=&r"(r) : "l"(p), "r"((uint32_t)on) : "memory");
-    return r;
-}
-
-__device__ __forceinline__ uint32_t load1_if(const void* p, bool on)
-{
-    uint32_t r;
-    asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; mov.u32 %0, 0; @p ld.global.u8 %0, [%1]; }"
-                 : "=&r"(r) : "l"(p), "r"((uint32_t)on) : "memory");
-    return r;
-}
-
-// The chunk's raw elements (zeros outside the mask); expanded later, so that
-// several loads can be in flight in few registers.
 template <class T>
+constexpr int kVector = 16 / (int)sizeof(T);
+
+// The first column of lane `threadIdx.x` in the chunk i * blockDim.x + threadIdx.x.
+template <int G>
+__device__ __forceinline__ uint32_t first_col(int i)
+{
+    const uint32_t c = (uint32_t)i * blockDim.x + threadIdx.x;
+    return (c & ~31u) * 8 + (c & 31u) * G;
+}
+template <int G>
+__device__ __forceinline__ constexpr uint32_t run_step() { return 32 * G; }
+
+// Which of the chunk's runs, from column `col` on, lie below `cols`.
+template <int G>
+__device__ __forceinline__ uint32_t runs_below(uint32_t col, int64_t cols)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < 8 / G; ++q) m |= (int64_t)col + q * 32 * G < cols ? 1u << q : 0u;
+    return m;
+}
+
+// A chunk as read: words of the type (G > 1), or one element per word.
+template <class T, int G>
 struct Raw8 {
-    Words<8 * sizeof(T) / 4> w;
-    __device__ __forceinline__ float at(int j) const
+    static constexpr int kWords = G == 1 ? 8 : 8 * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+
+    __device__ __forceinline__ F8 expand() const
     {
-        if constexpr (sizeof(T) == 4) return __uint_as_float(w.w[j]);
-        else if constexpr (std::is_same<T, __nv_bfloat16>::value)
-            return __uint_as_float(j & 1 ? w.w[j >> 1] & 0xffff0000u : w.w[j >> 1] << 16);
-        else {
-            const uint32_t p = w.w[j >> 1];
-            return to_f32(bitcast<T>((uint16_t)(j & 1 ? p >> 16 : p & 0xffffu)));
+        F8 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (sizeof(T) == 4) f.p[i] = pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+            else if constexpr (G == 1) f.p[i] = pair(widen(w[2 * i]), widen(w[2 * i + 1]));
+            else f.p[i] = pair(widen(w[i] & 0xffffu), widen_high(w[i]));
         }
+        return f;
+    }
+    static __device__ __forceinline__ float widen(uint32_t h)
+    {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(h << 16);
+        else return __half2float(bitcast<__half>((uint16_t)h));
+    }
+    static __device__ __forceinline__ float widen_high(uint32_t h)
+    {
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) return __uint_as_float(h & 0xffff0000u);
+        else return __half2float(bitcast<__half>((uint16_t)(h >> 16)));
     }
 };
 
-template <class T, bool V>
-__device__ __forceinline__ Raw8<T> load8(const T* row, int64_t c, uint32_t mask)
+// `row` is the same for all threads, `col` this thread's first column; runs
+// outside the mask give zeros. Ordinary loads: the wait for the previous
+// kernel is a barrier for them, which it would not be for read-only loads.
+template <class T, int G>
+__device__ __forceinline__ Raw8<T, G> load8(const T* row, uint32_t col, uint32_t mask)
 {
-    Raw8<T> r;
-    if constexpr (V) {
-        const char* p = (const char*)(row + c * 8);
+    Raw8<T, G> r;
+    const T* p = row + col;
+    if constexpr (G == 1) {
 #pragma unroll
-        for (int q = 0; q < (int)sizeof(T) / 2; ++q) {
-            const Words<4> v = load16_if(p + 16 * q, mask != 0);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) r.w.w[4 * q + i] = v.w[i];
+        for (int j = 0; j < 8; ++j) {
+            r.w[j] = 0;
+            if (mask >> j & 1) {
+                if constexpr (sizeof(T) == 4) r.w[j] = *(const uint32_t*)(p + 32 * j);
+                else r.w[j] = *(const uint16_t*)(p + 32 * j);
+            }
         }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r.w.w[j] = load4_if(row + col_of<V>(c, j), mask >> j & 1);
     } else {
-        uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[j] = load2_if(row + col_of<V>(c, j), mask >> j & 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.w.w[i] = h[2 * i] | h[2 * i + 1] << 16;
+        for (int q = 0; q < 8 / G; ++q) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (mask >> q & 1) v = *(const uint4*)(p + 32 * G * q);
+            r.w[4 * q] = v.x, r.w[4 * q + 1] = v.y, r.w[4 * q + 2] = v.z, r.w[4 * q + 3] = v.w;
+        }
     }
     return r;
 }
 
 // Two floats rounded to a word of two elements (the first in the low half).
 template <class T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi)
+__device__ __forceinline__ uint32_t pack2(Pair v)
 {
+    float lo, hi;
+    split(v, lo, hi);
     if constexpr (std::is_same<T, __half>::value) return bitcast<uint32_t>(__floats2half2_rn(lo, hi));
     else return bitcast<uint32_t>(__floats2bfloat162_rn(lo, hi));
 }
 
-template <class T, bool V>
-__device__ __forceinline__ void store8(T* row, int64_t c, uint32_t mask, const float* v)
+// The words that store8 writes.
+template <class T, int G>
+__device__ __forceinline__ Raw8<T, G> round8(const F8& v)
 {
-    if constexpr (V) {
-        char* p = (char*)(row + c * 8);
+    Raw8<T, G> r;
 #pragma unroll
-        for (int q = 0; q < (int)sizeof(T) / 2; ++q) {
-            Words<4> w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 4) w.w[i] = __float_as_uint(v[4 * q + i]);
-                else w.w[i] = pack2<T>(v[2 * i], v[2 * i + 1]);
-            }
-            asm volatile("{ .reg .pred p; setp.ne.u32 p, %5, 0; @p st.global.v4.u32 [%4], {%0, %1, %2, %3}; }"
-                         ::"r"(w.w[0]), "r"(w.w[1]), "r"(w.w[2]), "r"(w.w[3]), "l"(p + 16 * q), "r"(mask)
-                         : "memory");
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) {
+            float lo, hi;
+            split(v.p[i], lo, hi);
+            r.w[2 * i] = __float_as_uint(lo), r.w[2 * i + 1] = __float_as_uint(hi);
+        } else {
+            const uint32_t w = pack2<T>(v.p[i]);
+            if constexpr (G == 1) r.w[2 * i] = w & 0xffffu, r.w[2 * i + 1] = w >> 16;
+            else r.w[i] = w;
         }
+    }
+    return r;
+}
+
+template <class T, int G>
+__device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, const Raw8<T, G>& r)
+{
+    T* p = row + col;
+    if constexpr (G == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (mask >> j & 1) {
+                if constexpr (sizeof(T) == 4) *(uint32_t*)(p + 32 * j) = r.w[j];
+                else *(uint16_t*)(p + 32 * j) = (uint16_t)r.w[j];
+            }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            T* p = row + col_of<V>(c, j);
-            if constexpr (sizeof(T) == 4)
-                asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p st.global.u32 [%1], %0; }"
-                             ::"r"(__float_as_uint(v[j])), "l"(p), "r"(mask >> j & 1)
-                             : "memory");
-            else
-                asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p st.global.u16 [%1], %0; }"
-                             ::"h"(bitcast<uint16_t>(from_f32<T>(v[j]))), "l"(p), "r"(mask >> j & 1)
-                             : "memory");
-        }
+        for (int q = 0; q < 8 / G; ++q)
+            if (mask >> q & 1)
+                *(uint4*)(p + 32 * G * q) = make_uint4(r.w[4 * q], r.w[4 * q + 1], r.w[4 * q + 2], r.w[4 * q + 3]);
     }
 }
 
-// Parameters (weights, gates): of the activations' type or binary32; one where
-// null, zero outside the mask. Ordinary loads: a read-only load could be moved
-// ahead of the wait for the previous kernel.
-template <class T, bool V>
-__device__ __forceinline__ void load_param8(const void* base, bool f32, int64_t c, uint32_t mask, float* v)
+template <class T, int G>
+__device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, const F8& v)
 {
+    store8<T, G>(row, col, mask, round8<T, G>(v));
+}
+
+// Parameters (weights, gates) in the mapping of the activations: of their type
+// or binary32; one where null, zero outside the mask.
+template <class T, int G>
+__device__ __forceinline__ F8 load_param8(const void* base, bool f32, uint32_t col, uint32_t mask)
+{
+    F8 f;
     if (!base) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 1.0f;
-    } else if (f32) {
-        const Raw8<float> r = load8<float, V>((const float*)base, c, mask);
+        for (int i = 0; i < 4; ++i) f.p[i] = both(1.0f);
+    } else if (f32 && sizeof(T) == 2) {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r.at(j);
+        for (int j = 0; j < 8; ++j) {
+            const int q = j / G;
+            v[j] = mask >> q & 1 ? ((const float*)base)[col + q * 32 * G + j % G] : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f.p[i] = pair(v[2 * i], v[2 * i + 1]);
     } else {
-        const Raw8<T> r = load8<T, V>((const T*)base, c, mask);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r.at(j);
+        f = load8<T, G>((const T*)base, col, mask).expand();
     }
+    return f;
 }
 
 // ---- block-wide sums ---------------------------------------------------------------
@@ -257,10 +298,7 @@ __device__ __forceinline__ float ckpt_scale(uint32_t byte)
 // x / 2^e rounded to the nearest integer, ties to even, in the low byte of the
 // result: x * 2^-e is exact and at most 127 in magnitude, and adding 1.5 * 2^23
 // leaves no fraction bits, so the one rounding is that of the sum.
-__device__ __forceinline__ uint32_t ckpt_code(float x, float inverse)
-{
-    return __float_as_uint(__fmaf_rn(x, inverse, 12582912.0f));
-}
+constexpr float kCodeBias = 12582912.0f;
 
 // Largest magnitude, or NaN if either is one.
 __device__ __forceinline__ float max_abs(float a, float b)
@@ -276,187 +314,201 @@ struct Ckpt {
     int64_t ld_codes, ld_exps;
 };
 
-// Write chunk c (masked columns hold 0) of one row. Every lane of the warp
+// Write a chunk (zeros outside the mask) of one row. Every lane of the warp
 // takes part, also those whose mask is empty.
-template <bool V>
-__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int64_t c, uint32_t mask, const float* v)
+template <int G>
+__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, uint32_t col, uint32_t mask, const F8& f)
 {
-    int8_t* codes = k.codes + row * k.ld_codes;
+    int8_t* codes = k.codes + row * k.ld_codes + col;
     uint8_t* exps = k.exps + row * k.ld_exps;
-    if constexpr (V) {
-        float top = max_abs(v[0], v[1]);
+    float v[8];
 #pragma unroll
-        for (int j = 2; j < 8; ++j) top = max_abs(top, v[j]);
-        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t byte = ckpt_exponent(__float_as_uint(top));
-        const float inv = ckpt_inverse(byte);
-        uint32_t q[8];
+    for (int i = 0; i < 4; ++i) split(f.p[i], v[2 * i], v[2 * i + 1]);
+    if constexpr (G > 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = ckpt_code(v[j], inv);
-        uint32_t w[2];
+        for (int q = 0; q < 8 / G; ++q) {
+            float top = max_abs(v[G * q], v[G * q + 1]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            w[i] = __byte_perm(__byte_perm(q[4 * i], q[4 * i + 1], 0x0040),
-                               __byte_perm(q[4 * i + 2], q[4 * i + 3], 0x0040), 0x5410);
-            if (byte == 255u) w[i] = 0u;
+            for (int j = 2; j < G; ++j) top = max_abs(top, v[G * q + j]);
+#pragma unroll
+            for (int o = 1; o < 32 / G; o <<= 1) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const uint32_t byte = ckpt_exponent(__float_as_uint(top));
+            const Pair inv = both(ckpt_inverse(byte)), bias = both(kCodeBias);
+            uint32_t w[G / 4];
+#pragma unroll
+            for (int i = 0; i < G / 4; ++i) {
+                float c[4];
+                split(fma2(f.p[(G * q + 4 * i) / 2], inv, bias), c[0], c[1]);
+                split(fma2(f.p[(G * q + 4 * i) / 2 + 1], inv, bias), c[2], c[3]);
+                w[i] = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
+                                   __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040), 0x5410);
+                if (byte == 255u) w[i] = 0u;
+            }
+            if (mask >> q & 1) {
+                if constexpr (G == 8) *(uint2*)codes = make_uint2(w[0], w[G / 4 - 1]);
+                else *(uint32_t*)(codes + 32 * G * q) = w[0];
+                const uint32_t at = col + q * 32 * G;
+                if ((at & 31u) == 0) exps[at >> 5] = (uint8_t)byte;
+            }
         }
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %3, 0; @p st.global.v2.u32 [%2], {%0, %1}; }"
-                     ::"r"(w[0]), "r"(w[1]), "l"(codes + c * 8), "r"(mask)
-                     : "memory");
-        if (mask && (c & 3) == 0) exps[c >> 2] = (uint8_t)byte;
     } else {
         // lane j keeps the byte of element j's block and stores it
-        const int64_t block0 = (c & ~(int64_t)31) >> 2;      // 8 blocks of 32 columns per 32 chunks
-        uint32_t keep = 0, any = 0;
+        const uint32_t lane = threadIdx.x & 31;
+        uint32_t keep = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu);
             const uint32_t byte = ckpt_exponent(top);
-            const uint32_t code = byte == 255u ? 0u : ckpt_code(v[j], ckpt_inverse(byte));
-            asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p st.global.u8 [%1], %0; }"
-                         ::"r"(code), "l"(codes + col_of<false>(c, j)), "r"(mask >> j & 1)
-                         : "memory");
-            if ((c & 31) == j) keep = byte;
+            const uint32_t code = byte == 255u ? 0u : __float_as_uint(__fmaf_rn(v[j], ckpt_inverse(byte), kCodeBias));
+            if (mask >> j & 1) codes[32 * j] = (int8_t)code;
+            if (lane == j) keep = byte;
         }
-        any = __shfl_sync(0xffffffffu, mask, 0);              // a block exists where its first column does
-        if ((c & 31) < 8 && (any >> (c & 31) & 1)) exps[block0 + (c & 31)] = (uint8_t)keep;
+        const uint32_t any = __shfl_sync(0xffffffffu, mask, 0);        // a block exists where its first column does
+        if (lane < 8 && (any >> lane & 1)) exps[((col - lane) >> 5) + lane] = (uint8_t)keep;
     }
 }
 
-// Chunk c of one row as read: the codes and the exponent byte (V), or a code
-// for each element and, in lane j, the byte of element j's block.
-template <bool V>
+// A chunk as read: code words (or single codes), and exponent bytes: one per
+// run, or in lane j that of element j's block.
+template <int G>
 struct CkptRaw {
-    uint32_t w[V ? 2 : 8];
-    uint32_t byte;
+    uint32_t w[G == 1 ? 8 : 2];
+    uint32_t byte[G == 4 ? 2 : 1];
 };
 
-template <bool V>
-__device__ __forceinline__ CkptRaw<V> ckpt_load8(const Ckpt& k, int64_t row, int64_t c, uint32_t mask)
+template <int G>
+__device__ __forceinline__ CkptRaw<G> ckpt_load8(const Ckpt& k, int64_t row, uint32_t col, uint32_t mask)
 {
-    const int8_t* codes = k.codes + row * k.ld_codes;
+    const int8_t* codes = k.codes + row * k.ld_codes + col;
     const uint8_t* exps = k.exps + row * k.ld_exps;
-    CkptRaw<V> r;
-    if constexpr (V) {
-        const Words<2> w = load8_if(codes + c * 8, mask != 0);
-        r.w[0] = w.w[0];
-        r.w[1] = w.w[1];
-        r.byte = load1_if(exps + (c >> 2), mask != 0);
+    CkptRaw<G> r;
+    if constexpr (G == 8) {
+        uint2 w = make_uint2(0, 0);
+        if (mask) w = *(const uint2*)codes;
+        r.w[0] = w.x, r.w[1] = w.y;
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r.w[j] = load1_if(codes + col_of<V>(c, j), mask >> j & 1);
-        const uint32_t any = __shfl_sync(0xffffffffu, mask, 0);
-        const int lane = (int)(c & 31);
-        r.byte = load1_if(exps + ((c & ~(int64_t)31) >> 2) + lane, lane < 8 && (any >> lane & 1));
+        for (int j = 0; j < 8 / G; ++j) {
+            r.w[j] = 0;
+            if (mask >> j & 1) r.w[j] = G == 4 ? *(const uint32_t*)(codes + 128 * j) : *(const uint8_t*)(codes + 32 * j);
+        }
+    }
+    if constexpr (G == 1) {
+        const uint32_t any = __shfl_sync(0xffffffffu, mask, 0), lane = threadIdx.x & 31;
+        r.byte[0] = 0;
+        if (lane < 8 && (any >> lane & 1)) r.byte[0] = exps[((col - lane) >> 5) + lane];
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8 / G; ++q) {
+            r.byte[q] = 0;
+            if (mask >> q & 1) r.byte[q] = exps[(col + q * 32 * G) >> 5];
+        }
     }
     return r;
 }
 
-// A code byte as a float, without the slow integer conversion: with its sign
-// bit flipped it is the lowest byte of 2^23 + 128 + code.
-__device__ __forceinline__ float code_value(uint32_t flipped, int byte)
+// A code byte in the float 2^23 + 128 + code, without the slow integer
+// conversion: with its sign bit flipped it is the lowest byte.
+__device__ __forceinline__ float code_float(uint32_t flipped, int byte)
 {
-    return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7650 + byte)) - 8388736.0f;
+    return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7650 + byte));
 }
 
-// The chunk's values times `factor` (0 outside the mask, which has codes 0).
-template <bool V>
-__device__ __forceinline__ void ckpt_values(const CkptRaw<V>& r, float factor, float* v)
+// The chunk's values times `factor` (0 outside the mask, where codes are 0).
+template <int G>
+__device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
 {
-    if constexpr (V) {
-        const float scale = ckpt_scale(r.byte) * factor;
-        const uint32_t w[2] = {r.w[0] ^ 0x80808080u, r.w[1] ^ 0x80808080u};
+    F8 f;
+    const Pair bias = both(-8388736.0f);
+    if constexpr (G == 1) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = code_value(w[j >> 2], j & 3) * scale;
+        for (int i = 0; i < 4; ++i) {
+            const float lo = ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i)) * factor;
+            const float hi = ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i + 1)) * factor;
+            f.p[i] = mul2(add2(pair(code_float(r.w[2 * i] ^ 0x80u, 0), code_float(r.w[2 * i + 1] ^ 0x80u, 0)), bias),
+                          pair(lo, hi));
+        }
     } else {
+        Pair scale[8 / G];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float scale = ckpt_scale(__shfl_sync(0xffffffffu, r.byte, j)) * factor;
-            v[j] = code_value(r.w[j] ^ 0x80u, 0) * scale;
+        for (int q = 0; q < 8 / G; ++q) scale[q] = both(ckpt_scale(r.byte[q]) * factor);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w = r.w[i / 2] ^ 0x80808080u;
+            f.p[i] = mul2(add2(pair(code_float(w, 2 * (i & 1)), code_float(w, 2 * (i & 1) + 1)), bias),
+                          scale[G == 4 ? i / 2 : 0]);
         }
     }
+    return f;
 }
 
 // ---- a thread's queue of copies in shared memory ---------------------------------------
-// Items (one chunk of C * 8 elements of one row of one tensor) are copied
-// ahead of their use, in the order of their use: K of them are always in
-// flight or waiting. A thread copies and reads its own bytes only, so nothing
-// but its own wait for the copy is needed. Slots of 16 bytes per chunk word;
-// W words of 16 bytes per chunk.
-template <int C, int W, int K>
+// Items (this thread's C chunks of one row of one tensor) are copied ahead of
+// their use, in the order of their use: K of them are always in flight or
+// waiting. A thread copies and reads its own bytes only, so nothing but its
+// own wait for the copy is needed. A chunk past the row's end is filled with
+// zeros (a copy of no source bytes).
+template <class T, int C, int K>
 struct Queue {
-    uint32_t base, stride, slot;
-    static constexpr int kPerThread = C * W * 16;
+    static constexpr int G = kVector<T>, W = 8 / G;          // words of 16 bytes per chunk
+    uint32_t at, begin, end;                                 // the current slot; the first; past the last
 
     __device__ __forceinline__ Queue(void* smem)
     {
-        stride = (uint32_t)blockDim.x * kPerThread;
-        base = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-        slot = 0;
+        begin = at = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
+        end = begin + K * C * W * 16 * blockDim.x;
     }
-    __device__ __forceinline__ uint32_t word(int i, int q) const
-    {
-        return base + slot * stride + (uint32_t)((i * W + q) * 16) * blockDim.x;
-    }
-    // Start the copy of `bytes` (16 or 8) into word (i, q) of the current slot.
-    __device__ __forceinline__ void copy16(int i, int q, const void* src, bool on)
-    {
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p cp.async.cg.shared.global [%0], [%1], 16; }"
-                     ::"r"(word(i, q)), "l"(src), "r"((uint32_t)on)
-                     : "memory");
-    }
-    __device__ __forceinline__ void copy8(int i, const void* src, bool on)
-    {
-        asm volatile("{ .reg .pred p; setp.ne.u32 p, %2, 0; @p cp.async.ca.shared.global [%0], [%1], 8; }"
-                     ::"r"(word(i, 0)), "l"(src), "r"((uint32_t)on)
-                     : "memory");
-    }
-    // The current slot is filled (or left empty at the end): go on.
-    __device__ __forceinline__ void next()
-    {
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        slot = slot + 1 == K ? 0 : slot + 1;
-    }
-    // Wait until the oldest item, which lies in the current slot, has landed.
-    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory"); }
-    __device__ __forceinline__ Words<4> read(int i, int q) const
-    {
-        Words<4> r;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(word(i, q)) : "memory");
-        return r;
-    }
-    // The words of chunk i in every slot read as zeros: for a chunk past the row's end.
-    __device__ __forceinline__ void clear(int i)
-    {
-        for (slot = 0; slot < K; ++slot)
-#pragma unroll
-            for (int q = 0; q < W; ++q)
-                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(word(i, q)), "r"(0) : "memory");
-        slot = 0;
-    }
-    template <class T>
-    __device__ __forceinline__ Raw8<T> chunk(int i) const
-    {
-        Raw8<T> r;
-#pragma unroll
-        for (int q = 0; q < W; ++q) {
-            const Words<4> v = read(i, q);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) r.w.w[4 * q + k] = v.w[k];
-        }
-        return r;
-    }
-    // Start the copies of a row's chunks of this thread: elements of T.
-    template <class T>
-    __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&mask)[C])
+    __device__ __forceinline__ uint32_t word(int n) const { return at + (uint32_t)n * 16 * blockDim.x; }
+    // Start the copies of a row's elements of T from this thread's columns.
+    __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&col)[C], const uint32_t (&mask)[C])
     {
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
             for (int q = 0; q < W; ++q)
-                copy16(i, q, (const char*)(row + ((int64_t)i * blockDim.x + threadIdx.x) * 8) + 16 * q, mask[i] != 0);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             ::"r"(word(i * W + q)), "l"(row + col[i] + 32 * G * q), "r"(mask[i] >> q & 1 ? 16 : 0)
+                             : "memory");
+    }
+    // The same of a checkpoint's codes: one word of 8, or two of 4 bytes.
+    __device__ __forceinline__ void copy_codes(const int8_t* row, const uint32_t (&col)[C], const uint32_t (&mask)[C])
+    {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int q = 0; q < W; ++q)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
+                             ::"r"(word(i * W + q)), "l"(row + col[i] + 32 * G * q), "r"(mask[i] >> q & 1 ? G : 0), "n"(G)
+                             : "memory");
+    }
+    // The current slot is filled (or left as it is at the end): go on.
+    __device__ __forceinline__ void next()
+    {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        at += C * W * 16 * blockDim.x;
+        at = at == end ? begin : at;
+    }
+    // Wait until the oldest item, which lies in the current slot, has landed.
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory"); }
+
+    __device__ __forceinline__ Raw8<T, G> chunk(int i) const
+    {
+        Raw8<T, G> r;
+#pragma unroll
+        for (int q = 0; q < W; ++q)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
+                         : "r"(word(i * W + q))
+                         : "memory");
+        return r;
+    }
+    __device__ __forceinline__ void codes(int i, uint32_t (&w)[2]) const
+    {
+        if constexpr (W == 1)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(word(i)) : "memory");
+        else
+#pragma unroll
+            for (int q = 0; q < W; ++q) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[q]) : "r"(word(i * W + q)) : "memory");
     }
 };
 

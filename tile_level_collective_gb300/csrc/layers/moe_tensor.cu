@@ -191,18 +191,13 @@ __device__ __forceinline__ bool epilogue_wait(Shared& sh, uint64_t* bar, uint32_
 // ---- phase 0 ----------------------------------------------------------------------
 
 template <class T>
-__device__ __forceinline__ void load_router8(const void* base, bool f32, int64_t i, float (&v)[8])
+__device__ __forceinline__ F8 load_router8(const void* base, bool f32, int64_t i)
 {
     if (f32) {
         const float4 a = *(const float4*)((const float*)base + i), b = *(const float4*)((const float*)base + i + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
-        Raw8<T> r;
-        const uint4 a = *(const uint4*)((const T*)base + i);
-        r.w.w[0] = a.x, r.w.w[1] = a.y, r.w.w[2] = a.z, r.w.w[3] = a.w;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = r.at(j);
+        return F8{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)};
     }
+    return load8<T, 8>((const T*)base + i, 0, 1).expand();
 }
 
 // Dot products of kRouterExperts experts with kRouterTokens tokens per block
@@ -216,28 +211,27 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
     const int units = (m.experts + kRouterExperts - 1) / kRouterExperts * groups;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const int e0 = u / groups * kRouterExperts, t0 = u % groups * kRouterTokens;
-        float sum[kRouterExperts][kRouterTokens] = {};
+        Pair sum[kRouterExperts][kRouterTokens] = {};
         for (int64_t i = threadIdx.x * 8; i < m.hidden; i += kThreads * 8) {
-            float r[kRouterExperts][8];
+            F8 r[kRouterExperts];
 #pragma unroll
             for (int e = 0; e < kRouterExperts; ++e)
-                load_router8<T>(m.router, m.router_f32, (int64_t)min(e0 + e, m.experts - 1) * m.hidden + i, r[e]);
+                r[e] = load_router8<T>(m.router, m.router_f32, (int64_t)min(e0 + e, m.experts - 1) * m.hidden + i);
 #pragma unroll
             for (int t = 0; t < kRouterTokens; ++t) {
                 if (t0 + t >= m.tokens) break;
-                float x[8];
-                load_router8<T>(m.x, false, (t0 + t) * m.ld_x + i, x);
+                const F8 x = load_router8<T>(m.x, false, (t0 + t) * m.ld_x + i);
 #pragma unroll
                 for (int e = 0; e < kRouterExperts; ++e)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) sum[e][t] += r[e][j] * x[j];
+                    for (int j = 0; j < 4; ++j) sum[e][t] = fma2(r[e].p[j], x.p[j], sum[e][t]);
             }
         }
 #pragma unroll
         for (int e = 0; e < kRouterExperts; ++e)
 #pragma unroll
             for (int t = 0; t < kRouterTokens; ++t) {
-                const float v = warp_sum(sum[e][t]);
+                const float v = warp_sum(sum_of(sum[e][t]));
                 if (lane == 0) sh.dots[warp][e * kRouterTokens + t] = v;
             }
         __syncthreads();
