@@ -19,7 +19,7 @@ namespace {
 template <class T>
 __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
 {
-    if (!k.gate) return 1.0f;
+    if (!k.gate || k.gate_cs) return 1.0f;
     return k.param_f32 ? ((const float*)k.gate)[row * k.gate_rs] : to_f32(((const T*)k.gate)[row * k.gate_rs]);
 }
 
@@ -45,12 +45,12 @@ template <class T, int G, int C, bool KEEP>
 __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 (&a)[C], const Raw8<T, G> (&x)[C],
                                            const uint32_t (&col)[C], const uint32_t (&mask)[C],
                                            const F8 (&gw)[KEEP ? C : 1], const F8 (&wpre)[KEEP ? C : 1],
-                                           float (*slots)[32], int& turn)
+                                           float gate, SumSlots<1>& sums)
 {
     const NormCommon& k = p.c;
     const Ckpt bc{p.block_ckpt.codes, p.block_ckpt.exps, p.block_ckpt.ld_codes, p.block_ckpt.ld_exps};
     const Ckpt sc{p.stream_ckpt.codes, p.stream_ckpt.exps, p.stream_ckpt.ld_codes, p.stream_ckpt.ld_exps};
-    const float row_gate = k.gate_cs ? 1.0f : k.branch_scale * gate_of_row<T>(k, row);
+    const float row_gate = k.gate_cs ? 1.0f : k.branch_scale * gate;
     float ra = 1.0f;
     if (k.post_norm) {
         Pair sum = 0;
@@ -59,8 +59,7 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
 #pragma unroll
             for (int j = 0; j < 4; ++j) sum = fma2(a[i].p[j], a[i].p[j], sum);
         float total[1] = {sum_of(sum)};
-        block_sum(total, slots[turn]);
-        turn ^= 1;
+        sums.sum(total);
         ra = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     }
     const Pair scale = both(ra * row_gate), keep = both(k.residual_scale);
@@ -87,8 +86,7 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
         for (int i = 0; i < C; ++i) ckpt_store8<G>(sc, row, col[i], mask[i], s[i].expand());
     if (!p.normed && !p.rstd) return;
     float total[1] = {sum_of(sq)};
-    block_sum(total, slots[turn]);
-    turn ^= 1;
+    sums.sum(total);
     const float r = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     if (p.rstd && threadIdx.x == 0) {
         p.rstd[row] = ra;
@@ -114,8 +112,8 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     constexpr int G = kVector<T>;
     pdl_enter();
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float slots[2][32];
-    int turn = 0;                           // block_sum's slots in turn
+    __shared__ __align__(16) float slots[2 * 32];
+    SumSlots<1> sums(slots);
     const NormCommon& k = p.c;
     Queue<T, C, K> queue(smem);
     uint32_t col[C], mask[C];
@@ -126,13 +124,21 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
         mask[i] = runs_below<G>(col[i], k.cols);
     }
     // the item to copy next: source `src` (nparts: the residual) of row `ahead`
-    int64_t ahead = blockIdx.x;
+    int64_t ahead = blockIdx.x, part_at = ahead * p.ld_part;
+    const T* x_row = (const T*)p.x + ahead * p.ld_x;
     int src = 0;
     auto push = [&] {
         if (ahead < k.rows) {
-            const T* row = src < p.nparts ? (const T*)p.part[src] + ahead * p.ld_part : (const T*)p.x + ahead * p.ld_x;
-            queue.copy_row(row, col, mask);
-            if (++src > p.nparts) src = 0, ahead += gridDim.x;
+            if (src < p.nparts) {
+                queue.copy_row((const T*)p.part[src] + part_at, col, mask);
+                ++src;
+            } else {
+                queue.copy_row(x_row, col, mask);
+                src = 0;
+                ahead += gridDim.x;
+                part_at += gridDim.x * p.ld_part;
+                x_row += gridDim.x * p.ld_x;
+            }
         }
         queue.next();
     };
@@ -144,7 +150,10 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
             gw[i] = column_factor<T, G>(k, 0, col[i], mask[i]);
             wpre[i] = load_param8<T, G>(k.pre_weight, k.param_f32, col[i], mask[i]);
         }
+    // the row's gate (where it is one number), read a row before its use
+    float gate = gate_of_row<T>(k, blockIdx.x);
     for (int64_t row = blockIdx.x; row < k.rows; row += gridDim.x) {
+        const float next_gate = row + gridDim.x < k.rows ? gate_of_row<T>(k, row + gridDim.x) : 0.0f;
         F8 a[C];
         Raw8<T, G> x[C];
         queue.wait();
@@ -165,7 +174,8 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
 #pragma unroll
         for (int i = 0; i < C; ++i) x[i] = queue.chunk(i);
         push();
-        finish_row<T, G, C, KEEP>(p, row, a, x, col, mask, gw, wpre, slots, turn);
+        finish_row<T, G, C, KEEP>(p, row, a, x, col, mask, gw, wpre, gate, sums);
+        gate = next_gate;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -175,8 +185,8 @@ template <class T, int C>
 __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_kernel(const NormParams p)
 {
     pdl_enter();
-    __shared__ float slots[2][32];
-    int turn = 0;
+    __shared__ __align__(16) float slots[2 * 32];
+    SumSlots<1> sums(slots);
     const NormCommon& k = p.c;
     uint32_t col[C], mask[C];
 #pragma unroll
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_kernel(const N
             }
         }
         const F8 none[1] = {};
-        finish_row<T, 1, C, false>(p, row, a, x, col, mask, none, none, slots, turn);
+        finish_row<T, 1, C, false>(p, row, a, x, col, mask, none, none, gate_of_row<T>(k, row), sums);
     }
 }
 

@@ -3,8 +3,12 @@
 // With st = s * r, ah = a * ra, and gw the columns' factor (the weight of the
 // norm after the block, times branch_scale and the gate where that varies
 // along the columns; F is the rest, one number for the row):
-//   ds = du + r * (wpre * dy - st * mean(wpre * dy * st));  d_residual = residual_scale * ds
+//   ds = v - r * m * st,  v = du + r * wpre * dy,  m = mean(wpre * dy * st)
+//   d_residual = residual_scale * ds
 //   t = gw * ds;  d_block = ra * F * (t - ah * mean(t * ah))
+// The second mean is mean(gw * ah * v) - r * m * mean(gw * ah * st), so one
+// block-wide exchange of three sums serves both (with two, one after the
+// other, 8192 x 4096 from checkpoints took 81 us, and 16384 x 8192 274).
 // The weights' and the gate's gradients need two sums over the rows for each
 // column: of dy * st, and Q of ds * ah (times the gate where it varies by
 // row), from which d_post_weight and the gate's gradient follow.
@@ -25,7 +29,7 @@ namespace {
 template <class T>
 __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
 {
-    if (!k.gate) return 1.0f;
+    if (!k.gate || k.gate_cs) return 1.0f;
     return k.param_f32 ? ((const float*)k.gate)[row * k.gate_rs] : to_f32(((const T*)k.gate)[row * k.gate_rs]);
 }
 
@@ -85,123 +89,126 @@ struct Columns {
     }
 };
 
-// One row. The loader gives, chunk by chunk and in this order: the stream
-// times a factor, dy, du (if p.du), the block output times a factor.
-template <class T, int G, int C, bool KEEP, class Loader>
+// What a row has one of: its statistics, and the gate where it is one number.
+struct RowScalars {
+    float ra, r, gate;
+};
+
+// One row. The loader gives, in this order: what the row has one of, and chunk
+// by chunk the stream times a factor, dy, du (if p.du), the block output times
+// a factor. ELEMENT: the gate varies along both axes.
+template <class T, int G, int C, bool KEEP, bool ELEMENT, class Loader>
 __device__ __forceinline__ void back_row(const NormBackParams& p, int64_t row, Loader& in,
                                          const Columns<T, G, C, KEEP>& cols, F8 (&sum_pre)[C], F8 (&sum_q)[C],
-                                         float& sum_scalar, float (*slots)[32], int& turn)
+                                         float& sum_scalar, SumSlots<3>& sums)
 {
     const NormCommon& k = p.c;
     const uint32_t (&col)[C] = cols.col;
     const uint32_t (&mask)[C] = cols.mask;
-    const float ra = k.post_norm ? p.rstd[row] : 1.0f, r = p.rstd[k.rows + row];
-    const bool by_column = k.gate_cs != 0, by_element = by_column && k.gate_rs != 0;
-    const float g_row = by_column ? 1.0f : gate_of_row<T>(k, row);
-    F8 st[C], up[C];
-    Pair dot = 0;
-    in.begin_stream();
+    const RowScalars at = in.begin_row(row);
+    F8 st[C], v[C], ah[C];
+    Pair s1 = 0, s2 = 0, s3 = 0;
 #pragma unroll
-    for (int i = 0; i < C; ++i) st[i] = in.stream(i, r);
-    in.end();
-    in.begin_matrix(p.dy, p.ld_dy);
+    for (int i = 0; i < C; ++i) st[i] = in.stream(i, at.r);
+    in.end_stream();
+    in.begin_dy();
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const F8 dy = in.matrix(i).expand(), w = cols.pre(i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            up[i].p[j] = mul2(w.p[j], dy.p[j]);
+            v[i].p[j] = mul2(w.p[j], dy.p[j]);
             sum_pre[i].p[j] = fma2(dy.p[j], st[i].p[j], sum_pre[i].p[j]);
-            dot = fma2(up[i].p[j], st[i].p[j], dot);
+            s1 = fma2(v[i].p[j], st[i].p[j], s1);
         }
     }
-    in.end();
-    float total[1] = {sum_of(dot)};
-    block_sum(total, slots[turn]);
-    turn ^= 1;
-    // up becomes ds
-    const Pair m = both(-total[0] * k.inv_cols), r2 = both(r);
+    in.end_dy();
+    in.begin_du();
+    const Pair r2 = both(at.r);
     if (p.du) {
-        in.begin_matrix(p.du, p.ld_du);
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const F8 du = in.matrix(i).expand();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) up[i].p[j] = fma2(r2, fma2(m, st[i].p[j], up[i].p[j]), du.p[j]);
+            for (int j = 0; j < 4; ++j) v[i].p[j] = fma2(r2, v[i].p[j], du.p[j]);
         }
-        in.end();
     } else {
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) up[i].p[j] = mul2(r2, fma2(m, st[i].p[j], up[i].p[j]));
+            for (int j = 0; j < 4; ++j) v[i].p[j] = mul2(r2, v[i].p[j]);
     }
-    // st becomes ah
+    in.end_du();
     in.begin_block();
 #pragma unroll
-    for (int i = 0; i < C; ++i) st[i] = in.block(i, ra);
-    in.end();
-    const bool q_scaled = !by_column && k.gate_rs;       // a gate that varies by row goes into Q
-    dot = 0;
+    for (int i = 0; i < C; ++i) ah[i] = in.block(i, at.ra);
+    in.end_block();
+    F8 g[ELEMENT ? C : 1];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        F8 w;
+        F8 w = cols.factor(i);
+        if constexpr (ELEMENT) {
+            g[i] = gate8<T, G>(k, row, col[i], mask[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w.p[j] = mul2(both(k.residual_scale), up[i].p[j]);
-        store8<T, G>((T*)p.d_residual + row * p.ld_dres, col[i], mask[i], w);
-        w = cols.factor(i);
-        if (by_element) {
-            const F8 g = gate8<T, G>(k, row, col[i], mask[i]);
-            if (p.gate_kind == kGateElement) {
-                F8 d;
+            for (int j = 0; j < 4; ++j) w.p[j] = mul2(w.p[j], mul2(both(k.branch_scale), g[i].p[j]));
+        }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    d.p[j] = mul2(both(k.branch_scale), mul2(up[i].p[j], mul2(st[i].p[j], w.p[j])));
+        for (int j = 0; j < 4; ++j) {
+            const Pair wa = mul2(w.p[j], ah[i].p[j]);
+            s2 = fma2(wa, v[i].p[j], s2);
+            s3 = fma2(wa, st[i].p[j], s3);
+        }
+    }
+    float total[3] = {sum_of(s1), sum_of(s2), sum_of(s3)};
+    sums.sum(total);
+    const float rm = at.r * (total[0] * k.inv_cols);
+    const float dot = total[1] - rm * total[2];             // of gw * ds and ah
+    if (p.gate_kind == kGateToken || p.gate_kind == kGateScalar) {
+        const float d = k.branch_scale * dot;
+        if (p.gate_kind == kGateToken && threadIdx.x == 0) p.d_gate[row] = d;
+        sum_scalar += d;
+    }
+    const bool by_column = k.gate_cs != 0;
+    const bool q_scaled = !by_column && k.gate_rs;          // a gate that varies by row goes into Q
+    const Pair m1 = both(-rm), m2 = both(k.post_norm ? -dot * k.inv_cols : 0.0f);
+    const Pair f = both(at.ra * (by_column ? 1.0f : k.branch_scale * at.gate)), keep = both(k.residual_scale);
+    T* d_residual = (T*)p.d_residual + row * p.ld_dres;
+    T* d_block = (T*)p.d_block + row * p.ld_dblk;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        F8 out, w = cols.factor(i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[i].p[j] = fma2(m1, st[i].p[j], v[i].p[j]);    // ds
+            out.p[j] = mul2(keep, v[i].p[j]);
+        }
+        store8<T, G>(d_residual, col[i], mask[i], out);
+        if constexpr (ELEMENT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float e[2];
+                const Pair d = mul2(both(k.branch_scale), mul2(v[i].p[j / 2], mul2(ah[i].p[j / 2], w.p[j / 2])));
+                split(d, e[0], e[1]);
                 // packed rows of floats, whose alignment follows the number of columns
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float v[2];
-                    split(d.p[j / 2], v[0], v[1]);
-                    if (mask[i] >> (j / G) & 1) p.d_gate[row * k.cols + col[i] + j / G * 32 * G + j % G] = v[j & 1];
-                }
+                if (p.gate_kind == kGateElement && (mask[i] >> (j / G) & 1))
+                    p.d_gate[row * k.cols + col[i] + j / G * 32 * G + j % G] = e[j & 1];
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                sum_q[i].p[j] = fma2(mul2(g.p[j], up[i].p[j]), st[i].p[j], sum_q[i].p[j]);
-                w.p[j] = mul2(w.p[j], mul2(both(k.branch_scale), g.p[j]));
+                sum_q[i].p[j] = fma2(mul2(g[i].p[j], v[i].p[j]), ah[i].p[j], sum_q[i].p[j]);
+                w.p[j] = mul2(w.p[j], mul2(both(k.branch_scale), g[i].p[j]));
             }
         } else if (q_scaled) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                sum_q[i].p[j] = fma2(mul2(both(g_row), up[i].p[j]), st[i].p[j], sum_q[i].p[j]);
+                sum_q[i].p[j] = fma2(mul2(both(at.gate), v[i].p[j]), ah[i].p[j], sum_q[i].p[j]);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum_q[i].p[j] = fma2(up[i].p[j], st[i].p[j], sum_q[i].p[j]);
+            for (int j = 0; j < 4; ++j) sum_q[i].p[j] = fma2(v[i].p[j], ah[i].p[j], sum_q[i].p[j]);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            up[i].p[j] = mul2(up[i].p[j], w.p[j]);
-            dot = fma2(up[i].p[j], st[i].p[j], dot);
-        }
-    }
-    total[0] = sum_of(dot);
-    const bool row_gate = p.gate_kind == kGateToken || p.gate_kind == kGateScalar;
-    if (k.post_norm || row_gate) {
-        block_sum(total, slots[turn]);
-        turn ^= 1;
-    }
-    if (row_gate) {
-        const float d = k.branch_scale * total[0];
-        if (p.gate_kind == kGateToken && threadIdx.x == 0) p.d_gate[row] = d;
-        sum_scalar += d;
-    }
-    const Pair m2 = both(k.post_norm ? -total[0] * k.inv_cols : 0.0f);
-    const Pair f = both(ra * (by_column ? 1.0f : k.branch_scale * g_row));
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) up[i].p[j] = mul2(f, fma2(m2, st[i].p[j], up[i].p[j]));
-        store8<T, G>((T*)p.d_block + row * p.ld_dblk, col[i], mask[i], up[i]);
+        for (int j = 0; j < 4; ++j) out.p[j] = mul2(f, fma2(m2, ah[i].p[j], mul2(w.p[j], v[i].p[j])));
+        store8<T, G>(d_block, col[i], mask[i], out);
     }
 }
 
@@ -228,108 +235,197 @@ __device__ __forceinline__ void store_sums(const NormBackParams& p, const uint32
     if (p.gate_kind == kGateScalar && threadIdx.x == 0) p.partial[2 * plane + blockIdx.x] = sum_scalar;
 }
 
-// Chunks from the thread's queue, in the order of the items: stream, dy, du, block.
-template <class T, int C, int K>
+// What rows have one of, and the scales of the checkpoints' blocks, of
+// kHeaderRows rows of this block at a time, in shared memory. Loaded for each
+// row into registers they cost more, even a row ahead of their use: a warp has
+// few counters for its loads, and shared-memory reads that follow a load wait
+// for it too (8192 x 4096 from checkpoints: 93 us so, 81 in batches). A scale
+// is a power of two (or NaN): the upper half of its binary32 form.
+constexpr int kHeaderRows = 16;
+
+struct Header {
+    float* values;                          // [3][kHeaderRows]: r, ra, gate
+    uint16_t* scales;                       // [2][kHeaderRows][blocks]: the stream's, the block output's
+    int blocks, turn;
+
+    static constexpr size_t size(int64_t cols)
+    {
+        return 3 * kHeaderRows * 4 + (4 * kHeaderRows * (size_t)((cols + 31) / 32) + 15) / 16 * 16;
+    }
+    __device__ __forceinline__ Header(const NormCommon& k, unsigned char* smem)
+        : values((float*)smem), scales((uint16_t*)(smem + 3 * kHeaderRows * 4)), blocks((int)((k.cols + 31) >> 5)),
+          turn(kHeaderRows - 1)
+    {
+    }
+    // Go on to `row`, the next one of this block.
+    template <class T, bool CKPT>
+    __device__ __forceinline__ void advance(const NormBackParams& p, int64_t row)
+    {
+        if (++turn < kHeaderRows) return;
+        turn = 0;
+        __syncthreads();                    // the rows before are done with theirs
+        const int64_t left = (p.c.rows - 1 - row) / gridDim.x + 1;
+        const uint32_t rows = left < kHeaderRows ? (uint32_t)left : kHeaderRows;
+        for (uint32_t n = threadIdx.x; n < 3 * kHeaderRows; n += blockDim.x) {
+            const int64_t r = row + (int64_t)(n % kHeaderRows) * gridDim.x;
+            if (n % kHeaderRows < rows)
+                values[n] = n < kHeaderRows ? p.rstd[p.c.rows + r]
+                          : n < 2 * kHeaderRows ? (p.c.post_norm ? p.rstd[r] : 1.0f) : gate_of_row<T>(p.c, r);
+        }
+        if constexpr (CKPT) {
+            load_scales(0, p.stream_ckpt, row, rows);
+            load_scales(1, p.block_ckpt, row, rows);
+        }
+        __syncthreads();
+    }
+    // Several loads in flight per thread.
+    __device__ __forceinline__ void load_scales(int which, const ptoc_ckpt8& k, int64_t row, uint32_t rows)
+    {
+        constexpr int kAtOnce = 8;
+        uint16_t* to = scales + which * kHeaderRows * blocks;
+        for (uint32_t n0 = threadIdx.x; n0 < rows * blocks; n0 += kAtOnce * blockDim.x) {
+            uint32_t byte[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const uint32_t n = n0 + q * blockDim.x, i = n / (uint32_t)blocks;
+                byte[q] = n < rows * blocks ? k.exps[(row + (int64_t)i * gridDim.x) * k.ld_exps + (n - i * blocks)] : 0;
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q)
+                if (n0 + q * blockDim.x < rows * blocks)
+                    to[n0 + q * blockDim.x] = (uint16_t)(__float_as_uint(ckpt_scale(byte[q])) >> 16);
+        }
+    }
+    __device__ __forceinline__ RowScalars scalars() const
+    {
+        return RowScalars{values[kHeaderRows + turn], values[turn], values[2 * kHeaderRows + turn]};
+    }
+    __device__ __forceinline__ float scale(int which, uint32_t b) const
+    {
+        return __uint_as_float((uint32_t)scales[(which * kHeaderRows + turn) * blocks + b] << 16);
+    }
+};
+
+// Chunks from the thread's queue. A row has four items: stream, dy, du (empty
+// without du) and block. The queue holds kRows rows of them, so the slot that
+// an item leaves is filled with the same item of the row kRows turns later.
+// CKPT: stream and block are checkpoints; else both are matrices.
+template <class T, int C, int kRows, bool CKPT>
 struct QueueLoader {
-    static constexpr int G = kVector<T>;
+    static constexpr int G = kVector<T>, kRuns = 8 / G;
     const NormBackParams& p;
-    Queue<T, C, K> queue;
+    Queue<T, C, 4 * kRows> queue;
     const uint32_t (&col)[C];
     const uint32_t (&mask)[C];
-    int64_t ahead;                          // the row of the item to copy next
-    int item;
-    static constexpr int kRuns = 8 / G;
-    uint32_t s_exp[C * kRuns], a_exp[C * kRuns], s_next[C * kRuns], a_next[C * kRuns];   // exponent bytes of this row and the next
+    int64_t ahead;                          // the row whose items are copied next
+    const char *stream_row, *dy_row, *du_row, *block_row;               // in that row
+    Header head;
 
-    __device__ __forceinline__ QueueLoader(const NormBackParams& q, void* smem, const uint32_t (&c)[C],
+    __device__ __forceinline__ QueueLoader(const NormBackParams& q, unsigned char* smem, const uint32_t (&c)[C],
                                            const uint32_t (&m)[C])
-        : p(q), queue(smem), col(c), mask(m), ahead(blockIdx.x), item(0)
+        : p(q), queue(smem), col(c), mask(m), ahead(blockIdx.x),
+          head(q.c, smem + (size_t)blockDim.x * 4 * kRows * C * 8 * sizeof(T))
     {
+        const int64_t row = blockIdx.x;
+        stream_row = CKPT ? (const char*)(p.stream_ckpt.codes + row * p.stream_ckpt.ld_codes)
+                          : (const char*)((const T*)p.stream + row * p.ld_stream);
+        block_row = CKPT ? (const char*)(p.block_ckpt.codes + row * p.block_ckpt.ld_codes)
+                         : (const char*)((const T*)p.block + row * p.ld_block);
+        dy_row = (const char*)((const T*)p.dy + row * p.ld_dy);
+        du_row = (const char*)((const T*)p.du + row * p.ld_du);
 #pragma unroll 1
-        for (int k = 0; k < K; ++k) push();
-        exponents(blockIdx.x);
+        for (int k = 0; k < kRows; ++k) {
+            end_stream();
+            end_dy();
+            end_du();
+            end_block();
+        }
     }
-    __device__ __forceinline__ void push()
+    __device__ __forceinline__ RowScalars begin_row(int64_t row)
+    {
+        head.template advance<T, CKPT>(p, row);
+        queue.wait();
+        return head.scalars();
+    }
+    __device__ __forceinline__ void push(const char*& at, int64_t ld)
     {
         if (ahead < p.c.rows) {
-            if (item == 0) {
-                if (p.stream) queue.copy_row((const T*)p.stream + ahead * p.ld_stream, col, mask);
-                else queue.copy_codes(p.stream_ckpt.codes + ahead * p.stream_ckpt.ld_codes, col, mask);
-            } else if (item == 1) {
-                queue.copy_row((const T*)p.dy + ahead * p.ld_dy, col, mask);
-            } else if (item == 2) {
-                queue.copy_row((const T*)p.du + ahead * p.ld_du, col, mask);
-            } else {
-                if (p.block) queue.copy_row((const T*)p.block + ahead * p.ld_block, col, mask);
-                else queue.copy_codes(p.block_ckpt.codes + ahead * p.block_ckpt.ld_codes, col, mask);
-            }
-            item += item == 1 && !p.du ? 2 : 1;
-            if (item == 4) item = 0, ahead += gridDim.x;
+            queue.copy_row((const T*)at, col, mask);
+            at += gridDim.x * ld * (int64_t)sizeof(T);
         }
         queue.next();
     }
-    // Read a row's exponent bytes, a row before their use.
-    __device__ __forceinline__ void exponents(int64_t row)
+    __device__ __forceinline__ void push_codes(const char*& at, int64_t ld)
     {
-        const bool in = row < p.c.rows;
-        const uint8_t* s = p.stream ? nullptr : p.stream_ckpt.exps + row * p.stream_ckpt.ld_exps;
-        const uint8_t* a = p.block ? nullptr : p.block_ckpt.exps + row * p.block_ckpt.ld_exps;
-#pragma unroll
-        for (int i = 0; i < C; ++i)
+        if (ahead < p.c.rows) {
+            queue.copy_codes((const int8_t*)at, col, mask);
+            at += gridDim.x * ld;
+        }
+        queue.next();
+    }
+    // An item is read: its slot takes the next of its kind.
+    __device__ __forceinline__ void end_stream()
+    {
+        if constexpr (CKPT) push_codes(stream_row, p.stream_ckpt.ld_codes);
+        else push(stream_row, p.ld_stream);
+    }
+    __device__ __forceinline__ void end_dy() { push(dy_row, p.ld_dy); }
+    __device__ __forceinline__ void end_du()
+    {
+        if (p.du) push(du_row, p.ld_du);
+        else queue.next();
+    }
+    __device__ __forceinline__ void end_block()
+    {
+        if constexpr (CKPT) push_codes(block_row, p.block_ckpt.ld_codes);
+        else push(block_row, p.ld_block);
+        ahead += gridDim.x;
+    }
+    __device__ __forceinline__ void begin_dy() { queue.wait(); }
+    __device__ __forceinline__ void begin_du() { queue.wait(); }
+    __device__ __forceinline__ void begin_block() { queue.wait(); }
+    __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i); }
+    __device__ __forceinline__ F8 saved(int i, int which, float factor) const
+    {
+        F8 f;
+        if constexpr (CKPT) {
+            uint32_t w[2];
+            queue.codes(i, w);
+            Pair scale[kRuns];
 #pragma unroll
             for (int q = 0; q < kRuns; ++q) {
-                const bool on = in && (mask[i] >> q & 1);
                 const uint32_t b = (col[i] + q * 32 * G) >> 5;
-                s_next[i * kRuns + q] = s && on ? s[b] : 0u;
-                a_next[i * kRuns + q] = a && on ? a[b] : 0u;
+                scale[q] = both(mask[i] >> q & 1 ? head.scale(which, b) * factor : 0.0f);
             }
-    }
-    __device__ __forceinline__ void row(int64_t r)
-    {
-#pragma unroll
-        for (int i = 0; i < C * kRuns; ++i) s_exp[i] = s_next[i], a_exp[i] = a_next[i];
-        exponents(r + gridDim.x);
-    }
-    __device__ __forceinline__ void begin_stream() { queue.wait(); }
-    __device__ __forceinline__ void begin_block() { queue.wait(); }
-    __device__ __forceinline__ void begin_matrix(const void*, int64_t) { queue.wait(); }
-    __device__ __forceinline__ void end() { push(); }
-    __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i); }
-    __device__ __forceinline__ F8 saved(int i, bool whole, const uint32_t* bytes, float factor) const
-    {
-        if (whole) {
-            F8 f = queue.chunk(i).expand();
+            f = code_values<G>(w, scale);
+        } else {
+            f = queue.chunk(i).expand();
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.p[j] = mul2(f.p[j], both(factor));
-            return f;
         }
-        CkptRaw<G> k;
-        queue.codes(i, k.w);
-#pragma unroll
-        for (int q = 0; q < kRuns; ++q) k.byte[q] = bytes[i * kRuns + q];
-        return ckpt_values<G>(k, factor);
+        return f;
     }
-    __device__ __forceinline__ F8 stream(int i, float f) const { return saved(i, p.stream, s_exp, f); }
-    __device__ __forceinline__ F8 block(int i, float f) const { return saved(i, p.block, a_exp, f); }
+    __device__ __forceinline__ F8 stream(int i, float f) const { return saved(i, 0, f); }
+    __device__ __forceinline__ F8 block(int i, float f) const { return saved(i, 1, f); }
 };
 
 constexpr int kQueueThreads = 512;
 
-template <class T, int K>
+template <class T, int kRows, bool CKPT>
 __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(const NormBackParams p)
 {
     constexpr int C = 2, G = kVector<T>;
     pdl_enter();
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ float slots[2][32];
-    int turn = 0;                           // block_sum's slots in turn
+    __shared__ __align__(16) float slots[2 * 3 * 32];
+    SumSlots<3> sums(slots);
     uint32_t col[C], mask[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         col[i] = first_col<G>(i);
         mask[i] = runs_below<G>(col[i], p.c.cols);
     }
-    QueueLoader<T, C, K> in(p, smem + (size_t)blockDim.x * C * 2 * 32, col, mask);
+    QueueLoader<T, C, kRows, CKPT> in(p, smem + (size_t)blockDim.x * C * 2 * 32, col, mask);
     const Columns<T, G, C, true> cols{p.c, col, mask, (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16};
     const Columns<T, G, C, false> memory{p.c, col, mask, 0};
 #pragma unroll
@@ -340,8 +436,7 @@ __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(cons
     F8 sum_pre[C] = {}, sum_q[C] = {};
     float sum_scalar = 0.0f;
     for (int64_t row = blockIdx.x; row < p.c.rows; row += gridDim.x) {
-        in.row(row);
-        back_row<T, G, C, true>(p, row, in, cols, sum_pre, sum_q, sum_scalar, slots, turn);
+        back_row<T, G, C, true, false>(p, row, in, cols, sum_pre, sum_q, sum_scalar, sums);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     store_sums<G, C>(p, col, mask, sum_pre, sum_q, sum_scalar);
@@ -357,7 +452,10 @@ struct DirectLoader {
     CkptRaw<G> codes[C];
     Raw8<T, G> whole[C];
 
-    __device__ __forceinline__ void end() {}
+    __device__ __forceinline__ void end_stream() {}
+    __device__ __forceinline__ void end_dy() {}
+    __device__ __forceinline__ void end_du() {}
+    __device__ __forceinline__ void end_block() {}
     __device__ __forceinline__ void fetch(const void* m, int64_t ld, const ptoc_ckpt8& k)
     {
         const Ckpt c{k.codes, k.exps, k.ld_codes, k.ld_exps};
@@ -366,8 +464,18 @@ struct DirectLoader {
 #pragma unroll
             for (int i = 0; i < C; ++i) codes[i] = ckpt_load8<G>(c, row, col[i], mask[i]);
     }
-    __device__ __forceinline__ void begin_stream() { fetch(p.stream, p.ld_stream, p.stream_ckpt); }
+    __device__ __forceinline__ RowScalars begin_row(int64_t)
+    {
+        fetch(p.stream, p.ld_stream, p.stream_ckpt);
+        const NormCommon& k = p.c;
+        return RowScalars{k.post_norm ? p.rstd[row] : 1.0f, p.rstd[k.rows + row], gate_of_row<T>(k, row)};
+    }
     __device__ __forceinline__ void begin_block() { fetch(p.block, p.ld_block, p.block_ckpt); }
+    __device__ __forceinline__ void begin_dy() { begin_matrix(p.dy, p.ld_dy); }
+    __device__ __forceinline__ void begin_du()
+    {
+        if (p.du) begin_matrix(p.du, p.ld_du);
+    }
     __device__ __forceinline__ void begin_matrix(const void* m, int64_t ld)
     {
 #pragma unroll
@@ -386,12 +494,12 @@ struct DirectLoader {
     __device__ __forceinline__ F8 block(int i, float f) const { return saved(i, p.block, f); }
 };
 
-template <class T, int G, int C>
+template <class T, int G, int C, bool ELEMENT>
 __global__ void __launch_bounds__(C == 2 ? 512 : 1024) norm_backward_kernel(const NormBackParams p)
 {
     pdl_enter();
-    __shared__ float slots[2][32];
-    int turn = 0;
+    __shared__ __align__(16) float slots[2 * 3 * 32];
+    SumSlots<3> sums(slots);
     uint32_t col[C], mask[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -403,20 +511,22 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) norm_backward_kernel(cons
     float sum_scalar = 0.0f;
     for (int64_t row = blockIdx.x; row < p.c.rows; row += gridDim.x) {
         DirectLoader<T, G, C> in{p, col, mask, row};
-        back_row<T, G, C, false>(p, row, in, cols, sum_pre, sum_q, sum_scalar, slots, turn);
+        back_row<T, G, C, false, ELEMENT>(p, row, in, cols, sum_pre, sum_q, sum_scalar, sums);
     }
     store_sums<G, C>(p, col, mask, sum_pre, sum_q, sum_scalar);
 }
 
-// Sums of the partial rows: a block takes 32 columns of one kind; its 8 warps
+constexpr int kSumThreads = 1024;
+
+// Sums of the partial rows: a block takes 32 columns of one kind; its 32 warps
 // each add a run of the partial rows in order, and the runs are added in
 // order. Kind 0: d_pre; 1: Q, from which d_post and the gradient of a gate of
 // columns follow; 2: the gradient of a scalar gate.
 template <class T>
-__global__ void __launch_bounds__(kBlock) norm_backward_sum_kernel(const NormBackParams p)
+__global__ void __launch_bounds__(kSumThreads) norm_backward_sum_kernel(const NormBackParams p)
 {
     pdl_enter();
-    __shared__ float runs[kBlock / 32][32];
+    __shared__ float runs[kSumThreads / 32][32];
     const NormCommon& k = p.c;
     const int64_t plane = (int64_t)p.grid * k.cols;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -429,7 +539,7 @@ __global__ void __launch_bounds__(kBlock) norm_backward_sum_kernel(const NormBac
     if (live) {
         const float* src = p.partial + kind * plane + col;
         const int64_t step = kind == 2 ? 1 : k.cols;
-        const int per = (p.grid + kBlock / 32 - 1) / (kBlock / 32);
+        const int per = (p.grid + kSumThreads / 32 - 1) / (kSumThreads / 32);
         const int end = min(p.grid, (warp + 1) * per);
 #pragma unroll 8
         for (int b = warp * per; b < end; ++b) sum += src[b * step];
@@ -439,7 +549,7 @@ __global__ void __launch_bounds__(kBlock) norm_backward_sum_kernel(const NormBac
     if (warp || !live) return;
     sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kBlock / 32; ++w) sum += runs[w][lane];
+    for (int w = 0; w < kSumThreads / 32; ++w) sum += runs[w][lane];
     auto param = [&](const void* q, int64_t i) {
         return !q ? 1.0f : k.param_f32 ? ((const float*)q)[i] : to_f32(((const T*)q)[i]);
     };
@@ -454,36 +564,56 @@ __global__ void __launch_bounds__(kBlock) norm_backward_sum_kernel(const NormBac
     }
 }
 
-// The queue form: items in flight and its rule. Two chunks per thread and 512
-// threads on an SM; wider rows leave no room for two rows of copies.
+// The queue form: rows in flight and its rule. Two chunks per thread and 512
+// threads on an SM; wider rows leave no room for a row of copies ahead.
 template <class T>
-constexpr int kItems = 8 / ((int)sizeof(T) / 2);
+constexpr int kRowsAhead = 2 / ((int)sizeof(T) / 2);
 constexpr int64_t kQueueCols = kQueueThreads * 16;
+// Shared memory of a block: the columns' parameters, the queues, the header.
+template <class T>
+constexpr size_t queue_bytes(int64_t threads, int64_t cols)
+{
+    return threads * 2 * (64 + (size_t)kRowsAhead<T> * 4 * 8 * sizeof(T)) + Header::size(cols);
+}
+
+template <class T, bool CKPT>
+cudaError_t launch_queue(const NormBackParams& p, dim3 grid, unsigned threads, cudaStream_t s)
+{
+    auto kernel = norm_backward_queue_kernel<T, kRowsAhead<T>, CKPT>;
+    const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)queue_bytes<T>(kQueueThreads, kQueueCols));
+    return e == cudaSuccess ? launch_kernel(kernel, grid, threads, queue_bytes<T>(threads, p.c.cols), s, p) : e;
+}
+
+template <class T, int G, int C>
+cudaError_t launch_direct(const NormBackParams& p, dim3 grid, unsigned threads, cudaStream_t s)
+{
+    return p.c.gate_cs && p.c.gate_rs ? launch_kernel(norm_backward_kernel<T, G, C, true>, grid, threads, 0, s, p)
+                                      : launch_kernel(norm_backward_kernel<T, G, C, false>, grid, threads, 0, s, p);
+}
 
 template <class T>
 cudaError_t launch(const NormBackParams& p, cudaStream_t s)
 {
     const dim3 grid((unsigned)p.grid);
     const int64_t groups = (p.c.cols + 255) / 256;
+    const unsigned by2 = (unsigned)((groups + 1) / 2) * 32, by4 = (unsigned)((groups + 3) / 4) * 32;
+    // The queue takes aligned rows of up to kQueueCols columns, a gate that is
+    // none or varies along one axis, and two checkpoints or none.
+    const bool element = p.c.gate_cs && p.c.gate_rs, mixed = !p.stream != !p.block;
     cudaError_t e;
-    if (p.c.vec && p.c.cols <= kQueueCols) {
-        const unsigned threads = (unsigned)((groups + 1) / 2) * 32;
-        const size_t per_thread = 2 * (2 * 32 + (size_t)kItems<T> * sizeof(T) * 8);
-        auto kernel = norm_backward_queue_kernel<T, kItems<T>>;
-        e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(per_thread * kQueueThreads));
-        if (e == cudaSuccess) e = launch_kernel(kernel, grid, threads, per_thread * threads, s, p);
-    } else if (p.c.vec) {
-        e = launch_kernel(norm_backward_kernel<T, kVector<T>, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
-    } else if (p.c.cols <= kQueueCols) {
-        e = launch_kernel(norm_backward_kernel<T, 1, 2>, grid, (unsigned)((groups + 1) / 2) * 32, 0, s, p);
-    } else {
-        e = launch_kernel(norm_backward_kernel<T, 1, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);
-    }
+    if (p.c.cols > kQueueCols)
+        e = p.c.vec ? launch_direct<T, kVector<T>, 4>(p, grid, by4, s) : launch_direct<T, 1, 4>(p, grid, by4, s);
+    else if (!p.c.vec)
+        e = launch_direct<T, 1, 2>(p, grid, by2, s);
+    else if (element || mixed)
+        e = launch_direct<T, kVector<T>, 2>(p, grid, by2, s);
+    else
+        e = p.stream ? launch_queue<T, false>(p, grid, by2, s) : launch_queue<T, true>(p, grid, by2, s);
     if (e != cudaSuccess) return e;
     if (!p.d_pre && !p.need_q && p.gate_kind != kGateScalar) return cudaSuccess;
     const dim3 sums((unsigned)((p.c.cols + 31) / 32), p.gate_kind == kGateScalar ? 3 : 2);
-    return launch_kernel(norm_backward_sum_kernel<T>, sums, kBlock, 0, s, p);
+    return launch_kernel(norm_backward_sum_kernel<T>, sums, kSumThreads, 0, s, p);
 }
 
 }  // namespace
@@ -495,7 +625,8 @@ int norm_backward_grid(int64_t rows, int64_t cols)
 {
     constexpr int kSms = 152;
     const int64_t threads = (cols + 511) / 512 * 32;
-    const int64_t per_sm = threads >= 512 ? 1 : 512 / threads < 16 ? 512 / threads : 16;
+    // (of few threads, as many as their shared memory leaves room for)
+    const int64_t per_sm = threads >= 512 ? 1 : 512 / threads < 12 ? 512 / threads : 12;
     const int64_t most = (int64_t)kSms * per_sm;
     return (int)(rows < most ? rows : most);
 }

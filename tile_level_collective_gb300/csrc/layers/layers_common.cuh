@@ -145,13 +145,13 @@ __device__ __forceinline__ Raw8<T, G> load8(const T* row, uint32_t col, uint32_t
     Raw8<T, G> r;
     const T* p = row + col;
     if constexpr (G == 1) {
+        using Word = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+        if (mask == 0xffu) {                // all but the row's last chunks
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            r.w[j] = 0;
-            if (mask >> j & 1) {
-                if constexpr (sizeof(T) == 4) r.w[j] = *(const uint32_t*)(p + 32 * j);
-                else r.w[j] = *(const uint16_t*)(p + 32 * j);
-            }
+            for (int j = 0; j < 8; ++j) r.w[j] = *(const Word*)(p + 32 * j);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r.w[j] = mask >> j & 1 ? *(const Word*)(p + 32 * j) : 0u;
         }
     } else {
 #pragma unroll
@@ -199,12 +199,15 @@ __device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, cons
 {
     T* p = row + col;
     if constexpr (G == 1) {
+        using Word = std::conditional_t<sizeof(T) == 4, uint32_t, uint16_t>;
+        if (mask == 0xffu) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (mask >> j & 1) {
-                if constexpr (sizeof(T) == 4) *(uint32_t*)(p + 32 * j) = r.w[j];
-                else *(uint16_t*)(p + 32 * j) = (uint16_t)r.w[j];
-            }
+            for (int j = 0; j < 8; ++j) *(Word*)(p + 32 * j) = (Word)r.w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (mask >> j & 1) *(Word*)(p + 32 * j) = (Word)r.w[j];
+        }
     } else {
 #pragma unroll
         for (int q = 0; q < 8 / G; ++q)
@@ -246,8 +249,9 @@ __device__ __forceinline__ F8 load_param8(const void* base, bool f32, uint32_t c
 // ---- block-wide sums ---------------------------------------------------------------
 
 // Sums of N values over the block, the same bits in every thread: lanes by a
-// fixed exchange tree, then the warps' sums in order. `slot` is shared memory
-// of N * 32 floats; two calls in a row need two slots (one barrier per call).
+// fixed exchange tree, then the warps' sums by one. `slot` is shared memory of
+// N * 32 floats that held zeros before the first call; two calls in a row need
+// two slots (one barrier per call).
 template <int N>
 __device__ __forceinline__ void block_sum(float (&v)[N], float* slot)
 {
@@ -255,20 +259,40 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float* slot)
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    const int warps = (int)blockDim.x >> 5;
-    if (warps == 1) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0)
+    if (blockDim.x == 32) return;
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-        for (int k = 0; k < N; ++k) slot[k * 32 + warp] = v[k];
+        for (int k = 0; k < N; ++k) slot[32 * k + (threadIdx.x >> 5)] = v[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        v[k] = lane < warps ? slot[k * 32 + lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        const float4* w = (const float4*)(slot + 32 * k);
+        auto four = [&](int i) {
+            const float4 q = w[i];
+            return (q.x + q.y) + (q.z + q.w);
+        };
+        v[k] = four(0) + four(1);
+        if (blockDim.x > 256) v[k] += four(2) + four(3);
+        if (blockDim.x > 512) v[k] += (four(4) + four(5)) + (four(6) + four(7));
     }
 }
+
+// The two slots that calls of block_sum take in turn.
+template <int N>
+struct SumSlots {
+    float* slot;                            // 2 * N * 32 floats
+    int turn = 0;
+    __device__ __forceinline__ explicit SumSlots(float* s) : slot(s)
+    {
+        for (int i = threadIdx.x; i < 2 * N * 32; i += blockDim.x) s[i] = 0.0f;
+        __syncthreads();
+    }
+    __device__ __forceinline__ void sum(float (&v)[N])
+    {
+        block_sum(v, slot + turn * N * 32);
+        turn ^= 1;
+    }
+};
 
 // ---- the 8-bit checkpoint code -------------------------------------------------------
 // The shared exponent byte from the bits of the block's largest |x|: 127 is
@@ -354,14 +378,21 @@ __device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, uint32_t
     } else {
         // lane j keeps the byte of element j's block and stores it
         const uint32_t lane = threadIdx.x & 31;
-        uint32_t keep = 0;
+        uint32_t keep = 0, code[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu);
             const uint32_t byte = ckpt_exponent(top);
-            const uint32_t code = byte == 255u ? 0u : __float_as_uint(__fmaf_rn(v[j], ckpt_inverse(byte), kCodeBias));
-            if (mask >> j & 1) codes[32 * j] = (int8_t)code;
+            code[j] = byte == 255u ? 0u : __float_as_uint(__fmaf_rn(v[j], ckpt_inverse(byte), kCodeBias));
             if (lane == j) keep = byte;
+        }
+        if (mask == 0xffu) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) codes[32 * j] = (int8_t)code[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (mask >> j & 1) codes[32 * j] = (int8_t)code[j];
         }
         const uint32_t any = __shfl_sync(0xffffffffu, mask, 0);        // a block exists where its first column does
         if (lane < 8 && (any >> lane & 1)) exps[((col - lane) >> 5) + lane] = (uint8_t)keep;
@@ -386,6 +417,9 @@ __device__ __forceinline__ CkptRaw<G> ckpt_load8(const Ckpt& k, int64_t row, uin
         uint2 w = make_uint2(0, 0);
         if (mask) w = *(const uint2*)codes;
         r.w[0] = w.x, r.w[1] = w.y;
+    } else if (G == 1 && mask == 0xffu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r.w[j] = *(const uint8_t*)(codes + 32 * j);
     } else {
 #pragma unroll
         for (int j = 0; j < 8 / G; ++j) {
@@ -414,13 +448,28 @@ __device__ __forceinline__ float code_float(uint32_t flipped, int byte)
     return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7650 + byte));
 }
 
+// Code words as values, run q times scale[q].
+template <int G>
+__device__ __forceinline__ F8 code_values(const uint32_t (&words)[2], const Pair (&scale)[8 / G])
+{
+    F8 f;
+    const Pair bias = both(-8388736.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = words[i / 2] ^ 0x80808080u;
+        f.p[i] = mul2(add2(pair(code_float(w, 2 * (i & 1)), code_float(w, 2 * (i & 1) + 1)), bias),
+                      scale[G == 4 ? i / 2 : 0]);
+    }
+    return f;
+}
+
 // The chunk's values times `factor` (0 outside the mask, where codes are 0).
 template <int G>
 __device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
 {
-    F8 f;
-    const Pair bias = both(-8388736.0f);
     if constexpr (G == 1) {
+        F8 f;
+        const Pair bias = both(-8388736.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float lo = ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i)) * factor;
@@ -428,18 +477,13 @@ __device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
             f.p[i] = mul2(add2(pair(code_float(r.w[2 * i] ^ 0x80u, 0), code_float(r.w[2 * i + 1] ^ 0x80u, 0)), bias),
                           pair(lo, hi));
         }
+        return f;
     } else {
         Pair scale[8 / G];
 #pragma unroll
         for (int q = 0; q < 8 / G; ++q) scale[q] = both(ckpt_scale(r.byte[q]) * factor);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t w = r.w[i / 2] ^ 0x80808080u;
-            f.p[i] = mul2(add2(pair(code_float(w, 2 * (i & 1)), code_float(w, 2 * (i & 1) + 1)), bias),
-                          scale[G == 4 ? i / 2 : 0]);
-        }
+        return code_values<G>(r.w, scale);
     }
-    return f;
 }
 
 // ---- a thread's queue of copies in shared memory ---------------------------------------
@@ -459,7 +503,7 @@ struct Queue {
         end = begin + K * C * W * 16 * blockDim.x;
     }
     __device__ __forceinline__ uint32_t word(int n) const { return at + (uint32_t)n * 16 * blockDim.x; }
-    // Start the copies of a row's elements of T from this thread's columns.
+    // Start the copies of this thread's columns of a row of T.
     __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&col)[C], const uint32_t (&mask)[C])
     {
 #pragma unroll
