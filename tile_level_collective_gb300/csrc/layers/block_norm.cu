@@ -103,19 +103,18 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
     }
 }
 
-// Rows of 16-byte aligned words, through the threads' queues of K items. KEEP:
-// the column factors stay in registers (they do not depend on the row, and two
-// chunks leave room for them).
-template <class T, int C, int K, bool KEEP>
+// Through the warps' queues of K items. KEEP: the column factors stay in
+// registers (they do not depend on the row, and two chunks leave room for them).
+template <class T, int C, int K, bool KEEP, bool ODD>
 __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(const NormParams p)
 {
-    constexpr int G = kVector<T>;
+    constexpr int G = ODD ? 1 : kVector<T>;
     pdl_enter();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ __align__(16) float slots[2 * 32];
     SumSlots<1> sums(slots);
     const NormCommon& k = p.c;
-    Queue<T, C, K> queue(smem);
+    Queue<T, C, K, ODD> queue(smem);
     uint32_t col[C], mask[C];
     F8 gw[KEEP ? C : 1], wpre[KEEP ? C : 1];
 #pragma unroll
@@ -128,12 +127,13 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     const T* x_row = (const T*)p.x + ahead * p.ld_x;
     int src = 0;
     auto push = [&] {
+        queue.done();
         if (ahead < k.rows) {
             if (src < p.nparts) {
-                queue.copy_row((const T*)p.part[src] + part_at, col, mask);
+                queue.copy_row((const T*)p.part[src] + part_at, col, mask, k.cols);
                 ++src;
             } else {
-                queue.copy_row(x_row, col, mask);
+                queue.copy_row(x_row, col, mask, k.cols);
                 src = 0;
                 ahead += gridDim.x;
                 part_at += gridDim.x * p.ld_part;
@@ -154,17 +154,20 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     float gate = gate_of_row<T>(k, blockIdx.x);
     for (int64_t row = blockIdx.x; row < k.rows; row += gridDim.x) {
         const float next_gate = row + gridDim.x < k.rows ? gate_of_row<T>(k, row + gridDim.x) : 0.0f;
+        // where the rows begin in their words
+        const uint32_t part_shift = (uint32_t)row * (uint32_t)p.ld_part * (uint32_t)sizeof(T) & 15u;
+        const uint32_t x_shift = (uint32_t)row * (uint32_t)p.ld_x * (uint32_t)sizeof(T) & 15u;
         F8 a[C];
         Raw8<T, G> x[C];
         queue.wait();
 #pragma unroll
-        for (int i = 0; i < C; ++i) a[i] = queue.chunk(i).expand();
+        for (int i = 0; i < C; ++i) a[i] = queue.chunk(i, part_shift).expand();
         push();
         for (int r = 1; r < p.nparts; ++r) {
             queue.wait();
 #pragma unroll
             for (int i = 0; i < C; ++i) {
-                const F8 w = queue.chunk(i).expand();
+                const F8 w = queue.chunk(i, part_shift).expand();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) a[i].p[j] = add2(a[i].p[j], w.p[j]);
             }
@@ -172,7 +175,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
         }
         queue.wait();
 #pragma unroll
-        for (int i = 0; i < C; ++i) x[i] = queue.chunk(i);
+        for (int i = 0; i < C; ++i) x[i] = queue.chunk(i, x_shift);
         push();
         finish_row<T, G, C, KEEP>(p, row, a, x, col, mask, gw, wpre, gate, sums);
         gate = next_gate;
@@ -180,7 +183,8 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Rows at any address: element-wide accesses, the next row's by other blocks.
+// Rows whose base is not 16-byte aligned: element-wide accesses, the next row's
+// by other blocks.
 template <class T, int C>
 __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_kernel(const NormParams p)
 {
@@ -218,33 +222,35 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_kernel(const N
     }
 }
 
-template <class T, int C, int K>
+template <class T, int C, int K, bool ODD>
 cudaError_t launch_queue(const NormParams& p, cudaStream_t s)
 {
     const int64_t groups = (p.c.cols + 255) / 256;           // warps' worth of chunks
     const unsigned threads = (unsigned)((groups + C - 1) / C) * 32;
-    const size_t smem = (size_t)K * threads * C * sizeof(T) * 8;
     // one wave: the registers and the queues of 512 threads of two chunks fill an SM
     const int64_t per_sm = C == 2 ? (512 / threads < 16 ? 512 / threads : 16) : 1;
     const int64_t most = 152 * per_sm;
     const dim3 grid((unsigned)(p.c.rows < most ? p.c.rows : most));
     const bool keep = C == 2 && !(p.c.gate_cs && p.c.gate_rs);
-    auto kernel = keep ? block_norm_queue_kernel<T, C, K, C == 2> : block_norm_queue_kernel<T, C, K, false>;
+    auto kernel = keep ? block_norm_queue_kernel<T, C, K, C == 2, ODD> : block_norm_queue_kernel<T, C, K, false, ODD>;
+    using Q = Queue<T, C, K, ODD>;
     const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)(K * (C == 2 ? 512 : 1024) * C * sizeof(T) * 8));
+                                               (int)Q::bytes(C == 2 ? 512 : 1024));
     if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, grid, threads, smem, s, p);
+    return launch_kernel(kernel, grid, threads, Q::bytes(threads), s, p);
 }
 
 template <class T>
 cudaError_t launch(const NormParams& p, cudaStream_t s)
 {
     constexpr int kItems = 12 / ((int)sizeof(T) / 2);        // 192 KiB of queues on an SM
-    if (p.c.vec) {
-        if (p.c.cols <= 8192) return launch_queue<T, 2, kItems>(p, s);
-        return launch_queue<T, 4, kItems / 4>(p, s);
-    }
     const int64_t groups = (p.c.cols + 255) / 256;
+    if (p.c.cols <= 8192) {
+        if (p.c.access == kAligned) return launch_queue<T, 2, kItems, false>(p, s);
+        if (p.c.access == kOddPitch) return launch_queue<T, 2, kItems, true>(p, s);
+    } else if (p.c.access == kAligned) {
+        return launch_queue<T, 4, kItems / 4, false>(p, s);
+    }
     const dim3 grid((unsigned)(p.c.rows < INT32_MAX ? p.c.rows : INT32_MAX));
     if (groups <= 32) return launch_kernel(block_norm_kernel<T, 2>, grid, (unsigned)((groups + 1) / 2) * 32, 0, s, p);
     return launch_kernel(block_norm_kernel<T, 4>, grid, (unsigned)((groups + 3) / 4) * 32, 0, s, p);

@@ -310,21 +310,23 @@ struct Header {
 // without du) and block. The queue holds kRows rows of them, so the slot that
 // an item leaves is filled with the same item of the row kRows turns later.
 // CKPT: stream and block are checkpoints; else both are matrices.
-template <class T, int C, int kRows, bool CKPT>
+template <class T, int C, int kRows, bool CKPT, bool ODD>
 struct QueueLoader {
-    static constexpr int G = kVector<T>, kRuns = 8 / G;
+    using Q = Queue<T, C, 4 * kRows, ODD>;
+    static constexpr int G = Q::G;
     const NormBackParams& p;
-    Queue<T, C, 4 * kRows> queue;
+    Q queue;
     const uint32_t (&col)[C];
     const uint32_t (&mask)[C];
     int64_t ahead;                          // the row whose items are copied next
     const char *stream_row, *dy_row, *du_row, *block_row;               // in that row
+    uint32_t shift;                         // where the current item's row begins in its words
+    uint32_t row;
     Header head;
 
     __device__ __forceinline__ QueueLoader(const NormBackParams& q, unsigned char* smem, const uint32_t (&c)[C],
                                            const uint32_t (&m)[C])
-        : p(q), queue(smem), col(c), mask(m), ahead(blockIdx.x),
-          head(q.c, smem + (size_t)blockDim.x * 4 * kRows * C * 8 * sizeof(T))
+        : p(q), queue(smem), col(c), mask(m), ahead(blockIdx.x), head(q.c, smem + Q::bytes(blockDim.x))
     {
         const int64_t row = blockIdx.x;
         stream_row = CKPT ? (const char*)(p.stream_ckpt.codes + row * p.stream_ckpt.ld_codes)
@@ -344,21 +346,30 @@ struct QueueLoader {
     __device__ __forceinline__ RowScalars begin_row(int64_t row)
     {
         head.template advance<T, CKPT>(p, row);
-        queue.wait();
+        this->row = (uint32_t)row;
+        begin(CKPT ? p.stream_ckpt.ld_codes : p.ld_stream, CKPT ? 1 : sizeof(T));
         return head.scalars();
+    }
+    // The next item's slot: wait for it.
+    __device__ __forceinline__ void begin(int64_t ld, uint32_t size)
+    {
+        queue.wait();
+        if constexpr (ODD) shift = row * (uint32_t)ld * size & 15u;
     }
     __device__ __forceinline__ void push(const char*& at, int64_t ld)
     {
+        queue.done();
         if (ahead < p.c.rows) {
-            queue.copy_row((const T*)at, col, mask);
+            queue.copy_row((const T*)at, col, mask, p.c.cols);
             at += gridDim.x * ld * (int64_t)sizeof(T);
         }
         queue.next();
     }
     __device__ __forceinline__ void push_codes(const char*& at, int64_t ld)
     {
+        queue.done();
         if (ahead < p.c.rows) {
-            queue.copy_codes((const int8_t*)at, col, mask);
+            queue.copy_codes((const int8_t*)at, col, mask, p.c.cols);
             at += gridDim.x * ld;
         }
         queue.next();
@@ -381,25 +392,30 @@ struct QueueLoader {
         else push(block_row, p.ld_block);
         ahead += gridDim.x;
     }
-    __device__ __forceinline__ void begin_dy() { queue.wait(); }
-    __device__ __forceinline__ void begin_du() { queue.wait(); }
-    __device__ __forceinline__ void begin_block() { queue.wait(); }
-    __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i); }
+    __device__ __forceinline__ void begin_dy() { begin(p.ld_dy, sizeof(T)); }
+    __device__ __forceinline__ void begin_du() { begin(p.ld_du, sizeof(T)); }
+    __device__ __forceinline__ void begin_block() { begin(CKPT ? p.block_ckpt.ld_codes : p.ld_block, CKPT ? 1 : sizeof(T)); }
+    __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i, shift); }
     __device__ __forceinline__ F8 saved(int i, int which, float factor) const
     {
         F8 f;
         if constexpr (CKPT) {
-            uint32_t w[2];
-            queue.codes(i, w);
-            Pair scale[kRuns];
+            uint32_t w[ODD ? 8 : 2];
+            queue.codes(i, shift, w);
+            // a block past the row's end has codes 0; its scale is not read
+            constexpr int kRuns = 8 / G;
+            float scale[kRuns];
 #pragma unroll
             for (int q = 0; q < kRuns; ++q) {
-                const uint32_t b = (col[i] + q * 32 * G) >> 5;
-                scale[q] = both(mask[i] >> q & 1 ? head.scale(which, b) * factor : 0.0f);
+                const uint32_t b = (ODD ? col[i] - queue.lane : col[i]) / 32 + q * G;
+                scale[q] = b < (uint32_t)head.blocks ? head.scale(which, b) * factor : 0.0f;
             }
-            f = code_values<G>(w, scale);
+            Pair by[ODD ? 4 : kRuns];
+#pragma unroll
+            for (int q = 0; q < (ODD ? 4 : kRuns); ++q) by[q] = ODD ? pair(scale[2 * q % kRuns], scale[(2 * q + 1) % kRuns]) : both(scale[q]);
+            f = code_values<G>(w, by);
         } else {
-            f = queue.chunk(i).expand();
+            f = queue.chunk(i, shift).expand();
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.p[j] = mul2(f.p[j], both(factor));
         }
@@ -411,10 +427,10 @@ struct QueueLoader {
 
 constexpr int kQueueThreads = 512;
 
-template <class T, int kRows, bool CKPT>
+template <class T, int kRows, bool CKPT, bool ODD>
 __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(const NormBackParams p)
 {
-    constexpr int C = 2, G = kVector<T>;
+    constexpr int C = 2, G = ODD ? 1 : kVector<T>;
     pdl_enter();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ __align__(16) float slots[2 * 3 * 32];
@@ -425,7 +441,7 @@ __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(cons
         col[i] = first_col<G>(i);
         mask[i] = runs_below<G>(col[i], p.c.cols);
     }
-    QueueLoader<T, C, kRows, CKPT> in(p, smem + (size_t)blockDim.x * C * 2 * 32, col, mask);
+    QueueLoader<T, C, kRows, CKPT, ODD> in(p, smem + (size_t)blockDim.x * C * 64, col, mask);
     const Columns<T, G, C, true> cols{p.c, col, mask, (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16};
     const Columns<T, G, C, false> memory{p.c, col, mask, 0};
 #pragma unroll
@@ -570,19 +586,19 @@ template <class T>
 constexpr int kRowsAhead = 2 / ((int)sizeof(T) / 2);
 constexpr int64_t kQueueCols = kQueueThreads * 16;
 // Shared memory of a block: the columns' parameters, the queues, the header.
-template <class T>
-constexpr size_t queue_bytes(int64_t threads, int64_t cols)
+template <class T, bool ODD>
+size_t queue_bytes(int64_t threads, int64_t cols)
 {
-    return threads * 2 * (64 + (size_t)kRowsAhead<T> * 4 * 8 * sizeof(T)) + Header::size(cols);
+    return threads * 2 * 64 + Queue<T, 2, 4 * kRowsAhead<T>, ODD>::bytes(threads) + Header::size(cols);
 }
 
-template <class T, bool CKPT>
+template <class T, bool CKPT, bool ODD>
 cudaError_t launch_queue(const NormBackParams& p, dim3 grid, unsigned threads, cudaStream_t s)
 {
-    auto kernel = norm_backward_queue_kernel<T, kRowsAhead<T>, CKPT>;
+    auto kernel = norm_backward_queue_kernel<T, kRowsAhead<T>, CKPT, ODD>;
     const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)queue_bytes<T>(kQueueThreads, kQueueCols));
-    return e == cudaSuccess ? launch_kernel(kernel, grid, threads, queue_bytes<T>(threads, p.c.cols), s, p) : e;
+                                               (int)queue_bytes<T, ODD>(kQueueThreads, kQueueCols));
+    return e == cudaSuccess ? launch_kernel(kernel, grid, threads, queue_bytes<T, ODD>(threads, p.c.cols), s, p) : e;
 }
 
 template <class T, int G, int C>
@@ -598,18 +614,21 @@ cudaError_t launch(const NormBackParams& p, cudaStream_t s)
     const dim3 grid((unsigned)p.grid);
     const int64_t groups = (p.c.cols + 255) / 256;
     const unsigned by2 = (unsigned)((groups + 1) / 2) * 32, by4 = (unsigned)((groups + 3) / 4) * 32;
-    // The queue takes aligned rows of up to kQueueCols columns, a gate that is
-    // none or varies along one axis, and two checkpoints or none.
+    // The queue takes rows of up to kQueueCols columns, a gate that is none or
+    // varies along one axis, and two checkpoints or none.
     const bool element = p.c.gate_cs && p.c.gate_rs, mixed = !p.stream != !p.block;
+    const bool vec = p.c.access == kAligned, odd = p.c.access == kOddPitch;
     cudaError_t e;
     if (p.c.cols > kQueueCols)
-        e = p.c.vec ? launch_direct<T, kVector<T>, 4>(p, grid, by4, s) : launch_direct<T, 1, 4>(p, grid, by4, s);
-    else if (!p.c.vec)
-        e = launch_direct<T, 1, 2>(p, grid, by2, s);
+        e = vec ? launch_direct<T, kVector<T>, 4>(p, grid, by4, s) : launch_direct<T, 1, 4>(p, grid, by4, s);
     else if (element || mixed)
-        e = launch_direct<T, kVector<T>, 2>(p, grid, by2, s);
+        e = vec ? launch_direct<T, kVector<T>, 2>(p, grid, by2, s) : launch_direct<T, 1, 2>(p, grid, by2, s);
+    else if (vec)
+        e = p.stream ? launch_queue<T, false, false>(p, grid, by2, s) : launch_queue<T, true, false>(p, grid, by2, s);
+    else if (odd)
+        e = p.stream ? launch_queue<T, false, true>(p, grid, by2, s) : launch_queue<T, true, true>(p, grid, by2, s);
     else
-        e = p.stream ? launch_queue<T, false>(p, grid, by2, s) : launch_queue<T, true>(p, grid, by2, s);
+        e = launch_direct<T, 1, 2>(p, grid, by2, s);
     if (e != cudaSuccess) return e;
     if (!p.d_pre && !p.need_q && p.gate_kind != kGateScalar) return cudaSuccess;
     const dim3 sums((unsigned)((p.c.cols + 31) / 32), p.gate_kind == kGateScalar ? 3 : 2);

@@ -17,6 +17,7 @@ struct Operands {
     int nw = 0, nr = 0;
     bool ok = true;               // sizes, pitches and alignments so far
     bool vec = true;              // every base and pitch allows 16-byte vectors
+    bool bases = true;            // every matrix begins at a multiple of 16 bytes
 
     void add(bool write, const void* p, int64_t bytes)
     {
@@ -33,6 +34,7 @@ struct Operands {
             return;
         }
         if (((uintptr_t)p | (uintptr_t)(rows > 1 ? ld * eb : 0)) & (uintptr_t)(word - 1)) vec = false;
+        if ((uintptr_t)p & 15u) bases = false;
         add(write, p, footprint(rows, cols, ld, eb));
     }
     void matrix(bool write, const ptoc_matrix* m, int64_t nrows, int64_t cols, int eb)
@@ -57,6 +59,10 @@ struct Operands {
         if (!aligned(p, eb)) ok = false;
         if ((uintptr_t)p & 15u) vec = false;
         add(false, p, footprint(1, n, n, eb));
+    }
+    int access(int64_t cols, int eb) const
+    {
+        return vec && cols % (16 / eb) == 0 ? kAligned : bases ? kOddPitch : kAnywhere;
     }
     ptoc_status disjoint() const { return check_disjoint_outputs(writes, nw, reads, nr); }
 };
@@ -203,6 +209,7 @@ extern "C" ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts
     for (int r = 0; r < parts->nranks; ++r) {
         if ((!parts->tensors[r] && fp > 0) || !aligned(parts->tensors[r], eb)) return PTOC_ERR_INVALID_ARG;
         if (((uintptr_t)parts->tensors[r] | (uintptr_t)(rows > 1 ? ld_parts * eb : 0)) & 15u) o.vec = false;
+        if ((uintptr_t)parts->tensors[r] & 15u) o.bases = false;
         part_reads[r] = Span{parts->tensors[r], (uintptr_t)fp};
         p.part[r] = parts->tensors[r];
     }
@@ -212,7 +219,7 @@ extern "C" ptoc_status ptoc_block_norm(const ptoc_group* parts, int64_t ld_parts
     if (st != PTOC_OK) return st;
     if (cols > PTOC_NORM_MAX_COLS) return PTOC_ERR_UNSUPPORTED;
     if (rows == 0 || cols == 0) return PTOC_OK;
-    p.c.vec = o.vec && cols % (16 / eb) == 0;
+    p.c.access = o.access(cols, eb);
     p.nparts = parts->nranks;
     p.ld_part = ld_parts;
     p.x = x->data;
@@ -295,7 +302,7 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
         if (gate_bytes && cudaMemsetAsync(d_gate, 0, gate_bytes, stream) != cudaSuccess) return PTOC_ERR_CUDA;
         return PTOC_OK;
     }
-    p.c.vec = o.vec && cols % (16 / eb) == 0;
+    p.c.access = o.access(cols, eb);
     p.block = sv.block.data;
     p.ld_block = sv.block.ld;
     p.block_ckpt = sv.block_ckpt;

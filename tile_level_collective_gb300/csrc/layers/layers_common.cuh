@@ -448,14 +448,19 @@ __device__ __forceinline__ float code_float(uint32_t flipped, int byte)
     return __uint_as_float(__byte_perm(flipped, 0x4b000000u, 0x7650 + byte));
 }
 
-// Code words as values, run q times scale[q].
+// Code words as values, run q times scale[q] (G = 1: pair q of runs).
 template <int G>
-__device__ __forceinline__ F8 code_values(const uint32_t (&words)[2], const Pair (&scale)[8 / G])
+__device__ __forceinline__ F8 code_values(const uint32_t (&words)[G == 1 ? 8 : 2], const Pair (&scale)[G == 1 ? 4 : 8 / G])
 {
     F8 f;
     const Pair bias = both(-8388736.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+        if constexpr (G == 1) {
+            f.p[i] = mul2(add2(pair(code_float(words[2 * i] ^ 0x80u, 0), code_float(words[2 * i + 1] ^ 0x80u, 0)), bias),
+                          scale[i]);
+            continue;
+        }
         const uint32_t w = words[i / 2] ^ 0x80808080u;
         f.p[i] = mul2(add2(pair(code_float(w, 2 * (i & 1)), code_float(w, 2 * (i & 1) + 1)), bias),
                       scale[G == 4 ? i / 2 : 0]);
@@ -468,16 +473,12 @@ template <int G>
 __device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
 {
     if constexpr (G == 1) {
-        F8 f;
-        const Pair bias = both(-8388736.0f);
+        Pair scale[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float lo = ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i)) * factor;
-            const float hi = ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i + 1)) * factor;
-            f.p[i] = mul2(add2(pair(code_float(r.w[2 * i] ^ 0x80u, 0), code_float(r.w[2 * i + 1] ^ 0x80u, 0)), bias),
-                          pair(lo, hi));
-        }
-        return f;
+        for (int i = 0; i < 4; ++i)
+            scale[i] = pair(ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i)) * factor,
+                            ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i + 1)) * factor);
+        return code_values<1>(r.w, scale);
     } else {
         Pair scale[8 / G];
 #pragma unroll
@@ -486,73 +487,162 @@ __device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
     }
 }
 
-// ---- a thread's queue of copies in shared memory ---------------------------------------
-// Items (this thread's C chunks of one row of one tensor) are copied ahead of
+// ---- queues of copies in shared memory -----------------------------------------------------
+// Items (C chunks per thread of one row of one tensor) are copied ahead of
 // their use, in the order of their use: K of them are always in flight or
-// waiting. A thread copies and reads its own bytes only, so nothing but its
-// own wait for the copy is needed. A chunk past the row's end is filled with
-// zeros (a copy of no source bytes).
-template <class T, int C, int K>
+// waiting. A warp copies and reads the bytes of its own columns only. What
+// lies past the row's end is filled with zeros.
+// Aligned rows (ODD = false): each lane copies and reads its own words, so
+// that its own wait for the copy suffices. Rows at any pitch (ODD; the base is
+// 16-byte aligned): the lanes copy the aligned words that hold the warp's
+// columns, one more than it has, and read elements where the row's address
+// puts them; the lanes then wait for one another too. The word that holds the
+// row's first element may begin in the row before.
+template <class T, int C, int K, bool ODD>
 struct Queue {
-    static constexpr int G = kVector<T>, W = 8 / G;          // words of 16 bytes per chunk
-    uint32_t at, begin, end;                                 // the current slot; the first; past the last
+    static constexpr int G = ODD ? 1 : kVector<T>;
+    static constexpr int W = (int)sizeof(T) / 2;             // words of 16 bytes per lane and chunk
+    static constexpr uint32_t kChunk = (32 * W + (ODD ? 1 : 0)) * 16;       // bytes per warp
+    static __host__ __device__ constexpr size_t bytes(size_t threads) { return K * C * (threads / 32) * kChunk; }
+    uint32_t at, begin, end;                                 // this warp's current slot; the first; past the last
+    uint32_t lane;
 
     __device__ __forceinline__ Queue(void* smem)
     {
-        begin = at = (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16;
-        end = begin + K * C * W * 16 * blockDim.x;
+        lane = threadIdx.x & 31;
+        begin = at = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kChunk;
+        end = begin + (uint32_t)bytes(blockDim.x);
     }
-    __device__ __forceinline__ uint32_t word(int n) const { return at + (uint32_t)n * 16 * blockDim.x; }
-    // Start the copies of this thread's columns of a row of T.
-    __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&col)[C], const uint32_t (&mask)[C])
+    __device__ __forceinline__ uint32_t chunk_at(int i) const { return at + (uint32_t)i * (blockDim.x >> 5) * kChunk; }
+    static __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t size)
+    {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
+    }
+    // Words of a row from byte `first` (a multiple of 16 past the row's start)
+    // on: 32 * n and one more, from the aligned word that holds that byte. What
+    // lies at or past byte `size` of the row is not read (a copy of no bytes
+    // names the row's first word).
+    __device__ __forceinline__ void copy_run(uint32_t dst, const char* row, int64_t first, int64_t size, int n) const
+    {
+        const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
+        const int64_t left = row + size - word0 - first - lane * 16;         // bytes from this lane's first word on
+        const int32_t have = (int32_t)(left < 0 ? 0 : left > 4096 ? 4096 : left);
+        const char* from = word0 + first + lane * 16;
+#pragma unroll
+        for (int q = 0; q <= n; ++q) {
+            const int32_t bytes = min(max(have - 512 * q, 0), 16);
+            if (q < n || lane == 0) copy16(dst + (lane + 32 * q) * 16, bytes > 0 ? from + 512 * q : word0, (uint32_t)bytes);
+        }
+    }
+    // Start the copies of this warp's columns of a row of T.
+    __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&col)[C], const uint32_t (&mask)[C],
+                                             int64_t cols)
     {
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) {
+            if constexpr (ODD) {
+                copy_run(chunk_at(i), (const char*)row, (int64_t)(col[i] - lane) * (int64_t)sizeof(T),
+                         cols * (int64_t)sizeof(T), W);
+            } else {
 #pragma unroll
-            for (int q = 0; q < W; ++q)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                             ::"r"(word(i * W + q)), "l"(row + col[i] + 32 * G * q), "r"(mask[i] >> q & 1 ? 16 : 0)
-                             : "memory");
+                for (int q = 0; q < W; ++q)
+                    copy16(chunk_at(i) + (lane + 32 * q) * 16, row + col[i] + 32 * G * q, mask[i] >> q & 1 ? 16 : 0);
+            }
+        }
     }
-    // The same of a checkpoint's codes: one word of 8, or two of 4 bytes.
-    __device__ __forceinline__ void copy_codes(const int8_t* row, const uint32_t (&col)[C], const uint32_t (&mask)[C])
+    // The same of a checkpoint's codes (aligned: one word of 8, or two of 4 bytes per lane).
+    __device__ __forceinline__ void copy_codes(const int8_t* row, const uint32_t (&col)[C], const uint32_t (&mask)[C],
+                                               int64_t cols)
     {
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) {
+            if constexpr (ODD) {
+                const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
+                const int64_t at0 = (int64_t)(col[i] - lane) + lane * 16;    // this lane's word
+                const int64_t left = (const char*)row + cols - word0 - at0;
+                if (lane < 17)
+                    copy16(chunk_at(i) + lane * 16, left > 0 ? word0 + at0 : word0,
+                           left < 0 ? 0u : left > 16 ? 16u : (uint32_t)left);
+            } else {
 #pragma unroll
-            for (int q = 0; q < W; ++q)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
-                             ::"r"(word(i * W + q)), "l"(row + col[i] + 32 * G * q), "r"(mask[i] >> q & 1 ? G : 0), "n"(G)
-                             : "memory");
+                for (int q = 0; q < W; ++q)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
+                                 ::"r"(chunk_at(i) + (lane + 32 * q) * 16), "l"(row + col[i] + 32 * G * q),
+                                 "r"(mask[i] >> q & 1 ? G : 0), "n"(ODD ? 8 : G)
+                                 : "memory");
+            }
+        }
     }
     // The current slot is filled (or left as it is at the end): go on.
     __device__ __forceinline__ void next()
     {
         asm volatile("cp.async.commit_group;" ::: "memory");
-        at += C * W * 16 * blockDim.x;
-        at = at == end ? begin : at;
+        at += C * (blockDim.x >> 5) * kChunk;
+        if (at >= end) at -= K * C * (blockDim.x >> 5) * kChunk;
     }
     // Wait until the oldest item, which lies in the current slot, has landed.
-    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory"); }
-
-    __device__ __forceinline__ Raw8<T, G> chunk(int i) const
+    __device__ __forceinline__ void wait() const
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(K - 1) : "memory");
+        if constexpr (ODD) __syncwarp();
+    }
+    // The current slot has been read: it may be filled again.
+    __device__ __forceinline__ void done() const
+    {
+        if constexpr (ODD) __syncwarp();
+    }
+    // Chunk i; `shift`: the row's address modulo 16.
+    __device__ __forceinline__ Raw8<T, G> chunk(int i, uint32_t shift) const
     {
         Raw8<T, G> r;
+        if constexpr (ODD) {
+            const uint32_t from = chunk_at(i) + shift + lane * (uint32_t)sizeof(T);
+            if constexpr (sizeof(T) == 4)
+                asm volatile("ld.shared.u32 %0, [%8]; ld.shared.u32 %1, [%8 + 128];\n"
+                             "ld.shared.u32 %2, [%8 + 256]; ld.shared.u32 %3, [%8 + 384];\n"
+                             "ld.shared.u32 %4, [%8 + 512]; ld.shared.u32 %5, [%8 + 640];\n"
+                             "ld.shared.u32 %6, [%8 + 768]; ld.shared.u32 %7, [%8 + 896];"
+                             : "=&r"(r.w[0]), "=&r"(r.w[1]), "=&r"(r.w[2]), "=&r"(r.w[3]), "=&r"(r.w[4]), "=&r"(r.w[5]),
+                               "=&r"(r.w[6]), "=&r"(r.w[7])
+                             : "r"(from) : "memory");
+            else
+                asm volatile("{ .reg .u16 h<8>;\n"
+                             "ld.shared.u16 h0, [%8]; ld.shared.u16 h1, [%8 + 64];\n"
+                             "ld.shared.u16 h2, [%8 + 128]; ld.shared.u16 h3, [%8 + 192];\n"
+                             "ld.shared.u16 h4, [%8 + 256]; ld.shared.u16 h5, [%8 + 320];\n"
+                             "ld.shared.u16 h6, [%8 + 384]; ld.shared.u16 h7, [%8 + 448];\n"
+                             "cvt.u32.u16 %0, h0; cvt.u32.u16 %1, h1; cvt.u32.u16 %2, h2; cvt.u32.u16 %3, h3;\n"
+                             "cvt.u32.u16 %4, h4; cvt.u32.u16 %5, h5; cvt.u32.u16 %6, h6; cvt.u32.u16 %7, h7; }"
+                             : "=&r"(r.w[0]), "=&r"(r.w[1]), "=&r"(r.w[2]), "=&r"(r.w[3]), "=&r"(r.w[4]), "=&r"(r.w[5]),
+                               "=&r"(r.w[6]), "=&r"(r.w[7])
+                             : "r"(from) : "memory");
+        } else {
 #pragma unroll
-        for (int q = 0; q < W; ++q)
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
-                         : "r"(word(i * W + q))
-                         : "memory");
+            for (int q = 0; q < W; ++q)
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
+                             : "r"(chunk_at(i) + (lane + 32 * q) * 16)
+                             : "memory");
+        }
         return r;
     }
-    __device__ __forceinline__ void codes(int i, uint32_t (&w)[2]) const
+    __device__ __forceinline__ void codes(int i, uint32_t shift, uint32_t (&w)[ODD ? 8 : 2]) const
     {
-        if constexpr (W == 1)
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(word(i)) : "memory");
-        else
+        if constexpr (ODD) {
+            const uint32_t from = chunk_at(i) + shift + lane;
+            asm volatile("ld.shared.u8 %0, [%8]; ld.shared.u8 %1, [%8 + 32]; ld.shared.u8 %2, [%8 + 64];\n"
+                         "ld.shared.u8 %3, [%8 + 96]; ld.shared.u8 %4, [%8 + 128]; ld.shared.u8 %5, [%8 + 160];\n"
+                         "ld.shared.u8 %6, [%8 + 192]; ld.shared.u8 %7, [%8 + 224];"
+                         : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]), "=&r"(w[4]), "=&r"(w[5]), "=&r"(w[6]),
+                           "=&r"(w[7])
+                         : "r"(from) : "memory");
+        } else if constexpr (W == 1) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(chunk_at(i) + lane * 16) : "memory");
+        } else {
 #pragma unroll
-            for (int q = 0; q < W; ++q) asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[q]) : "r"(word(i * W + q)) : "memory");
+            for (int q = 0; q < W; ++q)
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[q]) : "r"(chunk_at(i) + (lane + 32 * q) * 16) : "memory");
+        }
     }
 };
 

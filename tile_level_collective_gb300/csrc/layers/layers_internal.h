@@ -19,6 +19,10 @@ struct Ckpt8Params {
     int32_t vec;                  // 16-byte aligned bases and pitches
 };
 
+// How rows can be read: at any address, at any pitch from 16-byte aligned
+// bases, or in 16-byte aligned words throughout.
+enum Access : int { kAnywhere = 0, kOddPitch = 1, kAligned = 2 };
+
 // The element types of the norms' parameters are dtype, or binary32 where
 // param_f32 is set.
 struct NormCommon {
@@ -27,7 +31,7 @@ struct NormCommon {
     int32_t post_norm, param_f32;
     float residual_scale, branch_scale, eps, inv_cols;
     int64_t rows, cols;
-    int32_t vec;
+    int32_t access;               // Access
 };
 
 struct NormParams {
