@@ -518,21 +518,13 @@ struct Queue {
     {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
     }
-    // Words of a row from byte `first` (a multiple of 16 past the row's start)
-    // on: 32 * n and one more, from the aligned word that holds that byte. What
-    // lies at or past byte `size` of the row is not read (a copy of no bytes
-    // names the row's first word).
-    __device__ __forceinline__ void copy_run(uint32_t dst, const char* row, int64_t first, int64_t size, int n) const
+    // This lane's word at byte `o` of the row's aligned words, which hold `total`
+    // bytes up to the row's end; what lies past it is not read (a copy of no
+    // bytes names the first word).
+    static __device__ __forceinline__ void copy_part(uint32_t dst, const char* word0, int32_t o, int32_t total)
     {
-        const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
-        const int64_t left = row + size - word0 - first - lane * 16;         // bytes from this lane's first word on
-        const int32_t have = (int32_t)(left < 0 ? 0 : left > 4096 ? 4096 : left);
-        const char* from = word0 + first + lane * 16;
-#pragma unroll
-        for (int q = 0; q <= n; ++q) {
-            const int32_t bytes = min(max(have - 512 * q, 0), 16);
-            if (q < n || lane == 0) copy16(dst + (lane + 32 * q) * 16, bytes > 0 ? from + 512 * q : word0, (uint32_t)bytes);
-        }
+        const int32_t bytes = min(max(total - o, 0), 16);
+        copy16(dst, word0 + (bytes > 0 ? o : 0), (uint32_t)bytes);
     }
     // Start the copies of this warp's columns of a row of T.
     __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&col)[C], const uint32_t (&mask)[C],
@@ -541,8 +533,12 @@ struct Queue {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             if constexpr (ODD) {
-                copy_run(chunk_at(i), (const char*)row, (int64_t)(col[i] - lane) * (int64_t)sizeof(T),
-                         cols * (int64_t)sizeof(T), W);
+                const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
+                const int32_t total = (int32_t)((uintptr_t)row & 15) + (int32_t)cols * (int32_t)sizeof(T);
+                const int32_t o = (int32_t)((col[i] - lane) * (uint32_t)sizeof(T) + lane * 16);
+#pragma unroll
+                for (int q = 0; q <= W; ++q)
+                    if (q < W || lane == 0) copy_part(chunk_at(i) + (lane + 32 * q) * 16, word0, o + 512 * q, total);
             } else {
 #pragma unroll
                 for (int q = 0; q < W; ++q)
@@ -558,11 +554,9 @@ struct Queue {
         for (int i = 0; i < C; ++i) {
             if constexpr (ODD) {
                 const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
-                const int64_t at0 = (int64_t)(col[i] - lane) + lane * 16;    // this lane's word
-                const int64_t left = (const char*)row + cols - word0 - at0;
+                const int32_t total = (int32_t)((uintptr_t)row & 15) + (int32_t)cols;
                 if (lane < 17)
-                    copy16(chunk_at(i) + lane * 16, left > 0 ? word0 + at0 : word0,
-                           left < 0 ? 0u : left > 16 ? 16u : (uint32_t)left);
+                    copy_part(chunk_at(i) + lane * 16, word0, (int32_t)(col[i] - lane + lane * 16), total);
             } else {
 #pragma unroll
                 for (int q = 0; q < W; ++q)
