@@ -4,27 +4,30 @@
 // Bound by HBM: the active experts' 3 * inter * hidden weights, read once.
 // The kernel is therefore one stream of weight tiles through shared memory
 // (tensor-map copies, a ring of stages deep enough to cover the latency of
-// HBM) into tcgen05.mma, whose 128 rows are rows of weights and whose N = 16
-// to 64 columns are all the call's tokens, padded to 16: an expert multiplies
-// every token, and the epilogue keeps those that chose it. The tensor cores
-// are nearly idle at any N; gathering tokens would save nothing that is short.
+// HBM) into tcgen05.mma, whose rows are rows of weights and whose N = 16 to 64
+// columns are all the call's tokens, padded to 16: an expert multiplies every
+// token, and the epilogue keeps those that chose it. The tensor cores are
+// nearly idle at any N (4 % busy at 1 token), so gathering tokens would save
+// nothing that is short. A stage is 256 rows of weights (two accumulators of
+// 128 rows) by 64 elements of depth, and the tokens' elements of that depth.
 //
 //   phase 0  logits in binary32 on the CUDA cores           | grid barrier
-//   routing  every block chooses for every token (the same bits everywhere)
-//   phase 1  tiles of 64 gate rows and the matching 64 up rows x hidden;
+//   routing  few tokens: every block chooses for every token (the same bits
+//            everywhere); more: one block per token         | grid barrier
+//   phase 1  tiles of 128 gate rows and the matching 128 up rows x hidden;
 //            epilogue: h[expert][token] = w * silu(gate) * up in the
 //            activations' type, zero for tokens that did not choose the
 //            expert                                         | grid barrier
-//   phase 2  tiles of 128 output columns x (inter of every active expert):
+//   phase 2  tiles of 256 output columns x (inter of every active expert):
 //            the sum over experts stays in the accumulator
 //
-// Work is split evenly in units of one 64-deep stage: block c takes the
-// stages [c, c + 1) * total / blocks, in tile order, so that a tile may be
-// spread over several blocks. Those write binary32 partial tiles; the block
-// that arrives last (a counter per tile) adds them in the order of the blocks,
-// so the sum does not depend on who is last. Nobody waits for another block
-// but at the two grid barriers, and the weights of phase 2's first stages are
-// on their way before the second one.
+// Work is split evenly in units of one stage: block c takes the stages
+// [c, c + 1) * total / blocks, in tile order, so that a tile may be spread over
+// several blocks. Those write binary32 partial tiles, which are added in the
+// order of the blocks: by the block that arrives last (a counter per tile), so
+// that nobody waits, or, where many parts of many tokens make up the output
+// tiles, by all blocks after one more grid barrier. The weights of phase 2's
+// first stages are on their way before the barrier in front of it.
 #include <cooperative_groups.h>
 
 #include "host/host_checks.h"
@@ -38,19 +41,24 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kDepth = 64;                  // one stage: 64 elements (128 bytes, one swizzle row) of K
-constexpr int kTileRows = 128;
-constexpr int kTileBytes = kTileRows * kDepth * 2;
+constexpr int kHalfRows = 128;              // rows of one accumulator
+constexpr int kTileRows = 2 * kHalfRows;    // phase 1: gate and up rows; phase 2: output columns
+constexpr int kHalfBytes = kHalfRows * kDepth * 2;
+constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kThreads = 256;               // warp 0 copies, warp 1 multiplies, warps 4 to 7 drain
 constexpr int kEpilogue = 128;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;
 constexpr int kRouterTokens = 8, kRouterExperts = 2;
+constexpr int kSpreadPairs = 64;
 
 struct MoeTensorParams {
     CUtensorMap w_in, w_out, x, h;
     MoeParams m;
     float* logits;                          // [tokens, experts]
     char* act;                              // [active, N, inter] activations (the h map)
-    float* partial;                         // [2 * grid][tokens][128] binary32 partial tiles
+    float* partial;                         // [2 * grid][2][tokens][128] binary32 partial tiles
+    int32_t* ids;                           // [tokens, top_k], where one block chooses per token
+    float* weights;
     uint32_t* arrived;                      // tiles of phase 1, then of phase 2
     int64_t counters;
     int64_t in_counters;                    // those of phase 1
@@ -72,7 +80,6 @@ struct Shared {
     float row_weight[PTOC_MOE_MAX_TOKENS];  // of the epilogue's expert; 0 where not chosen
     int32_t chosen[PTOC_MOE_MAX_TOKENS];
     union {
-        float up[16][64];                   // the epilogue's exchange of up rows
         float dots[kThreads / 32][kRouterExperts * kRouterTokens];
         uint32_t bits[PTOC_MOE_MAX_EXPERTS / 32];
     };
@@ -143,12 +150,12 @@ __device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes)
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// A box of a 2-D tensor map at column x (a multiple of 64 elements) and row y.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar)
+// A box of a tensor map at column x (a multiple of 64 elements) and row y of matrix z.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];"
-                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar))
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
                  : "memory");
 }
 
@@ -246,20 +253,36 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
     }
 }
 
-// The choice of every token, and the list of active local experts.
-__device__ __forceinline__ void route(const MoeTensorParams& p, Shared& sh)
+__device__ __forceinline__ void choose(const MoeParams& m, const float* logits, int32_t* ids, float* weights)
+{
+    if (m.experts <= 128) choose_experts<4>(m, logits, ids, weights);
+    else choose_experts<32>(m, logits, ids, weights);
+}
+
+// The choice of every token, and the list of active local experts. One choice
+// takes a warp about 1 us: up to kThreads / 32 tokens are chosen for in every
+// block, more by one block each and one more grid barrier (about 2 us).
+__device__ __forceinline__ void route(const MoeTensorParams& p, Shared& sh, const cg::grid_group& grid)
 {
     const MoeParams& m = p.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int t = warp; t < m.tokens; t += kThreads / 32) {
-        int32_t* ids = sh.ids + t * m.top_k;
-        float* w = sh.weights + t * m.top_k;
-        if (m.experts <= 128) choose_experts<4>(m, p.logits + t * m.experts, ids, w);
-        else choose_experts<32>(m, p.logits + t * m.experts, ids, w);
+    const int pairs = m.tokens * m.top_k;
+    if (m.tokens <= kThreads / 32) {
+        if (warp < m.tokens)
+            choose(m, p.logits + warp * m.experts, sh.ids + warp * m.top_k, sh.weights + warp * m.top_k);
+    } else {
+        if (warp == 0)
+            for (int t = blockIdx.x; t < m.tokens; t += gridDim.x)
+                choose(m, p.logits + t * m.experts, p.ids + t * m.top_k, p.weights + t * m.top_k);
+        grid.sync();
+        for (int i = threadIdx.x; i < pairs; i += kThreads) {
+            sh.ids[i] = p.ids[i];
+            sh.weights[i] = p.weights[i];
+        }
     }
     if (threadIdx.x < PTOC_MOE_MAX_EXPERTS / 32) sh.bits[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < m.tokens * m.top_k; i += kThreads) {
+    for (int i = threadIdx.x; i < pairs; i += kThreads) {
         const int local = sh.ids[i] - m.first;
         if (local >= 0 && local < m.local) atomicOr(&sh.bits[local >> 5], 1u << (local & 31));
         if (blockIdx.x == 0) {
@@ -283,6 +306,81 @@ __device__ __forceinline__ void route(const MoeTensorParams& p, Shared& sh)
     __syncthreads();
 }
 
+// ---- tiles ------------------------------------------------------------------------
+
+// One element of h: of an expert that the token did not choose it is 0,
+// whatever the sums hold.
+__device__ __forceinline__ float activation(const Shared& sh, int t, float gate, float up)
+{
+    return sh.chosen[t] ? sh.row_weight[t] * (gate / (1.0f + expf(-gate))) * up : 0.0f;
+}
+
+// Parts c0..c1 of a tile: sums in order of float4s at `at`(part) in both
+// halves, I of them `step` floats apart.
+template <int I>
+__device__ __forceinline__ void add_parts(const MoeTensorParams& p, uint32_t c0, uint32_t c1, int64_t at, int64_t step,
+                                          int items, float4 (&lo)[I], float4 (&hi)[I])
+{
+    const int64_t half = (int64_t)p.m.tokens * kHalfRows;
+#pragma unroll
+    for (int i = 0; i < I; ++i) lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [](float4& s, const float4& v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+    for (uint32_t c = c0; c <= c1; c += 2) {
+        float4 v[2][2 * I];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float* part = p.partial + (2 * (int64_t)(c + q) + (c + q == c0)) * 2 * half + at;
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+                if (i < items && c + q <= c1) {
+                    v[q][2 * i] = __ldcg((const float4*)(part + i * step));
+                    v[q][2 * i + 1] = __ldcg((const float4*)(part + half + i * step));
+                }
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+                if (i < items && c + q <= c1) {
+                    add(lo[i], v[q][2 * i]);
+                    add(hi[i], v[q][2 * i + 1]);
+                }
+    }
+}
+
+// Four neighbouring elements of a row of `n`, from column `col` on.
+template <class T>
+__device__ __forceinline__ void store4(T* row, int64_t col, int64_t n, const float4& v)
+{
+    const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (col + j < n) row[col + j] = from_f32<T>(e[j]);
+}
+
+// The output tile's sums of its parts, for the tokens and quads of rows that
+// thread `me` of `all` takes.
+template <class T>
+__device__ __forceinline__ void finish_output(const MoeTensorParams& p, uint32_t tile, uint32_t c0, uint32_t c1, int me,
+                                              int all)
+{
+    constexpr int I = 4;
+    const int quad = me & 31, row = quad * 4;
+    for (int t = me >> 5; t < p.m.tokens; t += I * (all >> 5)) {
+        const int step = all >> 5, items = min(I, (p.m.tokens - t + step - 1) / step);
+        float4 lo[I], hi[I];
+        add_parts<I>(p, c0, c1, (int64_t)t * kHalfRows + row, (int64_t)step * kHalfRows, items, lo, hi);
+        const int64_t col = (int64_t)tile * kTileRows + row;
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            if (i < items) {
+                T* y = (T*)p.m.y + (t + i * step) * p.m.ld_y;
+                store4(y, col, p.m.hidden, lo[i]);
+                store4(y, col + kHalfRows, p.m.hidden, hi[i]);
+            }
+    }
+}
+
 // ---- the kernel -------------------------------------------------------------------
 
 template <class T, int N>
@@ -293,10 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
     const uint32_t ring = (smem_u32(raw) + (uint32_t)kSharedHead + 1023u) & ~1023u;
     constexpr uint32_t kStage = kTileBytes + N * kDepth * 2;
     constexpr uint32_t kStages = kRing<N>;
-    constexpr uint32_t kTmem = 2 * N <= 32 ? 32 : 2 * N <= 64 ? 64 : 128;
+    constexpr uint32_t kColumns = 4 * N;                     // two accumulators in turn, of two halves
+    constexpr uint32_t kTmem = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : 256;
     // f32 accumulator, both operands T, both K-major, 128 x N
-    constexpr uint32_t kType = sizeof(T) == 2 && std::is_same<T, __half>::value ? 0u : 1u;
-    constexpr uint32_t kKind = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N >> 3) << 17 | (kTileRows >> 4) << 24;
+    constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
+    constexpr uint32_t kKind = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N >> 3) << 17 | (kHalfRows >> 4) << 24;
     const MoeParams& m = p.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const cg::grid_group grid = cg::this_grid();
@@ -320,15 +419,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
     router_logits<T>(p, sh);
     grid.sync();
     fence_after();
-    route(p, sh);
+    route(p, sh, grid);
 
     const uint32_t active = (uint32_t)sh.active;
     const uint32_t in_depth = (uint32_t)((m.hidden + kDepth - 1) / kDepth);
     const uint32_t out_depth = (uint32_t)((m.inter + kDepth - 1) / kDepth);
-    const uint32_t in_tiles = (uint32_t)((m.inter + 63) / 64);
+    const uint32_t in_tiles = (uint32_t)((m.inter + kHalfRows - 1) / kHalfRows);
     const uint32_t out_tiles = (uint32_t)((m.hidden + kTileRows - 1) / kTileRows);
     const Split in(active * in_tiles, in_depth, gridDim.x), out(out_tiles, active * out_depth, gridDim.x);
     const uint32_t tmem = sh.tmem;
+    // Output tiles of so many parts of so many tokens are summed by all blocks:
+    // one block alone takes about 1 us per 64 (token, part) pairs.
+    const bool spread = active > 0 && (int64_t)m.tokens * out.blocks > (int64_t)kSpreadPairs * out_tiles;
 
     if (active == 0) {                      // nothing is held here: rows of zeros
         for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < m.tokens * m.hidden;
@@ -348,32 +450,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             uint64_t* bar = &sh.full[slot];
             bar_expect(bar, kStage);
             if (phase == 1) {
-                const uint32_t a = tile / in_tiles, i0 = (tile - a * in_tiles) * 64;
-                const int row = (int)(sh.expert[a] * 2 * m.inter + i0);
-                copy_box(dst, &p.w_in, (int)d * kDepth, row, bar);
-                copy_box(dst + kTileBytes / 2, &p.w_in, (int)d * kDepth, row + (int)m.inter, bar);
+                const uint32_t a = tile / in_tiles;
+                const int i0 = (int)(tile - a * in_tiles) * kHalfRows, e = 2 * sh.expert[a];
+                copy_box(dst, &p.w_in, (int)d * kDepth, i0, e, bar);
+                copy_box(dst + kHalfBytes, &p.w_in, (int)d * kDepth, i0, e + 1, bar);
             } else {
                 const uint32_t a = d / out_depth, k = d - a * out_depth;
-                copy_box(dst, &p.w_out, (int)k * kDepth, (int)(sh.expert[a] * m.hidden) + (int)tile * kTileRows, bar);
+                const int h0 = (int)tile * kTileRows, e = sh.expert[a];
+                copy_box(dst, &p.w_out, (int)k * kDepth, h0, e, bar);
+                copy_box(dst + kHalfBytes, &p.w_out, (int)k * kDepth, h0 + kHalfRows, e, bar);
             }
         };
         auto tokens = [&](uint32_t x, uint32_t slot) {
             const uint32_t d = x % split.depth;
             const uint32_t dst = ring + slot * kStage + kTileBytes;
             if (phase == 1) {
-                copy_box(dst, &p.x, (int)d * kDepth, 0, &sh.full[slot]);
+                copy_box(dst, &p.x, (int)d * kDepth, 0, 0, &sh.full[slot]);
             } else {
                 const uint32_t a = d / out_depth, k = d - a * out_depth;
-                copy_box(dst, &p.h, (int)k * kDepth, (int)(a * N), &sh.full[slot]);
+                copy_box(dst, &p.h, (int)k * kDepth, 0, (int)a, &sh.full[slot]);
             }
         };
+        uint32_t sent = 0;
         if (phase == 2) {
             // the first weights do not wait for the other blocks
-            const uint32_t ahead = min(kStages, last - first);
-            uint32_t sent = 0;
             if (warp == 0) {
                 if (lane == 0)
-                    for (; sent < ahead; ++sent) {
+                    for (const uint32_t ahead = min(kStages, last - first); sent < ahead; ++sent) {
                         const uint32_t u = turn + sent;
                         if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
                         weights(first + sent, u % kStages);
@@ -381,18 +484,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 __syncwarp();
             }
             grid.sync();
-            if (warp == 0 && lane == 0) {
-                asm volatile("fence.proxy.async;" ::: "memory");     // h was written with ordinary stores
-                for (uint32_t s = 0; s < sent; ++s) tokens(first + s, (turn + s) % kStages);
-                for (uint32_t x = first + sent; x < last; ++x) {
-                    const uint32_t u = turn + (x - first);
-                    if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
-                    weights(x, u % kStages);
-                    tokens(x, u % kStages);
-                }
-            }
-        } else if (warp == 0 && lane == 0) {
-            for (uint32_t x = first; x < last; ++x) {
+        }
+        if (warp == 0 && lane == 0) {
+            if (phase == 2) asm volatile("fence.proxy.async;" ::: "memory");      // h was written with ordinary stores
+            for (uint32_t s = 0; s < sent; ++s) tokens(first + s, (turn + s) % kStages);
+            for (uint32_t x = first + sent; x < last; ++x) {
                 const uint32_t u = turn + (x - first);
                 if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
                 weights(x, u % kStages);
@@ -406,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             for (uint32_t x = first; x < last && ok;) {
                 // one segment: this block's stages of one tile
                 const uint32_t end = min(last, (x / split.depth + 1) * split.depth);
-                const uint32_t b = at & 1, d = tmem + b * N;
+                const uint32_t b = at & 1, d = tmem + b * 2 * N;
                 if (!wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns)) break;
                 fence_after();
                 for (const uint32_t from = x; x < end; ++x) {
@@ -416,8 +512,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                     fence_after();
                     const uint32_t a = ring + slot * kStage;
 #pragma unroll
-                    for (int k = 0; k < kDepth / 16; ++k)
-                        mma(d, operand(a + k * 32), operand(a + kTileBytes + k * 32), kKind, x > from || k > 0);
+                    for (int k = 0; k < kDepth / 16; ++k) {
+                        const uint64_t tok = operand(a + kTileBytes + k * 32);
+                        mma(d, operand(a + k * 32), tok, kKind, x > from || k > 0);
+                        mma(d + N, operand(a + kHalfBytes + k * 32), tok, kKind, x > from || k > 0);
+                    }
                     commit(&sh.empty[slot]);
                 }
                 if (ok) commit(&sh.acc_full[b]);
@@ -426,43 +525,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         }
 
         if (warp >= 4) {
-            const int row = threadIdx.x - 128;                       // of the tile
+            const int row = threadIdx.x - 128;                       // of either half
             uint32_t at = acc;
-            // One tile's sums of 16 tokens, complete, of this thread's row.
-            auto finish = [&](uint32_t tile, int n0, float (&v)[16]) {
-                if (phase == 1) {
-                    const uint32_t a = tile / in_tiles;
-                    const int64_t i = (tile - a * in_tiles) * 64 + (row & 63);
-                    if (row >= 64)
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) sh.up[n][row - 64] = v[n];
-                    epilogue_sync();
-                    if (row < 64 && i < m.inter)
-#pragma unroll
-                        for (int n = 0; n < 16; ++n) {
-                            const int t = n0 + n;
-                            if (t >= m.tokens) break;
-                            // a token that did not choose the expert has h = 0, whatever the sums hold
-                            const float h = sh.chosen[t] ? sh.row_weight[t] * (v[n] / (1.0f + expf(-v[n]))) * sh.up[n][row]
-                                                         : 0.0f;
-                            ((T*)p.act)[((int64_t)a * N + t) * m.inter + i] = from_f32<T>(h);
-                        }
-                    epilogue_sync();
-                } else {
-                    const int64_t col = (int64_t)tile * kTileRows + row;
-                    if (col < m.hidden)
-#pragma unroll
-                        for (int n = 0; n < 16; ++n)
-                            if (n0 + n < m.tokens) ((T*)m.y)[(n0 + n) * m.ld_y + col] = from_f32<T>(v[n]);
-                }
-            };
             for (uint32_t x = first; x < last;) {
                 const uint32_t tile = x / split.depth, head = tile * split.depth;
                 const uint32_t end = min(last, head + split.depth);
                 const bool whole = x == head && end == head + split.depth;
-                const uint32_t b = at & 1;
+                const uint32_t b = at & 1, a = tile / in_tiles;      // a: the expert, in phase 1
+                const int64_t i0 = (int64_t)(tile - a * in_tiles) * kHalfRows, col0 = (int64_t)tile * kTileRows;
+                T* h = (T*)p.act + (int64_t)a * N * m.inter;
                 if (phase == 1) {
-                    const int expert = m.first + sh.expert[tile / in_tiles];
+                    const int expert = m.first + sh.expert[a];
                     if (row < m.tokens) {
                         int hit = 0;
                         float w = 0.0f;
@@ -474,21 +547,33 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 }
                 if (!epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns)) break;
                 fence_after();
-                const uint32_t d = tmem + b * N + ((uint32_t)(warp & 3) << 21);
-                float* mine = p.partial + (2 * (int64_t)blockIdx.x + (x == head)) * m.tokens * kTileRows + row;
+                const uint32_t d = tmem + b * 2 * N + ((uint32_t)(warp & 3) << 21);
+                float* mine = p.partial + (2 * (int64_t)blockIdx.x + (x == head)) * 2 * m.tokens * kHalfRows + row;
 #pragma unroll 1
                 for (int n0 = 0; n0 < N && n0 < m.tokens; n0 += 16) {
-                    float v[16];
-                    load_columns(d + n0, v);
-                    if (whole) finish(tile, n0, v);
-                    else
+                    float lo[16], hi[16];
+                    load_columns(d + n0, lo);
+                    load_columns(d + N + n0, hi);
 #pragma unroll
-                        for (int n = 0; n < 16; ++n)
-                            if (n0 + n < m.tokens) mine[(n0 + n) * kTileRows] = v[n];
+                    for (int n = 0; n < 16; ++n) {
+                        const int t = n0 + n;
+                        if (t >= m.tokens) break;
+                        if (!whole) {
+                            mine[t * kHalfRows] = lo[n];
+                            mine[(m.tokens + t) * kHalfRows] = hi[n];
+                        } else if (phase == 1) {
+                            if (i0 + row < m.inter)
+                                h[t * m.inter + i0 + row] = from_f32<T>(activation(sh, t, lo[n], hi[n]));
+                        } else {
+                            T* y = (T*)m.y + t * m.ld_y + col0 + row;
+                            if (col0 + row < m.hidden) y[0] = from_f32<T>(lo[n]);
+                            if (col0 + kHalfRows + row < m.hidden) y[kHalfRows] = from_f32<T>(hi[n]);
+                        }
+                    }
                 }
                 fence_before();
                 bar_arrive(&sh.acc_empty[b]);
-                if (!whole) {
+                if (!whole && !(phase == 2 && spread)) {
                     const uint32_t c0 = split.owner(head), c1 = split.owner(head + split.depth - 1);
                     __threadfence();
                     epilogue_sync();
@@ -498,20 +583,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                         __threadfence();
                     }
                     epilogue_sync();
-                    if (sh.last) {
-#pragma unroll 1
-                        for (int n0 = 0; n0 < N && n0 < m.tokens; n0 += 16) {
-                            float v[16] = {};
-                            for (uint32_t c = c0; c <= c1; ++c) {
-                                const float* part =
-                                    p.partial + (2 * (int64_t)c + (c == c0)) * m.tokens * kTileRows + n0 * kTileRows + row;
+                    if (sh.last && phase == 2) finish_output<T>(p, tile, c0, c1, row, kEpilogue);
+                    if (sh.last && phase == 1) {
+                        constexpr int I = 2;
+                        const int quad = (row & 31) * 4, step = kEpilogue / 32;
+                        for (int t = row >> 5; t < m.tokens; t += I * step) {
+                            const int items = min(I, (m.tokens - t + step - 1) / step);
+                            float4 lo[I], hi[I];
+                            add_parts<I>(p, c0, c1, (int64_t)t * kHalfRows + quad, (int64_t)step * kHalfRows, items, lo, hi);
 #pragma unroll
-                                for (int n = 0; n < 16; ++n)
-                                    if (n0 + n < m.tokens) v[n] += __ldcg(part + n * kTileRows);
-                            }
-                            finish(tile, n0, v);
+                            for (int i = 0; i < I; ++i)
+                                if (i < items) {
+                                    const int tt = t + i * step;
+                                    store4(h + tt * m.inter, i0 + quad, m.inter,
+                                           make_float4(activation(sh, tt, lo[i].x, hi[i].x),
+                                                       activation(sh, tt, lo[i].y, hi[i].y),
+                                                       activation(sh, tt, lo[i].z, hi[i].z),
+                                                       activation(sh, tt, lo[i].w, hi[i].w)));
+                                }
                         }
                     }
+                    if (phase == 1) epilogue_sync();                 // chosen and row_weight are the next tile's now
+                } else if (phase == 1) {
+                    epilogue_sync();
                 }
                 x = end;
                 ++at;
@@ -522,6 +616,22 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         // every role advances by the same stages and segments
         turn += last - first;
         if (last > first) acc += (last - 1) / split.depth - first / split.depth + 1;
+    }
+
+    if (spread) {
+        grid.sync();
+        const int warps = kThreads / 32;
+        for (uint32_t u = blockIdx.x * warps + warp; u < out_tiles * (uint32_t)m.tokens; u += gridDim.x * warps) {
+            const uint32_t tile = u / (uint32_t)m.tokens, t = u - tile * (uint32_t)m.tokens;
+            const uint32_t c0 = out.owner(tile * out.depth), c1 = out.owner((tile + 1) * out.depth - 1);
+            if (c0 == c1) continue;
+            float4 lo[1], hi[1];
+            add_parts<1>(p, c0, c1, (int64_t)t * kHalfRows + lane * 4, 0, 1, lo, hi);
+            T* y = (T*)m.y + t * m.ld_y;
+            const int64_t col = (int64_t)tile * kTileRows + lane * 4;
+            store4(y, col, m.hidden, lo[0]);
+            store4(y, col + kHalfRows, m.hidden, hi[0]);
+        }
     }
 
     __syncthreads();
@@ -546,8 +656,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 // ---- host side --------------------------------------------------------------------
 
 struct TensorPlan {
-    size_t logits, act, partial, arrived, bytes;
-    int64_t in_counters, counters;
+    size_t logits, act, partial, arrived, ids, weights, bytes;
+    int64_t most, in_tiles, out_tiles, in_counters, counters;
 };
 
 constexpr int kGrid = 152;                  // one block per SM; the workspace is sized for it
@@ -556,29 +666,37 @@ int padded_tokens(int64_t tokens) { return (int)((tokens + 15) / 16 * 16); }
 
 TensorPlan tensor_plan(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k)
 {
-    const int64_t most = tokens * top_k < experts ? tokens * top_k : experts;
     auto up = [](size_t n) { return (n + 255) / 256 * 256; };
     TensorPlan t;
-    t.in_counters = most * ((inter + 63) / 64);
-    t.counters = t.in_counters + (hidden + kTileRows - 1) / kTileRows;
+    t.most = tokens * top_k < experts ? tokens * top_k : experts;
+    t.in_tiles = (inter + kHalfRows - 1) / kHalfRows;
+    t.out_tiles = (hidden + kTileRows - 1) / kTileRows;
+    t.in_counters = t.most * t.in_tiles;
+    t.counters = t.in_counters + t.out_tiles;
     size_t at = 0;
     t.logits = at, at += up((size_t)tokens * experts * 4);
-    t.act = at, at += up((size_t)most * padded_tokens(tokens) * inter * 2);
+    t.act = at, at += up((size_t)t.most * padded_tokens(tokens) * inter * 2);
     t.partial = at, at += up((size_t)2 * kGrid * tokens * kTileRows * 4);
     t.arrived = at, at += up((size_t)t.counters * 4);
+    t.ids = at, at += up((size_t)tokens * top_k * 4);
+    t.weights = at, at += up((size_t)tokens * top_k * 4);
     t.bytes = at;
     return t;
 }
 
-bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows, bool f16)
+// `count` matrices of [rows, cols] elements at pitch ld, one after another;
+// boxes of kDepth columns x box_rows rows of one matrix. What lies outside its
+// matrix is zeros and is not read.
+bool encode_matrices(CUtensorMap* map, const void* base, int64_t count, int64_t rows, int64_t cols, int64_t ld,
+                     int box_rows, bool f16)
 {
     const TensorMapEncoder enc = tensor_map_encoder();
     if (!enc) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {kDepth, (cuuint32_t)box_rows};
-    const cuuint32_t steps[2] = {1, 1};
-    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)count};
+    const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {kDepth, (cuuint32_t)box_rows, 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return enc(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -617,13 +735,10 @@ size_t moe_tensor_workspace(int64_t tokens, int64_t hidden, int64_t inter, int e
 
 bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_t* e)
 {
-    // tensor-map coordinates are int32
-    if ((int64_t)m.local * 2 * m.inter > INT32_MAX || (int64_t)m.local * m.hidden > INT32_MAX) return false;
     const TensorPlan t = tensor_plan(m.tokens, m.hidden, m.inter, m.experts, m.top_k);
-    const int64_t in_tiles = (m.inter + 63) / 64, most = t.in_counters / in_tiles;
-    // and stages are counted in 32 bits
-    if (most * in_tiles * ((m.hidden + kDepth - 1) / kDepth) > INT32_MAX ||
-        (m.hidden + kTileRows - 1) / kTileRows * most * ((m.inter + kDepth - 1) / kDepth) > INT32_MAX)
+    // stages are counted in 32 bits
+    if (t.in_counters * ((m.hidden + kDepth - 1) / kDepth) > INT32_MAX ||
+        t.out_tiles * t.most * ((m.inter + kDepth - 1) / kDepth) > INT32_MAX)
         return false;
     const int n = padded_tokens(m.tokens);
     const bool f16 = dtype == PTOC_F16;
@@ -634,13 +749,15 @@ bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_
     p.act = m.ws + t.act;
     p.partial = (float*)(m.ws + t.partial);
     p.arrived = (uint32_t*)(m.ws + t.arrived);
+    p.ids = (int32_t*)(m.ws + t.ids);
+    p.weights = (float*)(m.ws + t.weights);
     p.counters = t.counters;
     p.in_counters = t.in_counters;
     p.wait_ns = copy_wait_ns();
-    if (!encode_rows(&p.w_in, m.w_in, m.local * 2 * m.inter, m.hidden, m.hidden, 64, f16) ||
-        !encode_rows(&p.w_out, m.w_out, m.local * m.hidden, m.inter, m.inter, kTileRows, f16) ||
-        !encode_rows(&p.x, m.x, m.tokens, m.hidden, m.tokens > 1 ? m.ld_x : m.hidden, n, f16) ||
-        !encode_rows(&p.h, p.act, most * n, m.inter, m.inter, n, f16))
+    if (!encode_matrices(&p.w_in, m.w_in, 2 * (int64_t)m.local, m.inter, m.hidden, m.hidden, kHalfRows, f16) ||
+        !encode_matrices(&p.w_out, m.w_out, m.local, m.hidden, m.inter, m.inter, kHalfRows, f16) ||
+        !encode_matrices(&p.x, m.x, 1, m.tokens, m.hidden, m.tokens > 1 ? m.ld_x : m.hidden, n, f16) ||
+        !encode_matrices(&p.h, p.act, t.most, n, m.inter, m.inter, n, f16))
         return false;
     *e = f16 ? launch_for<__half>(p, s) : launch_for<__nv_bfloat16>(p, s);
     return true;
