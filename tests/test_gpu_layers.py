@@ -174,6 +174,13 @@ CASES = [
     ("f16", 2, 20001, 1, "none", True, 1, 1),
     ("bf16", 2, 32768, 2, "channel", True, 0, 0),
     ("f32", 700, 96, 64, "none", False, 0, 0),
+    ("bf16", 400, 4097, 3, "channel", True, 0, 0),         # odd pitch, more rows than blocks
+    ("f16", 701, 1031, 1, "scalar", True, 0, 0),
+    ("f32", 350, 2051, 2, "token", True, 1, 0),
+    ("bf16", 40, 8191, 2, "channel", True, 2, 0),
+    ("f16", 33, 515, 13, "token", True, 0, 1),             # odd base
+    ("f32", 17, 8190, 1, "channel", False, 0, 3),
+    ("bf16", 5, 9001, 2, "token", True, 0, 0),
 ]
 
 
@@ -607,6 +614,31 @@ def test_moe_parts_of_expert_parallel_ranks_add_up():
     layer(x, whole, workspace=layer.workspace(tokens))
     sizes = sum(p.double().abs() for p in parts)
     close(whole, sum(p.double() for p in parts), 2 * U[t] * sizes + U[t] * whole.double().abs(), "sum of parts")
+
+
+def test_moe_recovers_from_waits_that_gave_up(monkeypatch):
+    """With a bound of 1 ns a wait may give up (valid copies that are merely
+    not there yet): the call returns, the count says so, and the next call with
+    the default bound is right."""
+    g = gen(12)
+    x = rnd(g, (9, 512), torch.bfloat16)
+    layer = P.MoeLayer(rnd(g, (16, 512), torch.bfloat16, 0.1), rnd(g, (16, 256, 512), torch.bfloat16, 0.05),
+                       rnd(g, (16, 512, 128), torch.bfloat16, 0.1), 4)
+    want, got, ws = torch.empty_like(x), torch.empty_like(x), layer.workspace(9)
+    torch.cuda.synchronize()
+    P.ptoc_wait_faults()
+    layer(x, want, workspace=ws)
+    torch.cuda.synchronize()
+    assert P.ptoc_wait_faults() == 0
+    monkeypatch.setenv("PTOC_WAIT_NS", "1")
+    layer(x, got, workspace=ws)
+    torch.cuda.synchronize()
+    faults = P.ptoc_wait_faults()
+    monkeypatch.delenv("PTOC_WAIT_NS")
+    assert faults > 0 or torch.equal(got, want)
+    layer(x, got, workspace=ws)
+    torch.cuda.synchronize()
+    assert P.ptoc_wait_faults() == 0 and torch.equal(got, want)
 
 
 # ---- streams, graphs, repeats ---------------------------------------------------------

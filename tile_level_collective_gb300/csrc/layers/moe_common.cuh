@@ -55,7 +55,6 @@ __device__ __forceinline__ void choose_experts(const MoeParams& m, const float* 
         if (e < n && (m.sigmoid || m.bias)) k = m.bias ? score(k) + m.bias[e] : score(k);
         key[j] = e < n ? ordered(k) : 0u;
     }
-    float sum = 0.0f, mine = 0.0f;
     int id = 0;
     for (int k = 0; k < m.top_k; ++k) {
         uint32_t best = 0;
@@ -68,10 +67,11 @@ __device__ __forceinline__ void choose_experts(const MoeParams& m, const float* 
 #pragma unroll
         for (int j = 0; j < L; ++j)
             if (at == j * 32 + lane) key[j] = 0u;
-        const float w = score(logits[at]);
-        sum += w;
-        if (lane == k) mine = w, id = at;
+        if (lane == k) id = at;
     }
+    // the scores of the chosen, one lane each
+    float mine = lane < m.top_k ? score(logits[id]) : 0.0f;
+    const float sum = warp_sum(mine);
     if (lane < m.top_k) {
         if (m.renormalize) mine /= sum;
         ids[lane] = id;

@@ -18,16 +18,18 @@
 //            epilogue: h[expert][token] = w * silu(gate) * up in the
 //            activations' type, zero for tokens that did not choose the
 //            expert                                         | grid barrier
+//            the same for tiles of several parts            | grid barrier
 //   phase 2  tiles of 256 output columns x (inter of every active expert):
-//            the sum over experts stays in the accumulator
+//            the sum over experts stays in the accumulator  | grid barrier
+//            sums of tiles of several parts
 //
 // Work is split evenly in units of one stage: block c takes the stages
 // [c, c + 1) * total / blocks, in tile order, so that a tile may be spread over
-// several blocks. Those write binary32 partial tiles, which are added in the
-// order of the blocks: by the block that arrives last (a counter per tile), so
-// that nobody waits, or, where many parts of many tokens make up the output
-// tiles, by all blocks after one more grid barrier. The weights of phase 2's
-// first stages are on their way before the barrier in front of it.
+// several blocks. Those write binary32 partial tiles, which all blocks together
+// add after a barrier, in the order of the parts: the sum does not depend on
+// scheduling. (Added by the block that comes last at a tile, without the
+// barrier, 3 parts of 64 tokens took 22 us instead of 3.) The weights of phase
+// 2's first stages are on their way before the barriers in front of it.
 #include <cooperative_groups.h>
 
 #include "host/host_checks.h"
@@ -46,10 +48,10 @@ constexpr int kTileRows = 2 * kHalfRows;    // phase 1: gate and up rows; phase 
 constexpr int kHalfBytes = kHalfRows * kDepth * 2;
 constexpr int kTileBytes = 2 * kHalfBytes;
 constexpr int kThreads = 256;               // warp 0 copies, warp 1 multiplies, warps 4 to 7 drain
+constexpr int kWarps = kThreads / 32;
 constexpr int kEpilogue = 128;
 constexpr int kMaxStages = 8;
-constexpr int kRouterTokens = 8, kRouterExperts = 2;
-constexpr int kSpreadPairs = 64;
+constexpr int kRouterTokens = 8, kRouterExperts = 2;           // 16 sums: the exchange below counts on it
 
 struct MoeTensorParams {
     CUtensorMap w_in, w_out, x, h;
@@ -59,10 +61,15 @@ struct MoeTensorParams {
     float* partial;                         // [2 * grid][2][tokens][128] binary32 partial tiles
     int32_t* ids;                           // [tokens, top_k], where one block chooses per token
     float* weights;
-    uint32_t* arrived;                      // tiles of phase 1, then of phase 2
-    int64_t counters;
-    int64_t in_counters;                    // those of phase 1
     uint64_t wait_ns;
+};
+
+constexpr int kGrid = 152;                  // one block per SM; the workspace is sized for it
+
+// A tile of several parts, which the blocks c0 to c1 hold.
+struct PartedTile {
+    uint32_t tile;
+    uint16_t c0, c1;
 };
 
 // ---- shared memory ----------------------------------------------------------------
@@ -73,11 +80,12 @@ struct Shared {
     uint32_t tmem;
     int32_t active;                         // active local experts
     int32_t fault;                          // a bounded wait gave up
-    int32_t last;                           // this block finishes the tile
     int32_t ids[PTOC_MOE_MAX_TOKENS * PTOC_MOE_MAX_TOP_K];
     float weights[PTOC_MOE_MAX_TOKENS * PTOC_MOE_MAX_TOP_K];
     int16_t expert[PTOC_MOE_MAX_EXPERTS];   // the active local experts, ascending
-    float row_weight[PTOC_MOE_MAX_TOKENS];  // of the epilogue's expert; 0 where not chosen
+    PartedTile parted[2][kGrid];            // the tiles of several parts of either phase
+    int32_t parted_tiles[2];
+    float row_weight[PTOC_MOE_MAX_TOKENS];  // of the epilogue's expert
     int32_t chosen[PTOC_MOE_MAX_TOKENS];
     union {
         float dots[kThreads / 32][kRouterExperts * kRouterTokens];
@@ -172,12 +180,27 @@ struct Split {
     __device__ uint32_t begin(uint32_t c) const { return c >= blocks ? total : (uint32_t)((uint64_t)c * total / blocks); }
     // the block that holds stage x: the largest c with begin(c) <= x
     __device__ uint32_t owner(uint32_t x) const { return (uint32_t)((((uint64_t)x + 1) * blocks - 1) / total); }
+    // Tiles of several parts are those that a block other than the first begins
+    // within. Whether block c >= 1 is the first to begin within its tile.
+    __device__ bool parted(uint32_t c, PartedTile& t) const
+    {
+        const uint32_t x = begin(c);
+        t.tile = x / depth;
+        if (x == t.tile * depth || begin(c - 1) > t.tile * depth) return false;
+        t.c0 = (uint16_t)(c - 1);
+        t.c1 = (uint16_t)owner((t.tile + 1) * depth - 1);
+        return true;
+    }
 };
 
-// A bounded wait on a barrier of this block; false once any wait gave up.
+// A bounded wait on a barrier of this block; false once any wait gave up. The
+// clock is read only after a number of polls (each of which may be suspended
+// for a while): read by all SMs at once it takes a microsecond or more.
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, uint64_t bound_ns)
 {
-    if (stage_ready(smem_u32(bar), parity)) return true;
+    constexpr int kPolls = 64;
+    for (int i = 0; i < kPolls; ++i)
+        if (stage_ready(smem_u32(bar), parity)) return true;
     if (*(volatile int32_t*)&sh.fault) return false;
     if (stage_wait(smem_u32(bar), parity, globaltimer_ns() + bound_ns, bound_ns)) return true;
     if (atomicExch(&sh.fault, 1) == 0) atomicAdd(&g_stage_faults, 1u);
@@ -219,6 +242,7 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const int e0 = u / groups * kRouterExperts, t0 = u % groups * kRouterTokens;
         Pair sum[kRouterExperts][kRouterTokens] = {};
+#pragma unroll 2
         for (int64_t i = threadIdx.x * 8; i < m.hidden; i += kThreads * 8) {
             F8 r[kRouterExperts];
 #pragma unroll
@@ -226,21 +250,29 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
                 r[e] = load_router8<T>(m.router, m.router_f32, (int64_t)min(e0 + e, m.experts - 1) * m.hidden + i);
 #pragma unroll
             for (int t = 0; t < kRouterTokens; ++t) {
-                if (t0 + t >= m.tokens) break;
-                const F8 x = load_router8<T>(m.x, false, (t0 + t) * m.ld_x + i);
+                const F8 x = load_router8<T>(m.x, false, min(t0 + t, m.tokens - 1) * m.ld_x + i);
 #pragma unroll
                 for (int e = 0; e < kRouterExperts; ++e)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sum[e][t] = fma2(r[e].p[j], x.p[j], sum[e][t]);
             }
         }
+        // 16 sums over 32 lanes: each exchange halves the values that a lane
+        // keeps; lanes 2 i and 2 i + 1 end up with halves of sum i
+        float v[16];
 #pragma unroll
-        for (int e = 0; e < kRouterExperts; ++e)
+        for (int i = 0; i < 16; ++i) v[i] = sum_of(sum[i / kRouterTokens][i % kRouterTokens]);
 #pragma unroll
-            for (int t = 0; t < kRouterTokens; ++t) {
-                const float v = warp_sum(sum_of(sum[e][t]));
-                if (lane == 0) sh.dots[warp][e * kRouterTokens + t] = v;
+        for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float give = upper ? v[i] : v[n + i], keep = upper ? v[n + i] : v[i];
+                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
             }
+        }
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
+        if (!(lane & 1)) sh.dots[warp][lane >> 1] = v[0];
         __syncthreads();
         if (threadIdx.x < kRouterExperts * kRouterTokens) {
             float v = 0.0f;
@@ -308,43 +340,45 @@ __device__ __forceinline__ void route(const MoeTensorParams& p, Shared& sh, cons
 
 // ---- tiles ------------------------------------------------------------------------
 
-// One element of h: of an expert that the token did not choose it is 0,
-// whatever the sums hold.
-__device__ __forceinline__ float activation(const Shared& sh, int t, float gate, float up)
+// One element of h.
+__device__ __forceinline__ float activation(float w, float gate, float up)
 {
-    return sh.chosen[t] ? sh.row_weight[t] * (gate / (1.0f + expf(-gate))) * up : 0.0f;
+    return w * (gate / (1.0f + expf(-gate))) * up;
 }
 
-// Parts c0..c1 of a tile: sums in order of float4s at `at`(part) in both
-// halves, I of them `step` floats apart.
-template <int I>
-__device__ __forceinline__ void add_parts(const MoeTensorParams& p, uint32_t c0, uint32_t c1, int64_t at, int64_t step,
-                                          int items, float4 (&lo)[I], float4 (&hi)[I])
+// The weight with which token t chose `expert`; false if it did not.
+__device__ __forceinline__ bool chosen(const MoeParams& m, const Shared& sh, int t, int expert, float& w)
 {
+    bool hit = false;
+    for (int k = 0; k < m.top_k; ++k)
+        if (sh.ids[t * m.top_k + k] == expert) hit = true, w = sh.weights[t * m.top_k + k];
+    return hit;
+}
+
+// The sums, in order, of the parts c0..c1 of a tile, for one token and the
+// rows quad..quad+3 of both halves.
+__device__ __forceinline__ void add_parts(const MoeTensorParams& p, uint32_t c0, uint32_t c1, int t, int quad,
+                                          float4& lo, float4& hi)
+{
+    constexpr int kAtOnce = 8;
     const int64_t half = (int64_t)p.m.tokens * kHalfRows;
-#pragma unroll
-    for (int i = 0; i < I; ++i) lo[i] = hi[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    lo = hi = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     auto add = [](float4& s, const float4& v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
-    for (uint32_t c = c0; c <= c1; c += 2) {
-        float4 v[2][2 * I];
+    for (uint32_t c = c0; c <= c1; c += kAtOnce) {
+        float4 v[kAtOnce][2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const float* part = p.partial + (2 * (int64_t)(c + q) + (c + q == c0)) * 2 * half + at;
+        for (int q = 0; q < kAtOnce; ++q)
+            if (c + q <= c1) {
+                const float* part = p.partial + (2 * (int64_t)(c + q) + (c + q == c0)) * 2 * half + t * kHalfRows + quad;
+                v[q][0] = __ldcg((const float4*)part);
+                v[q][1] = __ldcg((const float4*)(part + half));
+            }
 #pragma unroll
-            for (int i = 0; i < I; ++i)
-                if (i < items && c + q <= c1) {
-                    v[q][2 * i] = __ldcg((const float4*)(part + i * step));
-                    v[q][2 * i + 1] = __ldcg((const float4*)(part + half + i * step));
-                }
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-                if (i < items && c + q <= c1) {
-                    add(lo[i], v[q][2 * i]);
-                    add(hi[i], v[q][2 * i + 1]);
-                }
+        for (int q = 0; q < kAtOnce; ++q)
+            if (c + q <= c1) {
+                add(lo, v[q][0]);
+                add(hi, v[q][1]);
+            }
     }
 }
 
@@ -357,31 +391,6 @@ __device__ __forceinline__ void store4(T* row, int64_t col, int64_t n, const flo
     for (int j = 0; j < 4; ++j)
         if (col + j < n) row[col + j] = from_f32<T>(e[j]);
 }
-
-// The output tile's sums of its parts, for the tokens and quads of rows that
-// thread `me` of `all` takes.
-template <class T>
-__device__ __forceinline__ void finish_output(const MoeTensorParams& p, uint32_t tile, uint32_t c0, uint32_t c1, int me,
-                                              int all)
-{
-    constexpr int I = 4;
-    const int quad = me & 31, row = quad * 4;
-    for (int t = me >> 5; t < p.m.tokens; t += I * (all >> 5)) {
-        const int step = all >> 5, items = min(I, (p.m.tokens - t + step - 1) / step);
-        float4 lo[I], hi[I];
-        add_parts<I>(p, c0, c1, (int64_t)t * kHalfRows + row, (int64_t)step * kHalfRows, items, lo, hi);
-        const int64_t col = (int64_t)tile * kTileRows + row;
-#pragma unroll
-        for (int i = 0; i < I; ++i)
-            if (i < items) {
-                T* y = (T*)p.m.y + (t + i * step) * p.m.ld_y;
-                store4(y, col, p.m.hidden, lo[i]);
-                store4(y, col + kHalfRows, p.m.hidden, hi[i]);
-            }
-    }
-}
-
-// ---- the kernel -------------------------------------------------------------------
 
 template <class T, int N>
 __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_constant__ MoeTensorParams p)
@@ -414,8 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         fence_before();
     }
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < p.counters; i += (int64_t)gridDim.x * kThreads)
-        p.arrived[i] = 0;
     router_logits<T>(p, sh);
     grid.sync();
     fence_after();
@@ -428,14 +435,25 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
     const uint32_t out_tiles = (uint32_t)((m.hidden + kTileRows - 1) / kTileRows);
     const Split in(active * in_tiles, in_depth, gridDim.x), out(out_tiles, active * out_depth, gridDim.x);
     const uint32_t tmem = sh.tmem;
-    // Output tiles of so many parts of so many tokens are summed by all blocks:
-    // one block alone takes about 1 us per 64 (token, part) pairs.
-    const bool spread = active > 0 && (int64_t)m.tokens * out.blocks > (int64_t)kSpreadPairs * out_tiles;
-
     if (active == 0) {                      // nothing is held here: rows of zeros
         for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < m.tokens * m.hidden;
              i += (int64_t)gridDim.x * kThreads)
             ((T*)m.y)[i / m.hidden * m.ld_y + i % m.hidden] = from_f32<T>(0.0f);
+    }
+
+    // warps 2 and 3 list the tiles of several parts while the others begin (each
+    // in the same order: the places are those of the blocks)
+    if (warp == 2 || warp == 3) {
+        const Split& split = warp == 2 ? in : out;
+        int n = 0;
+        for (uint32_t c0 = 1; c0 < split.blocks; c0 += 32) {
+            PartedTile t;
+            const bool on = c0 + lane < split.blocks && split.parted(c0 + lane, t);
+            const uint32_t all = __ballot_sync(0xffffffffu, on);
+            if (on) sh.parted[warp - 2][n + __popc(all & ((1u << lane) - 1))] = t;
+            n += __popc(all);
+        }
+        if (lane == 0) sh.parted_tiles[warp - 2] = n;
     }
 
     // the roles' places in the ring and in the two accumulators, kept over both phases
@@ -483,6 +501,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                     }
                 __syncwarp();
             }
+            grid.sync();
+            // h of the tiles of several parts: a warp takes 128 rows for one token
+            for (uint32_t u = blockIdx.x * kWarps + warp; u < (uint32_t)(sh.parted_tiles[0] * m.tokens); u += gridDim.x * kWarps) {
+                const uint32_t i = u / (uint32_t)m.tokens;
+                const int t = (int)(u - i * (uint32_t)m.tokens), quad = lane * 4;
+                const PartedTile part = sh.parted[0][i];
+                const uint32_t a = part.tile / in_tiles;
+                float4 lo, hi;
+                float w = 0.0f;
+                if (chosen(m, sh, t, m.first + sh.expert[a], w)) {
+                    add_parts(p, part.c0, part.c1, t, quad, lo, hi);
+                    lo = make_float4(activation(w, lo.x, hi.x), activation(w, lo.y, hi.y), activation(w, lo.z, hi.z),
+                                     activation(w, lo.w, hi.w));
+                } else {
+                    lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                }
+                store4((T*)p.act + ((int64_t)a * N + t) * m.inter, (int64_t)(part.tile - a * in_tiles) * kHalfRows + quad,
+                       m.inter, lo);
+            }
+            asm volatile("fence.proxy.async;" ::: "memory");          // h is read by tensor-map copies
             grid.sync();
         }
         if (warp == 0 && lane == 0) {
@@ -536,12 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 T* h = (T*)p.act + (int64_t)a * N * m.inter;
                 if (phase == 1) {
                     const int expert = m.first + sh.expert[a];
+                    float w = 0.0f;
                     if (row < m.tokens) {
-                        int hit = 0;
-                        float w = 0.0f;
-                        for (int k = 0; k < m.top_k; ++k)
-                            if (sh.ids[row * m.top_k + k] == expert) hit = 1, w = sh.weights[row * m.top_k + k];
-                        sh.chosen[row] = hit;
+                        sh.chosen[row] = chosen(m, sh, row, expert, w);
                         sh.row_weight[row] = w;
                     }
                 }
@@ -562,8 +597,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                             mine[t * kHalfRows] = lo[n];
                             mine[(m.tokens + t) * kHalfRows] = hi[n];
                         } else if (phase == 1) {
+                            // of an expert that the token did not choose it is 0, whatever the sums hold
                             if (i0 + row < m.inter)
-                                h[t * m.inter + i0 + row] = from_f32<T>(activation(sh, t, lo[n], hi[n]));
+                                h[t * m.inter + i0 + row] =
+                                    from_f32<T>(sh.chosen[t] ? activation(sh.row_weight[t], lo[n], hi[n]) : 0.0f);
                         } else {
                             T* y = (T*)m.y + t * m.ld_y + col0 + row;
                             if (col0 + row < m.hidden) y[0] = from_f32<T>(lo[n]);
@@ -573,40 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 }
                 fence_before();
                 bar_arrive(&sh.acc_empty[b]);
-                if (!whole && !(phase == 2 && spread)) {
-                    const uint32_t c0 = split.owner(head), c1 = split.owner(head + split.depth - 1);
-                    __threadfence();
-                    epilogue_sync();
-                    if (row == 0) {
-                        uint32_t* counter = p.arrived + (phase == 1 ? 0 : p.in_counters) + tile;
-                        sh.last = atomicAdd(counter, 1u) == c1 - c0;
-                        __threadfence();
-                    }
-                    epilogue_sync();
-                    if (sh.last && phase == 2) finish_output<T>(p, tile, c0, c1, row, kEpilogue);
-                    if (sh.last && phase == 1) {
-                        constexpr int I = 2;
-                        const int quad = (row & 31) * 4, step = kEpilogue / 32;
-                        for (int t = row >> 5; t < m.tokens; t += I * step) {
-                            const int items = min(I, (m.tokens - t + step - 1) / step);
-                            float4 lo[I], hi[I];
-                            add_parts<I>(p, c0, c1, (int64_t)t * kHalfRows + quad, (int64_t)step * kHalfRows, items, lo, hi);
-#pragma unroll
-                            for (int i = 0; i < I; ++i)
-                                if (i < items) {
-                                    const int tt = t + i * step;
-                                    store4(h + tt * m.inter, i0 + quad, m.inter,
-                                           make_float4(activation(sh, tt, lo[i].x, hi[i].x),
-                                                       activation(sh, tt, lo[i].y, hi[i].y),
-                                                       activation(sh, tt, lo[i].z, hi[i].z),
-                                                       activation(sh, tt, lo[i].w, hi[i].w)));
-                                }
-                        }
-                    }
-                    if (phase == 1) epilogue_sync();                 // chosen and row_weight are the next tile's now
-                } else if (phase == 1) {
-                    epilogue_sync();
-                }
+                if (phase == 1) epilogue_sync();                     // chosen and row_weight are the next tile's now
                 x = end;
                 ++at;
             }
@@ -618,19 +622,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         if (last > first) acc += (last - 1) / split.depth - first / split.depth + 1;
     }
 
-    if (spread) {
+    if (active > 0) {
         grid.sync();
-        const int warps = kThreads / 32;
-        for (uint32_t u = blockIdx.x * warps + warp; u < out_tiles * (uint32_t)m.tokens; u += gridDim.x * warps) {
-            const uint32_t tile = u / (uint32_t)m.tokens, t = u - tile * (uint32_t)m.tokens;
-            const uint32_t c0 = out.owner(tile * out.depth), c1 = out.owner((tile + 1) * out.depth - 1);
-            if (c0 == c1) continue;
-            float4 lo[1], hi[1];
-            add_parts<1>(p, c0, c1, (int64_t)t * kHalfRows + lane * 4, 0, 1, lo, hi);
+        for (uint32_t u = blockIdx.x * kWarps + warp; u < (uint32_t)(sh.parted_tiles[1] * m.tokens); u += gridDim.x * kWarps) {
+            const uint32_t i = u / (uint32_t)m.tokens;
+            const int t = (int)(u - i * (uint32_t)m.tokens), quad = lane * 4;
+            const PartedTile part = sh.parted[1][i];
+            float4 lo, hi;
+            add_parts(p, part.c0, part.c1, t, quad, lo, hi);
             T* y = (T*)m.y + t * m.ld_y;
-            const int64_t col = (int64_t)tile * kTileRows + lane * 4;
-            store4(y, col, m.hidden, lo[0]);
-            store4(y, col + kHalfRows, m.hidden, hi[0]);
+            const int64_t col = (int64_t)part.tile * kTileRows + quad;
+            store4(y, col, m.hidden, lo);
+            store4(y, col + kHalfRows, m.hidden, hi);
         }
     }
 
@@ -656,11 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 // ---- host side --------------------------------------------------------------------
 
 struct TensorPlan {
-    size_t logits, act, partial, arrived, ids, weights, bytes;
-    int64_t most, in_tiles, out_tiles, in_counters, counters;
+    size_t logits, act, partial, ids, weights, bytes;
+    int64_t most, in_tiles, out_tiles;
 };
-
-constexpr int kGrid = 152;                  // one block per SM; the workspace is sized for it
 
 int padded_tokens(int64_t tokens) { return (int)((tokens + 15) / 16 * 16); }
 
@@ -671,13 +672,10 @@ TensorPlan tensor_plan(int64_t tokens, int64_t hidden, int64_t inter, int expert
     t.most = tokens * top_k < experts ? tokens * top_k : experts;
     t.in_tiles = (inter + kHalfRows - 1) / kHalfRows;
     t.out_tiles = (hidden + kTileRows - 1) / kTileRows;
-    t.in_counters = t.most * t.in_tiles;
-    t.counters = t.in_counters + t.out_tiles;
     size_t at = 0;
     t.logits = at, at += up((size_t)tokens * experts * 4);
     t.act = at, at += up((size_t)t.most * padded_tokens(tokens) * inter * 2);
     t.partial = at, at += up((size_t)2 * kGrid * tokens * kTileRows * 4);
-    t.arrived = at, at += up((size_t)t.counters * 4);
     t.ids = at, at += up((size_t)tokens * top_k * 4);
     t.weights = at, at += up((size_t)tokens * top_k * 4);
     t.bytes = at;
@@ -737,7 +735,7 @@ bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_
 {
     const TensorPlan t = tensor_plan(m.tokens, m.hidden, m.inter, m.experts, m.top_k);
     // stages are counted in 32 bits
-    if (t.in_counters * ((m.hidden + kDepth - 1) / kDepth) > INT32_MAX ||
+    if (t.most * t.in_tiles * ((m.hidden + kDepth - 1) / kDepth) > INT32_MAX ||
         t.out_tiles * t.most * ((m.inter + kDepth - 1) / kDepth) > INT32_MAX)
         return false;
     const int n = padded_tokens(m.tokens);
@@ -748,11 +746,8 @@ bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_
     p.logits = (float*)(m.ws + t.logits);
     p.act = m.ws + t.act;
     p.partial = (float*)(m.ws + t.partial);
-    p.arrived = (uint32_t*)(m.ws + t.arrived);
     p.ids = (int32_t*)(m.ws + t.ids);
     p.weights = (float*)(m.ws + t.weights);
-    p.counters = t.counters;
-    p.in_counters = t.in_counters;
     p.wait_ns = copy_wait_ns();
     if (!encode_matrices(&p.w_in, m.w_in, 2 * (int64_t)m.local, m.inter, m.hidden, m.hidden, kHalfRows, f16) ||
         !encode_matrices(&p.w_out, m.w_out, m.local, m.hidden, m.inter, m.inter, kHalfRows, f16) ||
