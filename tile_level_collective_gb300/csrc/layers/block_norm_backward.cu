@@ -241,7 +241,7 @@ __device__ __forceinline__ void store_sums(const NormBackParams& p, const uint32
 // few counters for its loads, and shared-memory reads that follow a load wait
 // for it too (8192 x 4096 from checkpoints: 93 us so, 81 in batches). A scale
 // is a power of two (or NaN): the upper half of its binary32 form.
-constexpr int kHeaderRows = 16;
+constexpr int kHeaderRows = 32;
 
 struct Header {
     float* values;                          // [3][kHeaderRows]: r, ra, gate
@@ -278,11 +278,35 @@ struct Header {
         }
         __syncthreads();
     }
-    // Several loads in flight per thread.
+    static __device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return __float_as_uint(ckpt_scale(byte)) >> 16; }
+    // Words of four bytes where the checkpoint's rows allow them, several in
+    // flight per thread: a batch costs about 1 us, byte by byte about 4.
     __device__ __forceinline__ void load_scales(int which, const ptoc_ckpt8& k, int64_t row, uint32_t rows)
     {
-        constexpr int kAtOnce = 8;
         uint16_t* to = scales + which * kHeaderRows * blocks;
+        const uint32_t words = (uint32_t)blocks / 4;
+        if (words && words * 4 == (uint32_t)blocks && words <= blockDim.x &&
+            (((uintptr_t)k.exps | (uintptr_t)k.ld_exps) & 3u) == 0) {
+            constexpr int kAtOnce = 4;
+            const uint32_t i0 = threadIdx.x / words, w = threadIdx.x - i0 * words, step = blockDim.x / words;
+            if (i0 >= step) return;
+            for (uint32_t i = i0; i < rows; i += kAtOnce * step) {
+                uint32_t v[kAtOnce];
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q)
+                    v[q] = i + q * step < rows
+                               ? *(const uint32_t*)(k.exps + (row + (int64_t)(i + q * step) * gridDim.x) * k.ld_exps + 4 * w)
+                               : 0u;
+#pragma unroll
+                for (int q = 0; q < kAtOnce; ++q)
+                    if (i + q * step < rows)
+                        *(uint2*)(to + (i + q * step) * blocks + 4 * w) =
+                            make_uint2(scale_bits(v[q] & 255u) | scale_bits(v[q] >> 8 & 255u) << 16,
+                                       scale_bits(v[q] >> 16 & 255u) | scale_bits(v[q] >> 24) << 16);
+            }
+            return;
+        }
+        constexpr int kAtOnce = 8;
         for (uint32_t n0 = threadIdx.x; n0 < rows * blocks; n0 += kAtOnce * blockDim.x) {
             uint32_t byte[kAtOnce];
 #pragma unroll
@@ -292,8 +316,7 @@ struct Header {
             }
 #pragma unroll
             for (int q = 0; q < kAtOnce; ++q)
-                if (n0 + q * blockDim.x < rows * blocks)
-                    to[n0 + q * blockDim.x] = (uint16_t)(__float_as_uint(ckpt_scale(byte[q])) >> 16);
+                if (n0 + q * blockDim.x < rows * blocks) to[n0 + q * blockDim.x] = (uint16_t)scale_bits(byte[q]);
         }
     }
     __device__ __forceinline__ RowScalars scalars() const
@@ -581,9 +604,11 @@ __global__ void __launch_bounds__(kSumThreads) norm_backward_sum_kernel(const No
 }
 
 // The queue form: rows in flight and its rule. Two chunks per thread and 512
-// threads on an SM; wider rows leave no room for a row of copies ahead.
+// threads on an SM; wider rows leave no room for a row of copies ahead. (Two
+// rows ahead of 16-bit elements: 8192 x 4096 from matrices 83 us instead of 76,
+// from checkpoints the same.)
 template <class T>
-constexpr int kRowsAhead = 2 / ((int)sizeof(T) / 2);
+constexpr int kRowsAhead = 1;
 constexpr int64_t kQueueCols = kQueueThreads * 16;
 // Shared memory of a block: the columns' parameters, the queues, the header.
 template <class T, bool ODD>

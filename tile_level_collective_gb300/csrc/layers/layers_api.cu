@@ -62,7 +62,7 @@ struct Operands {
     }
     int access(int64_t cols, int eb) const
     {
-        return vec && cols % (16 / eb) == 0 ? kAligned : bases ? kOddPitch : kAnywhere;
+        return !bases ? kAnywhere : vec && cols % (16 / eb) == 0 ? kAligned : kOddPitch;
     }
     ptoc_status disjoint() const { return check_disjoint_outputs(writes, nw, reads, nr); }
 };
@@ -134,6 +134,7 @@ ptoc_status norm_common(const ptoc_block_norm_params* q, int64_t rows, int64_t c
             o.param(q->gate, cols, eb);
         } else {
             if (!aligned(q->gate, eb)) return PTOC_ERR_INVALID_ARG;
+            if ((uintptr_t)q->gate & 3u) o.vec = o.bases = false;
             o.add(false, q->gate, footprint(kind == kGateToken ? rows : 1, 1, q->gate_row_stride, eb));
         }
     }
