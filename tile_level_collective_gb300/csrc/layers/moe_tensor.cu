@@ -51,7 +51,6 @@ constexpr int kThreads = 256;               // warp 0 copies, warp 1 multiplies,
 constexpr int kWarps = kThreads / 32;
 constexpr int kEpilogue = 128;
 constexpr int kMaxStages = 8;
-constexpr int kRouterTokens = 8, kRouterExperts = 2;           // 16 sums: the exchange below counts on it
 
 struct MoeTensorParams {
     CUtensorMap w_in, w_out, x, h;
@@ -88,7 +87,7 @@ struct Shared {
     float row_weight[PTOC_MOE_MAX_TOKENS];  // of the epilogue's expert
     int32_t chosen[PTOC_MOE_MAX_TOKENS];
     union {
-        float dots[kThreads / 32][kRouterExperts * kRouterTokens];
+        float dots[kWarps][16];
         uint32_t bits[PTOC_MOE_MAX_EXPERTS / 32];
     };
 };
@@ -230,40 +229,44 @@ __device__ __forceinline__ F8 load_router8(const void* base, bool f32, int64_t i
     return load8<T, 8>((const T*)base + i, 0, 1).expand();
 }
 
-// Dot products of kRouterExperts experts with kRouterTokens tokens per block
-// and turn; the warps share the row and their sums are added in order.
-template <class T>
+// Dot products of ET experts with TT tokens per block and turn (ET * TT is a
+// power of two of at most 16); the warps share the rows and their sums are
+// added in order.
+template <class T, int ET, int TT>
 __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& sh)
 {
+    constexpr int kSums = ET * TT;
     const MoeParams& m = p.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int groups = (m.tokens + kRouterTokens - 1) / kRouterTokens;
-    const int units = (m.experts + kRouterExperts - 1) / kRouterExperts * groups;
+    const int groups = (m.tokens + TT - 1) / TT;
+    const int units = (m.experts + ET - 1) / ET * groups;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
-        const int e0 = u / groups * kRouterExperts, t0 = u % groups * kRouterTokens;
-        Pair sum[kRouterExperts][kRouterTokens] = {};
-#pragma unroll 2
+        const int e0 = u / groups * ET, t0 = u % groups * TT;
+        Pair sum[ET][TT] = {};
+        // tokens and experts past the last are computed as the last and dropped
+#pragma unroll(kSums > 4 ? 2 : 4)
         for (int64_t i = threadIdx.x * 8; i < m.hidden; i += kThreads * 8) {
-            F8 r[kRouterExperts];
+            F8 r[ET];
 #pragma unroll
-            for (int e = 0; e < kRouterExperts; ++e)
+            for (int e = 0; e < ET; ++e)
                 r[e] = load_router8<T>(m.router, m.router_f32, (int64_t)min(e0 + e, m.experts - 1) * m.hidden + i);
 #pragma unroll
-            for (int t = 0; t < kRouterTokens; ++t) {
+            for (int t = 0; t < TT; ++t) {
                 const F8 x = load_router8<T>(m.x, false, min(t0 + t, m.tokens - 1) * m.ld_x + i);
 #pragma unroll
-                for (int e = 0; e < kRouterExperts; ++e)
+                for (int e = 0; e < ET; ++e)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) sum[e][t] = fma2(r[e].p[j], x.p[j], sum[e][t]);
             }
         }
-        // 16 sums over 32 lanes: each exchange halves the values that a lane
-        // keeps; lanes 2 i and 2 i + 1 end up with halves of sum i
-        float v[16];
+        // kSums sums over 32 lanes: each exchange halves the values that a lane
+        // keeps, until it keeps one; then the lanes that keep the same add up
+        float v[kSums];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = sum_of(sum[i / kRouterTokens][i % kRouterTokens]);
+        for (int i = 0; i < kSums; ++i) v[i] = sum_of(sum[i / TT][i % TT]);
+        int o = 16;
 #pragma unroll
-        for (int n = 8, o = 16; n >= 1; n >>= 1, o >>= 1) {
+        for (int n = kSums / 2; n >= 1; n >>= 1, o >>= 1) {
             const bool upper = lane & o;
 #pragma unroll
             for (int i = 0; i < n; ++i) {
@@ -271,15 +274,16 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
                 v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
             }
         }
-        v[0] += __shfl_xor_sync(0xffffffffu, v[0], 1);
-        if (!(lane & 1)) sh.dots[warp][lane >> 1] = v[0];
+        constexpr int kSame = 32 / kSums;                    // neighbouring lanes that keep the same sum
+        for (; o >= 1; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        if (lane % kSame == 0) sh.dots[warp][lane / kSame] = v[0];
         __syncthreads();
-        if (threadIdx.x < kRouterExperts * kRouterTokens) {
-            float v = 0.0f;
+        if (threadIdx.x < kSums) {
+            float d = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kThreads / 32; ++w) v += sh.dots[w][threadIdx.x];
-            const int e = e0 + threadIdx.x / kRouterTokens, t = t0 + threadIdx.x % kRouterTokens;
-            if (e < m.experts && t < m.tokens) p.logits[t * m.experts + e] = v;
+            for (int w = 0; w < kWarps; ++w) d += sh.dots[w][threadIdx.x];
+            const int e = e0 + threadIdx.x / TT, t = t0 + threadIdx.x % TT;
+            if (e < m.experts && t < m.tokens) p.logits[t * m.experts + e] = d;
         }
         __syncthreads();
     }
@@ -423,7 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         fence_before();
     }
-    router_logits<T>(p, sh);
+    // one or two tokens: all loads of a row at once, an expert to a block
+    if (m.tokens <= 2) router_logits<T, 1, 2>(p, sh);
+    else router_logits<T, 2, 8>(p, sh);
     grid.sync();
     fence_after();
     route(p, sh, grid);

@@ -140,9 +140,9 @@ _raw_stream = None
 def _torch_names():
     """Fill what depends on torch, which the package imports on first use."""
     import torch
-    global _raw_stream, _float32, _int32, _int8, _uint8
+    global _raw_stream, _float32, _int32
     _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
-    _float32, _int32, _int8, _uint8 = torch.float32, torch.int32, torch.int8, torch.uint8
+    _float32, _int32 = torch.float32, torch.int32
     _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -156,9 +156,10 @@ def _code(dtype):
 
 
 def _stream_of(stream, device):
-    """The given stream, or torch's current one on the tensors' device."""
-    if stream is None and device.type == "cuda":
-        return _raw_stream(device.index)
+    """The given stream, or torch's current one on the tensors' device (an
+    index; -1 for the host's memory)."""
+    if stream is None and device >= 0:
+        return _raw_stream(device)
     return _stream(stream)
 
 
@@ -168,32 +169,39 @@ def _call(status, where):
     return status
 
 
-def _pitch(t, what):
-    """The row pitch of a 2-D tensor. A single row may have any row stride."""
-    if t.dim() != 2:
-        raise ValueError("%s: expected a 2-D tensor" % what)
+def _pitch(t, rows, cols, what):
+    """The row pitch of a [rows, cols] tensor. A single row may have any row stride."""
     ld, one = t.stride()
-    rows, cols = t.shape
     if one != 1 and cols > 1:
         raise ValueError("%s: rows must be contiguous (stride(1) == 1)" % what)
     return ld if rows > 1 or ld > cols else cols
 
 
-def _like(t, shape, dtype, device, what):
-    """A matrix argument of the activations' kind, packed for C; None stays None."""
+def _first(t, what):
+    """Shape, rows, columns, dtype and device index of the tensor that the others must match."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s: expected a 2-D tensor" % what)
+    return shape, shape[0], shape[1], t.dtype, t.get_device()
+
+
+def _like(t, kind, what):
+    """A matrix argument of the activations' kind (_first's answer), packed for C; None stays None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device:
+    shape, rows, cols, dtype, device = kind
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
         raise ValueError("%s: needs the shape, dtype and device of the activations" % what)
-    return _matrix_bytes(t.data_ptr(), _pitch(t, what))
+    return _matrix_bytes(t.data_ptr(), _pitch(t, rows, cols, what))
 
 
 def _packed(t, shape, dtype, device, what):
     """The address of a packed tensor argument; None stays None."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError("%s: expected a packed %s tensor of shape %s on %s" % (what, dtype, tuple(shape), device))
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s: expected a packed %s tensor of shape %s on the activations' device" %
+                         (what, dtype, tuple(shape)))
     return t.data_ptr()
 
 
@@ -228,35 +236,37 @@ class Checkpoint8:
 
     def _hold(self, codes, exps):
         self.codes, self.exps = codes, exps
-        self.shape, self.device = codes.shape, codes.device
-        self.c = (codes.data_ptr(), _pitch(codes, "codes"), exps.data_ptr(), _pitch(exps, "exps"))
+        self.shape, self.device = codes.shape, codes.get_device()
+        self.c = (codes.data_ptr(), _pitch(codes, *codes.shape, "codes"), exps.data_ptr(),
+                  _pitch(exps, *exps.shape, "exps"))
 
 
-def _ckpt(k, shape, device, what):
+def _ckpt(k, kind, what):
     if k is None:
         return None
-    if k.shape != shape or k.device != device:
+    if k.shape != kind[0] or k.device != kind[4]:
         raise ValueError("%s: the checkpoint needs the shape and device of the activations" % what)
     return _ckpt_bytes(*k.c)
 
 
-def _ckpt_call(call, x, ckpt, stream, what):
-    shape, device = x.shape, x.device
-    m = _matrix_bytes(x.data_ptr(), _pitch(x, what))
-    k = _ckpt(ckpt, shape, device, what)
-    code = _code(x.dtype)
-    a, b = (m, k) if what == "checkpoint8" else (k, m)
-    return _call(call(a, b, shape[0], shape[1], code, _stream_of(stream, device)), "ptoc_" + what)
-
-
 def checkpoint8(x, ckpt, stream=None):
     """ckpt = x [rows, cols] in 8 bits."""
-    return _ckpt_call(_lib.ptoc_checkpoint8, x, ckpt, stream, "checkpoint8")
+    kind = _first(x, "checkpoint8")
+    shape, rows, cols, dtype, device = kind
+    code = _code(dtype)
+    st = _lib.ptoc_checkpoint8(_like(x, kind, "checkpoint8"), _ckpt(ckpt, kind, "checkpoint8"), rows, cols, code,
+                               _stream_of(stream, device))
+    return _call(st, "ptoc_checkpoint8")
 
 
 def restore8(ckpt, x, stream=None):
     """x [rows, cols] = the values that the checkpoint holds."""
-    return _ckpt_call(_lib.ptoc_restore8, x, ckpt, stream, "restore8")
+    kind = _first(x, "restore8")
+    shape, rows, cols, dtype, device = kind
+    code = _code(dtype)
+    st = _lib.ptoc_restore8(_ckpt(ckpt, kind, "restore8"), _like(x, kind, "restore8"), rows, cols, code,
+                            _stream_of(stream, device))
+    return _call(st, "ptoc_restore8")
 
 
 def _gate_strides(gate, rows, cols):
@@ -277,22 +287,23 @@ def _gate_strides(gate, rows, cols):
     return rs, cs
 
 
-def _norm_params(shape, dtype, device, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps):
-    rows, cols = shape
+def _norm_params(kind, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps):
+    shape, rows, cols, dtype, device = kind
     if post_weight is not None and not post_norm:
         raise ValueError("block_norm: post_weight without the norm after the block")
-    kind = None
+    params = None
     for t in (post_weight, pre_weight, gate):
         if t is not None:
-            if kind is None:
-                kind = t.dtype
-            if t.dtype != kind or (kind != dtype and kind != _float32) or t.device != device:
+            if params is None:
+                params = t.dtype
+            if t.dtype is not params or (params is not dtype and params is not _float32) or t.get_device() != device:
                 raise ValueError("block_norm: weights and gate need one dtype (the activations' or float32) and their "
                                  "device")
     rs, cs = _gate_strides(gate, rows, cols) if gate is not None else (0, 0)
-    return _params_bytes(1 if post_norm else 0, _codes[dtype if kind is None else kind],
-                         _packed(post_weight, (cols,), kind, device, "post_weight") or 0,
-                         _packed(pre_weight, (cols,), kind, device, "pre_weight") or 0,
+    columns = (cols,)
+    return _params_bytes(1 if post_norm else 0, _codes[dtype if params is None else params],
+                         _packed(post_weight, columns, params, device, "post_weight") or 0,
+                         _packed(pre_weight, columns, params, device, "pre_weight") or 0,
                          0 if gate is None else gate.data_ptr(), rs, cs, residual_scale, branch_scale, eps)
 
 
@@ -306,26 +317,27 @@ def block_norm(parts, residual, out, normed=None, *, post_norm=True, post_weight
     if n == 0:
         raise ValueError("block_norm: expected at least one part")
     first = parts[0]
-    shape, dtype, device, strides = first.shape, first.dtype, first.device, first.stride()
+    kind = _first(first, "parts")
+    shape, rows, cols, dtype, device = kind
     code = _code(dtype)
-    ld = _pitch(first, "parts")
-    rows, cols = shape
-    pointers = []
-    for t in parts:
-        if t is not first and (t.shape != shape or t.stride() != strides or t.dtype != dtype or t.device != device):
-            raise ValueError("block_norm: every part needs the same shape, strides, dtype and device")
-        pointers.append(t.data_ptr())
-    kind = _array_types.get(n)
-    if kind is None:
-        kind = _array_types[n] = ctypes.c_void_p * n
-    group = kind(*pointers)
-    p = _norm_params(shape, dtype, device, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
+    ld = _pitch(first, rows, cols, "parts")
+    pointers = [first.data_ptr()]
+    if n > 1:
+        strides = first.stride()
+        for t in parts[1:]:
+            if t.dtype is not dtype or t.get_device() != device or t.shape != shape or t.stride() != strides:
+                raise ValueError("block_norm: every part needs the same shape, strides, dtype and device")
+            pointers.append(t.data_ptr())
+    array = _array_types.get(n)
+    if array is None:
+        array = _array_types[n] = ctypes.c_void_p * n
+    group = array(*pointers)
+    p = _norm_params(kind, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
     st = _lib.ptoc_block_norm(
-        _group_bytes(ctypes.addressof(group), n, 0), ld, _like(residual, shape, dtype, device, "residual"), p,
-        _like(out, shape, dtype, device, "out"), _like(normed, shape, dtype, device, "normed"),
-        _like(block_out, shape, dtype, device, "block_out"), _ckpt(block_ckpt, shape, device, "block_ckpt"),
-        _ckpt(stream_ckpt, shape, device, "stream_ckpt"), _packed(rstd, (2, rows), _float32, device, "rstd"), rows,
-        cols, code, _stream_of(stream, device))
+        _group_bytes(ctypes.addressof(group), n, 0), ld, _like(residual, kind, "residual"), p, _like(out, kind, "out"),
+        _like(normed, kind, "normed"), _like(block_out, kind, "block_out"), _ckpt(block_ckpt, kind, "block_ckpt"),
+        _ckpt(stream_ckpt, kind, "stream_ckpt"), _packed(rstd, (2, rows), _float32, device, "rstd"), rows, cols, code,
+        _stream_of(stream, device))
     return _call(st, "ptoc_block_norm")
 
 
@@ -343,30 +355,30 @@ def block_norm_backward(block, saved_stream, rstd, d_normed, d_residual, d_block
     the gradient that reaches the stream from later layers. ``d_block`` is the
     gradient of every part. Weight and gate gradients are float32, the gate's
     in the gate's shape."""
-    shape, dtype, device = d_normed.shape, d_normed.dtype, d_normed.device
+    kind = _first(d_normed, "d_normed")
+    shape, rows, cols, dtype, device = kind
     code = _code(dtype)
-    dy = _like(d_normed, shape, dtype, device, "d_normed")
-    rows, cols = shape
     if d_gate is not None and gate is None:
         raise ValueError("block_norm_backward: d_gate without a gate")
-    p = _norm_params(shape, dtype, device, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
+    p = _norm_params(kind, post_norm, post_weight, pre_weight, gate, residual_scale, branch_scale, eps)
     held = [(0, 0), (0, 0), (0, 0, 0, 0), (0, 0, 0, 0)]           # block, stream, their checkpoints
     for i, (t, what) in enumerate(((block, "block"), (saved_stream, "stream"))):
         if isinstance(t, Checkpoint8):
-            _ckpt(t, shape, device, what)
+            _ckpt(t, kind, what)
             held[2 + i] = t.c
         else:
-            _like(t, shape, dtype, device, what)
-            held[i] = (t.data_ptr(), _pitch(t, what))
+            _like(t, kind, what)
+            held[i] = (t.data_ptr(), _pitch(t, rows, cols, what))
+    columns = (cols,)
     s = _saved_bytes(*held[0], *held[1], *held[2], *held[3],
                      _packed(rstd, (2, rows), _float32, device, "rstd") or 0)
     st = _lib.ptoc_block_norm_backward(
-        s, p, dy, _like(d_stream, shape, dtype, device, "d_stream"),
-        _like(d_residual, shape, dtype, device, "d_residual"), _like(d_block, shape, dtype, device, "d_block"),
-        _packed(d_pre_weight, (cols,), _float32, device, "d_pre_weight"),
-        _packed(d_post_weight, (cols,), _float32, device, "d_post_weight"),
+        s, p, _like(d_normed, kind, "d_normed"), _like(d_stream, kind, "d_stream"),
+        _like(d_residual, kind, "d_residual"), _like(d_block, kind, "d_block"),
+        _packed(d_pre_weight, columns, _float32, device, "d_pre_weight"),
+        _packed(d_post_weight, columns, _float32, device, "d_post_weight"),
         _packed(d_gate, None if gate is None else gate.shape, _float32, device, "d_gate"), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), rows, cols, code, _stream_of(stream, device))
+        workspace.nbytes, rows, cols, code, _stream_of(stream, device))
     return _call(st, "ptoc_block_norm_backward")
 
 
@@ -382,7 +394,7 @@ class MoeLayer:
             raise ValueError("MoeLayer: expected router [experts, hidden], w_in [local, 2 * inter, hidden] and "
                              "w_out [local, hidden, inter]")
         local, hidden, inter = w_out.shape
-        dtype, device = w_in.dtype, w_in.device
+        dtype, device = w_in.dtype, w_in.get_device()
         self.code = _code(dtype)
         _packed(w_in, (local, 2 * inter, hidden), dtype, device, "w_in")
         _packed(w_out, (local, hidden, inter), dtype, device, "w_out")
@@ -393,7 +405,8 @@ class MoeLayer:
         if score not in SCORES:
             raise ValueError("MoeLayer: score is one of %s" % sorted(SCORES))
         self.router, self.w_in, self.w_out, self.bias = router, w_in, w_out, bias
-        self.dtype, self.device = dtype, device
+        self.dtype, self.device = dtype, w_in.device
+        self._kind = (dtype, device)
         self.hidden, self.inter, self.experts, self.top_k = hidden, inter, router.shape[0], top_k
         self.params = ptoc_moe_params(_addr(router), _addr(bias), _addr(w_in), _addr(w_out), _code(router.dtype),
                                       self.experts, first_expert, local, top_k, SCORES[score], int(bool(renormalize)),
@@ -408,15 +421,13 @@ class MoeLayer:
         """y [tokens, hidden] = the held experts' part of the layer's output
         for x; ids (int32) and weights (float32) [tokens, top_k] are optional
         outputs."""
-        shape, dtype, device = x.shape, self.dtype, self.device
-        m = _like(x, shape, dtype, device, "x")
-        tokens, hidden = shape
-        if hidden != self.hidden:
-            raise ValueError("MoeLayer: x needs the weights' width")
+        kind = _first(x, "x")
+        shape, tokens, hidden, dtype, device = kind
+        if (dtype, device) != self._kind or hidden != self.hidden:
+            raise ValueError("MoeLayer: x needs the weights' width, dtype and device")
         choice = (tokens, self.top_k)
         st = _lib.ptoc_moe_few_tokens(
-            m, ctypes.byref(self.params), _like(y, shape, dtype, device, "y"),
+            _like(x, kind, "x"), ctypes.byref(self.params), _like(y, kind, "y"),
             _packed(ids, choice, _int32, device, "ids"), _packed(weights, choice, _float32, device, "weights"),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), tokens, hidden, self.inter, self.code,
-            _stream_of(stream, device))
+            workspace.data_ptr(), workspace.nbytes, tokens, hidden, self.inter, self.code, _stream_of(stream, device))
         return _call(st, "ptoc_moe_few_tokens")
