@@ -240,9 +240,13 @@ __device__ __forceinline__ void store_sums(const NormBackParams& p, const uint32
 // row into registers they cost more, even a row ahead of their use: a warp has
 // few counters for its loads, and shared-memory reads that follow a load wait
 // for it too (8192 x 4096 from checkpoints: 93 us so, 81 in batches). A scale
-// is a power of two (or NaN): the upper half of its binary32 form.
-constexpr int kHeaderRows = 32;
+// is a power of two (or NaN): the upper half of its binary32 form. Binary32
+// rows of 8,192 columns at odd pitches have 199 KB of parameters and queues,
+// which leaves room for 16 rows.
+template <class T>
+constexpr int kHeaderRowsOf = sizeof(T) == 4 ? 16 : 32;
 
+template <int kHeaderRows>
 struct Header {
     float* values;                          // [3][kHeaderRows]: r, ra, gate
     uint16_t* scales;                       // [2][kHeaderRows][blocks]: the stream's, the block output's
@@ -345,7 +349,7 @@ struct QueueLoader {
     const char *stream_row, *dy_row, *du_row, *block_row;               // in that row
     uint32_t shift;                         // where the current item's row begins in its words
     uint32_t row;
-    Header head;
+    Header<kHeaderRowsOf<T>> head;
 
     __device__ __forceinline__ QueueLoader(const NormBackParams& q, unsigned char* smem, const uint32_t (&c)[C],
                                            const uint32_t (&m)[C])
@@ -614,7 +618,8 @@ constexpr int64_t kQueueCols = kQueueThreads * 16;
 template <class T, bool ODD>
 size_t queue_bytes(int64_t threads, int64_t cols)
 {
-    return threads * 2 * 64 + Queue<T, 2, 4 * kRowsAhead<T>, ODD>::bytes(threads) + Header::size(cols);
+    return threads * 2 * 64 + Queue<T, 2, 4 * kRowsAhead<T>, ODD>::bytes(threads) +
+           Header<kHeaderRowsOf<T>>::size(cols);
 }
 
 template <class T, bool CKPT, bool ODD>
