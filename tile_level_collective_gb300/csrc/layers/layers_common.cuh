@@ -43,7 +43,10 @@ __device__ __forceinline__ Pair pair(float lo, float hi)
     return r;
 }
 __device__ __forceinline__ Pair both(float v) { return pair(v, v); }
-__device__ __forceinline__ void split(Pair p, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p)); }
+__device__ __forceinline__ void split(Pair p, float& lo, float& hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
 __device__ __forceinline__ float sum_of(Pair p)
 {
     float a, b;
@@ -94,9 +97,6 @@ __device__ __forceinline__ uint32_t first_col(int i)
     const uint32_t c = (uint32_t)i * blockDim.x + threadIdx.x;
     return (c & ~31u) * 8 + (c & 31u) * G;
 }
-template <int G>
-__device__ __forceinline__ constexpr uint32_t run_step() { return 32 * G; }
-
 // Which of the chunk's runs, from column `col` on, lie below `cols`.
 template <int G>
 __device__ __forceinline__ uint32_t runs_below(uint32_t col, int64_t cols)
@@ -424,7 +424,8 @@ __device__ __forceinline__ CkptRaw<G> ckpt_load8(const Ckpt& k, int64_t row, uin
 #pragma unroll
         for (int j = 0; j < 8 / G; ++j) {
             r.w[j] = 0;
-            if (mask >> j & 1) r.w[j] = G == 4 ? *(const uint32_t*)(codes + 128 * j) : *(const uint8_t*)(codes + 32 * j);
+            if (mask >> j & 1)
+                r.w[j] = G == 4 ? *(const uint32_t*)(codes + 128 * j) : *(const uint8_t*)(codes + 32 * j);
         }
     }
     if constexpr (G == 1) {
@@ -450,15 +451,16 @@ __device__ __forceinline__ float code_float(uint32_t flipped, int byte)
 
 // Code words as values, run q times scale[q] (G = 1: pair q of runs).
 template <int G>
-__device__ __forceinline__ F8 code_values(const uint32_t (&words)[G == 1 ? 8 : 2], const Pair (&scale)[G == 1 ? 4 : 8 / G])
+__device__ __forceinline__ F8 code_values(const uint32_t (&words)[G == 1 ? 8 : 2],
+                                          const Pair (&scale)[G == 1 ? 4 : 8 / G])
 {
     F8 f;
     const Pair bias = both(-8388736.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (G == 1) {
-            f.p[i] = mul2(add2(pair(code_float(words[2 * i] ^ 0x80u, 0), code_float(words[2 * i + 1] ^ 0x80u, 0)), bias),
-                          scale[i]);
+            const Pair code = pair(code_float(words[2 * i] ^ 0x80u, 0), code_float(words[2 * i + 1] ^ 0x80u, 0));
+            f.p[i] = mul2(add2(code, bias), scale[i]);
             continue;
         }
         const uint32_t w = words[i / 2] ^ 0x80808080u;
@@ -542,7 +544,8 @@ struct Queue {
             } else {
 #pragma unroll
                 for (int q = 0; q < W; ++q)
-                    copy16(chunk_at(i) + (lane + 32 * q) * 16, row + col[i] + 32 * G * q, mask[i] >> q & 1 ? 16 : 0);
+                    copy16(chunk_at(i) + (lane + 32 * q) * 16, row + (mask[i] >> q & 1 ? col[i] + 32 * G * q : 0u),
+                           mask[i] >> q & 1 ? 16 : 0);
             }
         }
     }
@@ -561,7 +564,8 @@ struct Queue {
 #pragma unroll
                 for (int q = 0; q < W; ++q)
                     asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
-                                 ::"r"(chunk_at(i) + (lane + 32 * q) * 16), "l"(row + col[i] + 32 * G * q),
+                                 ::"r"(chunk_at(i) + (lane + 32 * q) * 16),
+                                 "l"(row + (mask[i] >> q & 1 ? col[i] + 32 * G * q : 0u)),
                                  "r"(mask[i] >> q & 1 ? G : 0), "n"(ODD ? 8 : G)
                                  : "memory");
             }
@@ -631,11 +635,13 @@ struct Queue {
                            "=&r"(w[7])
                          : "r"(from) : "memory");
         } else if constexpr (W == 1) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(chunk_at(i) + lane * 16) : "memory");
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                         : "=r"(w[0]), "=r"(w[1]) : "r"(chunk_at(i) + lane * 16) : "memory");
         } else {
 #pragma unroll
             for (int q = 0; q < W; ++q)
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[q]) : "r"(chunk_at(i) + (lane + 32 * q) * 16) : "memory");
+                asm volatile("ld.shared.u32 %0, [%1];"
+                             : "=r"(w[q]) : "r"(chunk_at(i) + (lane + 32 * q) * 16) : "memory");
         }
     }
 };

@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(kBlock) moe_router_kernel(const MoePlainParams
     const int64_t r = (int64_t)e * p.m.hidden;
     float sum = 0.0f;
 #pragma unroll 4
-    for (int64_t h = lane; h < p.m.hidden; h += 32) sum += to_f32(x[h]) * param_at<T>(p.m.router, p.m.router_f32, r + h);
+    for (int64_t h = lane; h < p.m.hidden; h += 32)
+        sum += to_f32(x[h]) * param_at<T>(p.m.router, p.m.router_f32, r + h);
     sum = warp_sum(sum);
     if (lane == 0) p.w.logits[dot] = sum;
 }

@@ -30,6 +30,16 @@
 // scheduling. (Added by the block that comes last at a tile, without the
 // barrier, 3 parts of 64 tokens took 22 us instead of 3.) The weights of phase
 // 2's first stages are on their way before the barriers in front of it.
+//
+// Measured on GB300 (bf16, of 6.68 TB/s copied): 64 tokens x 128 experts of 4096
+// x 1536 756 us (6.3 TB/s); 32 tokens 658 us (6.4 TB/s); 1 token, 8 of 64 experts
+// of 7168 x 2048, 126 us (5.6 TB/s); 1 token, 8 of 128 of 4096 x 1536, 67 us
+// (4.5 TB/s). What a call costs beside its stream of weights is 15 us at 1 token
+// and 22 us at 64: five or six grid barriers of 1.2 us, the latency of the first
+// copies of either phase (3 us each), the choice (2 us) and the epilogues.
+// Stages of 128 rows (two per tile of gate and up rows) took 829 us at 64 tokens,
+// as the tokens' elements then pass L2 twice as often; boxes without promotion
+// to 256 bytes in L2 872 us; stages of 128 elements of depth the same as 64.
 #include <cooperative_groups.h>
 
 #include "host/host_checks.h"
@@ -94,7 +104,10 @@ struct Shared {
 
 constexpr size_t kSharedHead = (sizeof(Shared) + 1023) / 1024 * 1024;
 // bytes of dynamic shared memory: the head, the ring, and room to align it
-constexpr size_t shared_bytes(int stages, int n) { return kSharedHead + 1024 + (size_t)stages * (kTileBytes + n * kDepth * 2); }
+constexpr size_t shared_bytes(int stages, int n)
+{
+    return kSharedHead + 1024 + (size_t)stages * (kTileBytes + n * kDepth * 2);
+}
 constexpr size_t kSharedMost = 227 * 1024;
 template <int N>
 constexpr int kRing = (int)((kSharedMost - kSharedHead - 1024) / (kTileBytes + N * kDepth * 2)) < kMaxStages
@@ -126,17 +139,39 @@ __device__ __forceinline__ void commit(uint64_t* bar)
                  : "memory");
 }
 
-__device__ __forceinline__ void load_columns(uint32_t addr, float (&v)[16])
+// Sixteen columns of both halves of an accumulator, this thread's row.
+__device__ __forceinline__ void load_columns(uint32_t lo_at, uint32_t hi_at, float (&lo)[16], float (&hi)[16])
 {
-    uint32_t u[16];
+    // (one statement: nothing may use the columns before the wait)
+    uint32_t u[16], v[16];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-                   "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-                 : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n"
+                 "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=&r"(u[0]), "=&r"(u[1]), "=&r"(u[2]), "=&r"(u[3]), "=&r"(u[4]), "=&r"(u[5]), "=&r"(u[6]),
+                   "=&r"(u[7]), "=&r"(u[8]), "=&r"(u[9]), "=&r"(u[10]), "=&r"(u[11]), "=&r"(u[12]), "=&r"(u[13]),
+                   "=&r"(u[14]), "=&r"(u[15]), "=&r"(v[0]), "=&r"(v[1]), "=&r"(v[2]), "=&r"(v[3]), "=&r"(v[4]),
+                   "=&r"(v[5]), "=&r"(v[6]), "=&r"(v[7]), "=&r"(v[8]), "=&r"(v[9]), "=&r"(v[10]), "=&r"(v[11]),
+                   "=&r"(v[12]), "=&r"(v[13]), "=&r"(v[14]), "=&r"(v[15])
+                 : "r"(lo_at), "r"(hi_at)
+                 : "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u[i]);
+    for (int i = 0; i < 16; ++i) lo[i] = __uint_as_float(u[i]), hi[i] = __uint_as_float(v[i]);
+}
+
+// f(0) to f(min(count, N) - 1), without a branch between them where all are asked for.
+template <int N, class F>
+__device__ __forceinline__ void each(int count, F f)
+{
+    if (count >= N) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) f(n);
+    } else {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (n < count) f(n);
+    }
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -176,7 +211,10 @@ struct Split {
     uint32_t blocks;                        // at most `total`: every one has work
     __device__ Split(uint32_t tiles, uint32_t d, uint32_t grid)
         : total(tiles * d), depth(d), blocks(tiles * d < grid ? tiles * d : grid) {}
-    __device__ uint32_t begin(uint32_t c) const { return c >= blocks ? total : (uint32_t)((uint64_t)c * total / blocks); }
+    __device__ uint32_t begin(uint32_t c) const
+    {
+        return c >= blocks ? total : (uint32_t)((uint64_t)c * total / blocks);
+    }
     // the block that holds stage x: the largest c with begin(c) <= x
     __device__ uint32_t owner(uint32_t x) const { return (uint32_t)((((uint64_t)x + 1) * blocks - 1) / total); }
     // Tiles of several parts are those that a block other than the first begins
@@ -240,7 +278,11 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int groups = (m.tokens + TT - 1) / TT;
     const int units = (m.experts + ET - 1) / ET * groups;
-    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+    // Every block takes a turn, though there may be fewer units than blocks (the
+    // answers of the extra turns are dropped): a block that has slept until the
+    // barrier takes 3 us longer over the choice that follows.
+    for (int turn = blockIdx.x; turn < max(units, (int)gridDim.x); turn += gridDim.x) {
+        const int u = turn % units;
         const int e0 = u / groups * ET, t0 = u % groups * TT;
         Pair sum[ET][TT] = {};
         // tokens and experts past the last are computed as the last and dropped
@@ -283,7 +325,7 @@ __device__ __forceinline__ void router_logits(const MoeTensorParams& p, Shared& 
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) d += sh.dots[w][threadIdx.x];
             const int e = e0 + threadIdx.x / TT, t = t0 + threadIdx.x % TT;
-            if (e < m.experts && t < m.tokens) p.logits[t * m.experts + e] = d;
+            if (turn < units && e < m.experts && t < m.tokens) p.logits[t * m.experts + e] = d;
         }
         __syncthreads();
     }
@@ -373,7 +415,8 @@ __device__ __forceinline__ void add_parts(const MoeTensorParams& p, uint32_t c0,
 #pragma unroll
         for (int q = 0; q < kAtOnce; ++q)
             if (c + q <= c1) {
-                const float* part = p.partial + (2 * (int64_t)(c + q) + (c + q == c0)) * 2 * half + t * kHalfRows + quad;
+                const int64_t slot = 2 * (int64_t)(c + q) + (c + q == c0);
+                const float* part = p.partial + slot * 2 * half + t * kHalfRows + quad;
                 v[q][0] = __ldcg((const float4*)part);
                 v[q][1] = __ldcg((const float4*)(part + half));
             }
@@ -509,7 +552,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             }
             grid.sync();
             // h of the tiles of several parts: a warp takes 128 rows for one token
-            for (uint32_t u = blockIdx.x * kWarps + warp; u < (uint32_t)(sh.parted_tiles[0] * m.tokens); u += gridDim.x * kWarps) {
+            const uint32_t pairs = (uint32_t)(sh.parted_tiles[0] * m.tokens);
+            for (uint32_t u = blockIdx.x * kWarps + warp; u < pairs; u += gridDim.x * kWarps) {
                 const uint32_t i = u / (uint32_t)m.tokens;
                 const int t = (int)(u - i * (uint32_t)m.tokens), quad = lane * 4;
                 const PartedTile part = sh.parted[0][i];
@@ -523,14 +567,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 } else {
                     lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
-                store4((T*)p.act + ((int64_t)a * N + t) * m.inter, (int64_t)(part.tile - a * in_tiles) * kHalfRows + quad,
-                       m.inter, lo);
+                store4((T*)p.act + ((int64_t)a * N + t) * m.inter,
+                       (int64_t)(part.tile - a * in_tiles) * kHalfRows + quad, m.inter, lo);
             }
-            asm volatile("fence.proxy.async;" ::: "memory");          // h is read by tensor-map copies
+            // h, here and in the epilogue, was written with ordinary stores, and is
+            // read by the tensor-map copies after the barrier
+            asm volatile("fence.proxy.async;" ::: "memory");
             grid.sync();
         }
         if (warp == 0 && lane == 0) {
-            if (phase == 2) asm volatile("fence.proxy.async;" ::: "memory");      // h was written with ordinary stores
             for (uint32_t s = 0; s < sent; ++s) tokens(first + s, (turn + s) % kStages);
             for (uint32_t x = first + sent; x < last; ++x) {
                 const uint32_t u = turn + (x - first);
@@ -593,25 +638,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 #pragma unroll 1
                 for (int n0 = 0; n0 < N && n0 < m.tokens; n0 += 16) {
                     float lo[16], hi[16];
-                    load_columns(d + n0, lo);
-                    load_columns(d + N + n0, hi);
-#pragma unroll
-                    for (int n = 0; n < 16; ++n) {
-                        const int t = n0 + n;
-                        if (t >= m.tokens) break;
-                        if (!whole) {
-                            mine[t * kHalfRows] = lo[n];
-                            mine[(m.tokens + t) * kHalfRows] = hi[n];
-                        } else if (phase == 1) {
-                            // of an expert that the token did not choose it is 0, whatever the sums hold
-                            if (i0 + row < m.inter)
-                                h[t * m.inter + i0 + row] =
+                    load_columns(d + n0, d + N + n0, lo, hi);
+                    const int count = m.tokens - n0;                 // columns that are tokens
+                    if (!whole) {
+                        float* to = mine + n0 * kHalfRows;
+                        each<16>(count, [&](int n) { to[n * kHalfRows] = lo[n]; });
+                        to += m.tokens * kHalfRows;
+                        each<16>(count, [&](int n) { to[n * kHalfRows] = hi[n]; });
+                    } else if (phase == 1) {
+                        // of an expert that the token did not choose it is 0, whatever the sums hold
+                        T* to = h + (int64_t)n0 * m.inter + i0 + row;
+                        if (i0 + row < m.inter)
+                            each<16>(count, [&](int n) {
+                                const int t = n0 + n;
+                                to[n * m.inter] =
                                     from_f32<T>(sh.chosen[t] ? activation(sh.row_weight[t], lo[n], hi[n]) : 0.0f);
-                        } else {
-                            T* y = (T*)m.y + t * m.ld_y + col0 + row;
-                            if (col0 + row < m.hidden) y[0] = from_f32<T>(lo[n]);
-                            if (col0 + kHalfRows + row < m.hidden) y[kHalfRows] = from_f32<T>(hi[n]);
-                        }
+                            });
+                    } else {
+                        T* to = (T*)m.y + n0 * m.ld_y + col0 + row;
+                        if (col0 + row < m.hidden) each<16>(count, [&](int n) { to[n * m.ld_y] = from_f32<T>(lo[n]); });
+                        to += kHalfRows;
+                        if (col0 + kHalfRows + row < m.hidden)
+                            each<16>(count, [&](int n) { to[n * m.ld_y] = from_f32<T>(hi[n]); });
                     }
                 }
                 fence_before();
@@ -620,7 +668,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 x = end;
                 ++at;
             }
-            if (phase == 1) asm volatile("fence.proxy.async;" ::: "memory");   // h is read by tensor-map copies
         }
         __syncwarp();
         // every role advances by the same stages and segments
@@ -630,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 
     if (active > 0) {
         grid.sync();
-        for (uint32_t u = blockIdx.x * kWarps + warp; u < (uint32_t)(sh.parted_tiles[1] * m.tokens); u += gridDim.x * kWarps) {
+        const uint32_t pairs = (uint32_t)(sh.parted_tiles[1] * m.tokens);
+        for (uint32_t u = blockIdx.x * kWarps + warp; u < pairs; u += gridDim.x * kWarps) {
             const uint32_t i = u / (uint32_t)m.tokens;
             const int t = (int)(u - i * (uint32_t)m.tokens), quad = lane * 4;
             const PartedTile part = sh.parted[1][i];
