@@ -31,7 +31,8 @@ def decode(tokens=5, hidden=1024, inter=512, experts=32, top_k=4, ranks=4, steps
         return torch.empty(shape, dtype=dt, device="cuda").normal_(0, std, generator=g)
 
     router = weights(experts, hidden, std=hidden ** -0.5)
-    w_in, w_out = weights(experts, 2 * inter, hidden, std=hidden ** -0.5), weights(experts, hidden, inter, std=inter ** -0.5)
+    w_in = weights(experts, 2 * inter, hidden, std=hidden ** -0.5)
+    w_out = weights(experts, hidden, inter, std=inter ** -0.5)
     post, pre = 1 + weights(hidden, std=0.1), 1 + weights(hidden, std=0.1)
     gate = weights(hidden, std=0.1) + 0.5
     per = experts // ranks
@@ -81,6 +82,6 @@ def train(rows=512, cols=2048, ranks=2, steps=4, lr=0.02, seed=0):
 
 if __name__ == "__main__":
     stream, normed = decode()
-    print("decode: stream %s, rms %.4f; next input rms %.4f" % (tuple(stream.shape), stream.float().square().mean().sqrt(),
-                                                                 normed.float().square().mean().sqrt()))
+    rms = [float(t.float().square().mean().sqrt()) for t in (stream, normed)]
+    print("decode: stream %s, rms %.4f; next input rms %.4f" % (tuple(stream.shape), *rms))
     print("train: loss " + ", ".join("%.4f" % v for v in train()))

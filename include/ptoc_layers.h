@@ -14,7 +14,9 @@
  * PTOC_ERR_UNSUPPORTED). Sums, norm statistics and gradients of weights are
  * held in binary32; an element is rounded once, when it is stored.
  * Results do not depend on scheduling: the same call on the same GPU gives
- * the same bits.
+ * the same bits. Rows are fastest where bases are 16-byte aligned, pitches too
+ * and rows of whole 16-byte words; an odd pitch alone costs up to half the
+ * speed, odd bases more.
  */
 #ifndef PTOC_LAYERS_H
 #define PTOC_LAYERS_H
@@ -179,9 +181,15 @@ typedef struct {
  * w_e * silu(..) * (..) are rounded once to dtype before the second product.
  * ids ([tokens, top_k] int32) and weights ([tokens, top_k] floats) may be null.
  * dtype is PTOC_F16 or PTOC_BF16 (PTOC_F32 is PTOC_ERR_UNSUPPORTED).
+ * An f16 activation beyond 65504 becomes infinite. Tokens share the products
+ * of the experts that any of them chose: an infinity or a NaN in such an
+ * expert's w_out reaches the other tokens too (one in x stays with its token).
  * y must not overlap an input. tokens, experts or top_k above the limits are
- * PTOC_ERR_UNSUPPORTED. Rows of 16-byte aligned multiples of 8 elements
- * (hidden and inter) take the tensor-core kernel, others a plain one.
+ * PTOC_ERR_UNSUPPORTED. 16-byte aligned x, router and weights with hidden and
+ * inter multiples of 8 take the tensor-core kernel: one cooperative launch,
+ * whose waits for copies are bounded by PTOC_WAIT_NS (ptoc.h) and counted by
+ * ptoc_wait_faults if they give up (part of y is then missing). Others take
+ * plain kernels.
  */
 size_t ptoc_moe_few_tokens_workspace(int64_t tokens, int64_t hidden, int64_t inter, int32_t experts, int32_t top_k);
 ptoc_status ptoc_moe_few_tokens(const ptoc_matrix* x, const ptoc_moe_params* params, const ptoc_matrix* y,

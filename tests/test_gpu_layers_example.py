@@ -55,7 +55,7 @@ def test_training_lowers_the_loss():
 
 
 def test_command():
-    r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "layer_step.py")], capture_output=True, text=True,
-                       timeout=300)
+    r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "layer_step.py")], capture_output=True,
+                       text=True, timeout=300)
     assert r.returncode == 0, r.stderr
     assert "decode: stream (5, 1024)" in r.stdout and "train: loss" in r.stdout

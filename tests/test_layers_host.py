@@ -208,7 +208,8 @@ def test_conveniences_refuse_what_the_calls_cannot_describe():
                dict(pre_weight=torch.zeros(64), post_weight=torch.zeros(64, dtype=torch.bfloat16)),
                dict(pre_weight=torch.zeros(128, dtype=torch.bfloat16)[::2]), dict(rstd=torch.zeros(4)),
                dict(stream_ckpt=P.Checkpoint8(4, 32, device="cpu")),
-               dict(post_weight=torch.zeros(64, dtype=torch.bfloat16), post_norm=False), dict(normed=t(4, 128)[:, ::2])):
+               dict(post_weight=torch.zeros(64, dtype=torch.bfloat16), post_norm=False),
+               dict(normed=t(4, 128)[:, ::2])):
         args = dict(dict(parts=[t()], residual=t()), **kw)
         with pytest.raises(ValueError):
             P.block_norm(args.pop("parts"), args.pop("residual"), t(), **args)

@@ -16,9 +16,18 @@
 // Bound by HBM: per element it reads dy, du, s and a (the last two in 2 or 4
 // bytes, or 33/32 as 8-bit checkpoints) and writes d_residual and d_block.
 // One wave of blocks walks the rows with the two column sums in registers;
-// copies of the next rows are queued in shared memory by each thread for
-// itself, as in the forward pass. Each block writes its column sums as one
-// partial row, and a second launch adds the partial rows in order.
+// copies of the next row are queued in shared memory, as in the forward pass.
+// Each block writes its column sums as one partial row, and a second launch
+// adds the partial rows in order (about 4 us).
+//
+// Measured on GB300 (bf16, both launches; of 6.68 TB/s copied): 8192 x 4096
+// from checkpoints 73 us (4.6 TB/s), from matrices 76 us (5.3 TB/s); 16384 x
+// 8192 from checkpoints 247 us (5.5 TB/s); f32 8192 x 4096 128 us (6.3 TB/s).
+// With 16-bit elements and codes the issue rate comes before HBM: 700
+// instructions per thread and row of 16 columns, 57 % of the issue slots at 16
+// warps per SM, which the registers allow (two column sums, three arrays of
+// the row: 120). One chunk per thread in 64 registers took 96 us, four chunks
+// in 255 registers 104 us, where two took 81.
 #include "layers/layers_common.cuh"
 #include "layers/layers_internal.h"
 
@@ -282,7 +291,10 @@ struct Header {
         }
         __syncthreads();
     }
-    static __device__ __forceinline__ uint32_t scale_bits(uint32_t byte) { return __float_as_uint(ckpt_scale(byte)) >> 16; }
+    static __device__ __forceinline__ uint32_t scale_bits(uint32_t byte)
+    {
+        return __float_as_uint(ckpt_scale(byte)) >> 16;
+    }
     // Words of four bytes where the checkpoint's rows allow them, several in
     // flight per thread: a batch costs about 1 us, byte by byte about 4.
     __device__ __forceinline__ void load_scales(int which, const ptoc_ckpt8& k, int64_t row, uint32_t rows)
@@ -294,13 +306,13 @@ struct Header {
             constexpr int kAtOnce = 4;
             const uint32_t i0 = threadIdx.x / words, w = threadIdx.x - i0 * words, step = blockDim.x / words;
             if (i0 >= step) return;
+            const uint8_t* from = k.exps + row * k.ld_exps + 4 * w;
             for (uint32_t i = i0; i < rows; i += kAtOnce * step) {
                 uint32_t v[kAtOnce];
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q)
                     v[q] = i + q * step < rows
-                               ? *(const uint32_t*)(k.exps + (row + (int64_t)(i + q * step) * gridDim.x) * k.ld_exps + 4 * w)
-                               : 0u;
+                               ? *(const uint32_t*)(from + (int64_t)(i + q * step) * gridDim.x * k.ld_exps) : 0u;
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q)
                     if (i + q * step < rows)
@@ -421,7 +433,10 @@ struct QueueLoader {
     }
     __device__ __forceinline__ void begin_dy() { begin(p.ld_dy, sizeof(T)); }
     __device__ __forceinline__ void begin_du() { begin(p.ld_du, sizeof(T)); }
-    __device__ __forceinline__ void begin_block() { begin(CKPT ? p.block_ckpt.ld_codes : p.ld_block, CKPT ? 1 : sizeof(T)); }
+    __device__ __forceinline__ void begin_block()
+    {
+        begin(CKPT ? p.block_ckpt.ld_codes : p.ld_block, CKPT ? 1 : sizeof(T));
+    }
     __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i, shift); }
     __device__ __forceinline__ F8 saved(int i, int which, float factor) const
     {
@@ -439,7 +454,8 @@ struct QueueLoader {
             }
             Pair by[ODD ? 4 : kRuns];
 #pragma unroll
-            for (int q = 0; q < (ODD ? 4 : kRuns); ++q) by[q] = ODD ? pair(scale[2 * q % kRuns], scale[(2 * q + 1) % kRuns]) : both(scale[q]);
+            for (int q = 0; q < (ODD ? 4 : kRuns); ++q)
+                by[q] = ODD ? pair(scale[2 * q % kRuns], scale[(2 * q + 1) % kRuns]) : both(scale[q]);
             f = code_values<G>(w, by);
         } else {
             f = queue.chunk(i, shift).expand();

@@ -4,6 +4,11 @@
 // Bound by HBM: 2 or 4 bytes per element in, 33/32 out (and back). One thread
 // holds 8 columns; a warp covers 256 columns of one row, so a block's largest
 // magnitude is two lane exchanges away and nothing is read twice.
+//
+// Measured on GB300 (of 6.68 TB/s copied): 16384 x 8192 bf16 kept in 64 us (6.3
+// TB/s), restored in 60 us (6.8 TB/s); with one 256-column unit per warp instead
+// of four, and integer conversions, 105 and 147 us. At 8191 columns, element by
+// element, 153 and 138 us: 8 loads or stores where an aligned row takes one.
 #include "layers/layers_common.cuh"
 #include "layers/layers_internal.h"
 
