@@ -181,9 +181,9 @@ typedef struct {
  * w_e * silu(..) * (..) are rounded once to dtype before the second product.
  * ids ([tokens, top_k] int32) and weights ([tokens, top_k] floats) may be null.
  * dtype is PTOC_F16 or PTOC_BF16 (PTOC_F32 is PTOC_ERR_UNSUPPORTED).
- * An f16 activation beyond 65504 becomes infinite. Tokens share the products
- * of the experts that any of them chose: an infinity or a NaN in such an
- * expert's w_out reaches the other tokens too (one in x stays with its token).
+ * An f16 activation beyond 65504 becomes infinite. An infinity or a NaN in x
+ * stays with its token, and one in an expert's weights with the tokens that
+ * chose the expert.
  * y must not overlap an input. tokens, experts or top_k above the limits are
  * PTOC_ERR_UNSUPPORTED. 16-byte aligned x, router and weights with hidden and
  * inter multiples of 8 take the tensor-core kernel: one cooperative launch,

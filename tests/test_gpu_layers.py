@@ -596,6 +596,42 @@ def test_moe_nan_and_infinite_logits_choose_valid_experts():
     assert bool(torch.isnan(y[1]).all())
 
 
+@pytest.mark.parametrize("tokens, hidden, inter, first, local", [
+    (1, 64, 64, 0, 4), (5, 512, 320, 0, 8), (40, 4096, 128, 2, 4), (20, 40960, 64, 0, 8), (9, 100, 36, 0, 8)])
+def test_moe_infinite_and_nan_weights_stay_with_their_expert(tokens, hidden, inter, first, local):
+    """Only tokens that chose the expert see what its w_out holds; the products
+    of all tokens are taken together, in tiles that one block sums or several."""
+    g, t, experts, k = gen(hidden + tokens), torch.bfloat16, 8, 2
+    x, router = rnd(g, (tokens, hidden), t), rnd(g, (experts, hidden), t, 0.1)
+    w_in = rnd(g, (local, 2 * inter, hidden), t, 1 / math.sqrt(hidden))
+    w_out = rnd(g, (local, hidden, inter), t, 1 / math.sqrt(inter))
+    layer = P.MoeLayer(router, w_in, w_out, k, first_expert=first)
+    ids = torch.empty(tokens, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(tokens, k, device="cuda")
+    clean, y = torch.empty_like(x), torch.empty_like(x)
+    layer(x, clean, ids=ids, weights=w, workspace=layer.workspace(tokens))
+    w_out[1, 3::5, inter // 2] = float("nan")
+    w_out[2, 4::5, inter - 1] = float("inf")
+    layer(x, y, workspace=layer.workspace(tokens))
+    # sizes of the sums, for the binary32 roundings of a sum in another order
+    size = torch.zeros(tokens, hidden, dtype=torch.float64, device="cuda")
+    hit = torch.zeros(tokens, local, dtype=torch.bool, device="cuda")
+    for e in range(local):
+        of = torch.where(ids == first + e, w, torch.zeros_like(w)).sum(1).double()
+        hit[:, e] = (ids == first + e).any(1)
+        a = x.double() @ w_in[e].double().t()
+        h = (of[:, None] * torch.nn.functional.silu(a[:, :inter]) * a[:, inter:]).abs()
+        size += 1.02 * h @ w_out[e].nan_to_num(nan=1.0, posinf=1.0).double().abs().t()
+    nan_cols = torch.zeros(hidden, dtype=torch.bool, device="cuda")
+    inf_cols = nan_cols.clone()
+    nan_cols[3::5], inf_cols[4::5] = True, True
+    gone = hit[:, 1:2] & nan_cols | hit[:, 2:3] & inf_cols
+    assert torch.equal(~torch.isfinite(y), gone)
+    assert torch.equal(torch.isnan(y) & nan_cols, hit[:, 1:2] & nan_cols)
+    keep = lambda v: torch.where(gone, torch.zeros_like(v), v)
+    close(keep(y), keep(clean).double(), 2 * (k * inter + 8) * E * size + 2 * U[t] * clean.double().abs(), "y")
+
+
 def test_moe_parts_of_expert_parallel_ranks_add_up():
     """Each rank's y is its part: block_norm over the ranks' parts equals
     block_norm over the whole layer's output, to the parts' rounding."""

@@ -439,6 +439,39 @@ __device__ __forceinline__ void store4(T* row, int64_t col, int64_t n, const flo
         if (col + j < n) row[col + j] = from_f32<T>(e[j]);
 }
 
+// y of one token and column from the token's own experts alone. NaN is final:
+// a token whose own activations are NaN ends the loop at once.
+template <class T, int N>
+__device__ __noinline__ float own_sum(const MoeTensorParams& p, const Shared& sh, int t, int64_t col)
+{
+    const MoeParams& m = p.m;
+    float sum = 0.0f;
+    for (int a = 0; a < sh.active; ++a) {
+        float w;
+        if (!chosen(m, sh, t, m.first + sh.expert[a], w)) continue;
+        const unsigned short* h = (const unsigned short*)p.act + ((int64_t)a * N + t) * m.inter;
+        const T* row = (const T*)m.w_out + ((int64_t)sh.expert[a] * m.hidden + col) * m.inter;
+        for (int64_t i = 0; i < m.inter && sum == sum; ++i)
+            sum = fmaf(to_f32(bitcast<T>((uint16_t)__ldcg(h + i))), to_f32(row[i]), sum);
+    }
+    return sum;
+}
+
+// The sums of phase 2 run over the experts of all tokens, with an activation
+// of 0 for those that a token did not choose: an infinity or a NaN in the
+// w_out of such an expert makes them NaN. So sums that are not finite (in
+// `sums`, which is NaN then: 0 times each of them) are taken again, for tokens
+// [t0, t1) of a column that this thread has stored.
+template <class T, int N>
+__device__ __forceinline__ void mend(const MoeTensorParams& p, const Shared& sh, float sums, int t0, int t1, int64_t col)
+{
+    if (sums == 0.0f) return;
+    for (int t = t0; t < t1; ++t) {
+        T* y = (T*)p.m.y + t * p.m.ld_y + col;
+        if (!isfinite(to_f32(*y))) *y = from_f32<T>(own_sum<T, N>(p, sh, t, col));
+    }
+}
+
 template <class T, int N>
 __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_constant__ MoeTensorParams p)
 {
@@ -655,11 +688,18 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                                     from_f32<T>(sh.chosen[t] ? activation(sh.row_weight[t], lo[n], hi[n]) : 0.0f);
                             });
                     } else {
-                        T* to = (T*)m.y + n0 * m.ld_y + col0 + row;
-                        if (col0 + row < m.hidden) each<16>(count, [&](int n) { to[n * m.ld_y] = from_f32<T>(lo[n]); });
-                        to += kHalfRows;
-                        if (col0 + kHalfRows + row < m.hidden)
-                            each<16>(count, [&](int n) { to[n * m.ld_y] = from_f32<T>(hi[n]); });
+                        auto put = [&](const float (&v)[16], int64_t col) {
+                            if (col >= m.hidden) return;
+                            T* to = (T*)m.y + n0 * m.ld_y + col;
+                            float sums = 0.0f;
+                            each<16>(count, [&](int n) {
+                                to[n * m.ld_y] = from_f32<T>(v[n]);
+                                sums = fmaf(0.0f, v[n], sums);
+                            });
+                            mend<T, N>(p, sh, sums, n0, min(n0 + 16, m.tokens), col);
+                        };
+                        put(lo, col0 + row);
+                        put(hi, col0 + kHalfRows + row);
                     }
                 }
                 fence_before();
@@ -685,9 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             float4 lo, hi;
             add_parts(p, part.c0, part.c1, t, quad, lo, hi);
             T* y = (T*)m.y + t * m.ld_y;
-            const int64_t col = (int64_t)part.tile * kTileRows + quad;
-            store4(y, col, m.hidden, lo);
-            store4(y, col + kHalfRows, m.hidden, hi);
+            auto put = [&](const float4& v, int64_t col) {
+                store4(y, col, m.hidden, v);
+                const float sums = 0.0f * v.x + 0.0f * v.y + 0.0f * v.z + 0.0f * v.w;
+                for (int j = 0; j < 4 && col + j < m.hidden; ++j) mend<T, N>(p, sh, sums, t, t + 1, col + j);
+            };
+            put(lo, (int64_t)part.tile * kTileRows + quad);
+            put(hi, (int64_t)part.tile * kTileRows + kHalfRows + quad);
         }
     }
 
