@@ -32,7 +32,7 @@ __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
 // The columns' factor of the norm after the block: its weight, times
 // branch_scale * gate where the gate varies along the columns.
 template <class T, int G>
-__device__ __forceinline__ F8 column_factor(const NormCommon& k, int64_t row, uint32_t col, uint32_t mask)
+__device__ __forceinline__ F8 column_factor(const NormCommon& k, int64_t row, int32_t col, uint32_t mask)
 {
     F8 w = load_param8<T, G>(k.post_weight, k.param_f32, col, mask);
     if (k.gate_cs) {
@@ -44,12 +44,29 @@ __device__ __forceinline__ F8 column_factor(const NormCommon& k, int64_t row, ui
     return w;
 }
 
+template <int C>
+__device__ __forceinline__ float square_sum(const F8 (&a)[C])
+{
+    Pair sum[2 * C];                        // (short chains of dependent operations)
+#pragma unroll
+    for (int i = 0; i < 2 * C; ++i) {
+        const Pair u = a[i / 2].p[2 * (i & 1)], v = a[i / 2].p[2 * (i & 1) + 1];
+        sum[i] = fma2(u, u, mul2(v, v));
+    }
+#pragma unroll
+    for (int n = C; n > 0; n /= 2)
+#pragma unroll
+        for (int i = 0; i < n; ++i) sum[i] = add2(sum[i], sum[i + n]);
+    return sum_of(sum[0]);
+}
+
 // What follows the sum of the parts, for one row in registers: a (the sum) and
 // x of C chunks. KEEP: the column factors are in gw and wpre for all rows;
-// else they are loaded for each row.
-template <class T, int G, int C, bool KEEP>
+// else they are loaded for each row. FULL: a norm after the block, both
+// checkpoints and `normed`, but no matrix of the block output are asked for.
+template <class T, int G, int C, bool KEEP, bool FULL = false>
 __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 (&a)[C], const Raw8<T, G> (&x)[C],
-                                           const uint32_t (&col)[C], const uint32_t (&mask)[C],
+                                           const int32_t (&col)[C], const uint32_t (&mask)[C],
                                            const F8 (&gw)[KEEP ? C : 1], const F8 (&wpre)[KEEP ? C : 1],
                                            float gate, SumSlots<1>& sums)
 {
@@ -57,24 +74,25 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
     const Ckpt bc{p.block_ckpt.codes, p.block_ckpt.exps, p.block_ckpt.ld_codes, p.block_ckpt.ld_exps};
     const Ckpt sc{p.stream_ckpt.codes, p.stream_ckpt.exps, p.stream_ckpt.ld_codes, p.stream_ckpt.ld_exps};
     const float row_gate = k.gate_cs ? 1.0f : k.branch_scale * gate;
-    float ra = 1.0f;
-    if (k.post_norm) {
-        Pair sum = 0;
+    float ra = 1.0f, total[1];
+    if (FULL || k.post_norm) {
+        total[0] = square_sum(a);
+        sums.begin(total);
+    }
+    if (!FULL && p.block_out)
 #pragma unroll
-        for (int i = 0; i < C; ++i)
+        for (int i = 0; i < C; ++i) store8<T, G>((T*)p.block_out + row * p.ld_block, col[i], mask[i], a[i]);
+    if (FULL || bc.codes)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sum = fma2(a[i].p[j], a[i].p[j], sum);
-        float total[1] = {sum_of(sum)};
-        sums.sum(total);
+        for (int i = 0; i < C; ++i) ckpt_store8<G>(bc, row, col[0], i, mask[i], a[i]);
+    if (FULL || k.post_norm) {
+        sums.end(total);
         ra = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     }
     const Pair scale = both(ra * row_gate), keep = both(k.residual_scale);
-    Pair sq = 0;
     Raw8<T, G> s[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        if (p.block_out) store8<T, G>((T*)p.block_out + row * p.ld_block, col[i], mask[i], a[i]);
-        if (bc.codes) ckpt_store8<G>(bc, row, col[i], mask[i], a[i]);
         F8 w;
         if constexpr (!KEEP) w = column_factor<T, G>(k, row, col[i], mask[i]);
         const F8 r = x[i].expand();
@@ -82,23 +100,26 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
         for (int j = 0; j < 4; ++j) {
             const Pair n = mul2(mul2(a[i].p[j], scale), KEEP ? gw[KEEP ? i : 0].p[j] : w.p[j]);
             a[i].p[j] = fma2(keep, r.p[j], n);
-            sq = fma2(a[i].p[j], a[i].p[j], sq);
         }
         s[i] = round8<T, G>(a[i]);
         store8<T, G>((T*)p.out + row * p.ld_out, col[i], mask[i], s[i]);
     }
-    if (sc.codes)
+    const bool statistic = FULL || p.normed || p.rstd;
+    if (statistic) {
+        total[0] = square_sum(a);
+        sums.begin(total);
+    }
+    if (FULL || sc.codes)
 #pragma unroll
-        for (int i = 0; i < C; ++i) ckpt_store8<G>(sc, row, col[i], mask[i], s[i].expand());
-    if (!p.normed && !p.rstd) return;
-    float total[1] = {sum_of(sq)};
-    sums.sum(total);
+        for (int i = 0; i < C; ++i) ckpt_store8<G>(sc, row, col[0], i, mask[i], s[i].expand());
+    if (!statistic) return;
+    sums.end(total);
     const float r = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     if (p.rstd && threadIdx.x == 0) {
         p.rstd[row] = ra;
         p.rstd[k.rows + row] = r;
     }
-    if (!p.normed) return;
+    if (!FULL && !p.normed) return;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         F8 w;
@@ -111,8 +132,11 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
 
 // Through the warps' queues of K items. KEEP: the column factors stay in
 // registers (they do not depend on the row, and two chunks leave room for them).
-template <class T, int C, int K, bool KEEP, bool ODD>
-__global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(const NormParams p)
+// The bound of one block per SM keeps the compiler from saving registers that
+// nothing else would use: 8192 x 4096 with both checkpoints takes 58 us with 95
+// registers and 70 with 82.
+template <class T, int C, int K, bool KEEP, bool ODD, bool FULL = false>
+__global__ void __launch_bounds__(C == 2 ? 512 : 1024, 1) block_norm_queue_kernel(const NormParams p)
 {
     constexpr int G = ODD ? 1 : kVector<T>;
     pdl_enter();
@@ -120,14 +144,15 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
     __shared__ __align__(16) float slots[2 * 32];
     SumSlots<1> sums(slots);
     const NormCommon& k = p.c;
-    Queue<T, C, K, ODD> queue(smem);
-    uint32_t col[C], mask[C];
+    int32_t col[C];
+    uint32_t mask[C];
     F8 gw[KEEP ? C : 1], wpre[KEEP ? C : 1];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        col[i] = first_col<G>(i);
+        col[i] = first_col<G, C>(i);
         mask[i] = runs_below<G>(col[i], k.cols);
     }
+    Queue<T, C, K, ODD> queue(smem, mask);
     // the item to copy next: source `src` (nparts: the residual) of row `ahead`
     int64_t ahead = blockIdx.x, part_at = ahead * p.ld_part;
     const T* x_row = (const T*)p.x + ahead * p.ld_x;
@@ -142,8 +167,8 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
                 queue.copy_row(x_row, col, mask, k.cols);
                 src = 0;
                 ahead += gridDim.x;
-                part_at += gridDim.x * p.ld_part;
-                x_row += gridDim.x * p.ld_x;
+                part_at += p.step_part;
+                x_row += p.step_x;
             }
         }
         queue.next();
@@ -183,7 +208,7 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_queue_kernel(c
 #pragma unroll
         for (int i = 0; i < C; ++i) x[i] = queue.chunk(i, x_shift);
         push();
-        finish_row<T, G, C, KEEP>(p, row, a, x, col, mask, gw, wpre, gate, sums);
+        finish_row<T, G, C, KEEP, FULL>(p, row, a, x, col, mask, gw, wpre, gate, sums);
         gate = next_gate;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -198,10 +223,11 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) block_norm_kernel(const N
     __shared__ __align__(16) float slots[2 * 32];
     SumSlots<1> sums(slots);
     const NormCommon& k = p.c;
-    uint32_t col[C], mask[C];
+    int32_t col[C];
+    uint32_t mask[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        col[i] = first_col<1>(i);
+        col[i] = first_col<1, C>(i);
         mask[i] = runs_below<1>(col[i], k.cols);
     }
     for (int64_t row = blockIdx.x; row < k.rows; row += gridDim.x) {
@@ -239,11 +265,18 @@ cudaError_t launch_queue(const NormParams& p, cudaStream_t s)
     const dim3 grid((unsigned)(p.c.rows < most ? p.c.rows : most));
     const bool keep = C == 2 && !(p.c.gate_cs && p.c.gate_rs);
     auto kernel = keep ? block_norm_queue_kernel<T, C, K, C == 2, ODD> : block_norm_queue_kernel<T, C, K, false, ODD>;
+    // what a training step asks for, without branches around its parts (16384 x
+    // 8192: 212 us instead of 225; 8192 x 4096 the same)
+    if (keep && !ODD && p.c.post_norm && p.block_ckpt.codes && p.stream_ckpt.codes && p.normed && !p.block_out)
+        kernel = block_norm_queue_kernel<T, C, K, C == 2, ODD, C == 2 && !ODD>;
+    NormParams q = p;
+    q.step_part = grid.x * p.ld_part;
+    q.step_x = grid.x * p.ld_x;
     using Q = Queue<T, C, K, ODD>;
     const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)Q::bytes(C == 2 ? 512 : 1024));
     if (e != cudaSuccess) return e;
-    return launch_kernel(kernel, grid, threads, Q::bytes(threads), s, p);
+    return launch_kernel(kernel, grid, threads, Q::bytes(threads), s, q);
 }
 
 template <class T>

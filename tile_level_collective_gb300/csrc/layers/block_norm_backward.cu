@@ -43,7 +43,7 @@ __device__ __forceinline__ float gate_of_row(const NormCommon& k, int64_t row)
 }
 
 template <class T, int G>
-__device__ __forceinline__ F8 gate8(const NormCommon& k, int64_t row, uint32_t col, uint32_t mask)
+__device__ __forceinline__ F8 gate8(const NormCommon& k, int64_t row, int32_t col, uint32_t mask)
 {
     return load_param8<T, G>((const char*)k.gate + row * k.gate_rs * (k.param_f32 ? 4 : (int)sizeof(T)), k.param_f32,
                              col, mask);
@@ -54,9 +54,9 @@ __device__ __forceinline__ F8 gate8(const NormCommon& k, int64_t row, uint32_t c
 template <class T, int G, int C, bool KEEP>
 struct Columns {
     const NormCommon& k;
-    const uint32_t (&col)[C];
+    const int32_t (&col)[C];
     const uint32_t (&mask)[C];
-    uint32_t kept;                          // [2][C][2][threads] 16-byte words: wpre, then the factor
+    uint32_t kept;                          // [2][C][2][32] 16-byte words of the warp: wpre, then the factor
 
     __device__ __forceinline__ F8 pre(int i) const
     {
@@ -79,7 +79,7 @@ struct Columns {
         }
         return w;
     }
-    __device__ __forceinline__ uint32_t word(int n) const { return kept + (uint32_t)(n * 16) * blockDim.x; }
+    __device__ __forceinline__ uint32_t word(int n) const { return kept + (uint32_t)n * 512; }
     __device__ __forceinline__ F8 read(int n) const
     {
         F8 f;
@@ -112,7 +112,7 @@ __device__ __forceinline__ void back_row(const NormBackParams& p, int64_t row, L
                                          float& sum_scalar, SumSlots<3>& sums)
 {
     const NormCommon& k = p.c;
-    const uint32_t (&col)[C] = cols.col;
+    const int32_t (&col)[C] = cols.col;
     const uint32_t (&mask)[C] = cols.mask;
     const RowScalars at = in.begin_row(row);
     F8 st[C], v[C], ah[C];
@@ -223,7 +223,7 @@ __device__ __forceinline__ void back_row(const NormBackParams& p, int64_t row, L
 
 // This block's partial rows of the column sums.
 template <int G, int C>
-__device__ __forceinline__ void store_sums(const NormBackParams& p, const uint32_t (&col)[C], const uint32_t (&mask)[C],
+__device__ __forceinline__ void store_sums(const NormBackParams& p, const int32_t (&col)[C], const uint32_t (&mask)[C],
                                            const F8 (&sum_pre)[C], const F8 (&sum_q)[C], float sum_scalar)
 {
     const int64_t cols = p.c.cols, plane = (int64_t)gridDim.x * cols;
@@ -257,33 +257,36 @@ constexpr int kHeaderRowsOf = sizeof(T) == 4 ? 16 : 32;
 
 template <int kHeaderRows>
 struct Header {
-    float* values;                          // [3][kHeaderRows]: r, ra, gate
-    uint16_t* scales;                       // [2][kHeaderRows][blocks]: the stream's, the block output's
-    int blocks, turn;
+    float4* values;                         // [kHeaderRows]: r, ra, gate
+    uint16_t* scales;                       // [kHeaderRows][2][width]: the stream's, the block output's
+    int blocks, width, turn;                // of a row; with those past its end up to the last warp's, zeros
+    uint32_t mine;                          // this thread's first scale of the current row
 
-    static constexpr size_t size(int64_t cols)
+    static constexpr size_t size(size_t threads) { return kHeaderRows * (16 + threads * 2); }
+    template <int G>
+    __device__ __forceinline__ Header(const NormCommon& k, unsigned char* smem, std::integral_constant<int, G>)
+        : values((float4*)smem), scales((uint16_t*)(smem + kHeaderRows * 16)), blocks((int)((k.cols + 31) >> 5)),
+          width((int)blockDim.x / 2), turn(kHeaderRows - 1),
+          mine((uint32_t)__cvta_generic_to_shared(scales) +
+               ((threadIdx.x >> 5) * 16 + (G == 1 ? 0 : (threadIdx.x & 31) * G / 32) + 2 * turn * width) * 2)
     {
-        return 3 * kHeaderRows * 4 + (4 * kHeaderRows * (size_t)((cols + 31) / 32) + 15) / 16 * 16;
-    }
-    __device__ __forceinline__ Header(const NormCommon& k, unsigned char* smem)
-        : values((float*)smem), scales((uint16_t*)(smem + 3 * kHeaderRows * 4)), blocks((int)((k.cols + 31) >> 5)),
-          turn(kHeaderRows - 1)
-    {
+        for (int i = threadIdx.x; i < kHeaderRows * width; i += blockDim.x) ((uint32_t*)scales)[i] = 0;
     }
     // Go on to `row`, the next one of this block.
     template <class T, bool CKPT>
     __device__ __forceinline__ void advance(const NormBackParams& p, int64_t row)
     {
+        mine += 4 * width;
         if (++turn < kHeaderRows) return;
         turn = 0;
+        mine -= 4 * kHeaderRows * width;
         __syncthreads();                    // the rows before are done with theirs
         const int64_t left = (p.c.rows - 1 - row) / gridDim.x + 1;
         const uint32_t rows = left < kHeaderRows ? (uint32_t)left : kHeaderRows;
-        for (uint32_t n = threadIdx.x; n < 3 * kHeaderRows; n += blockDim.x) {
-            const int64_t r = row + (int64_t)(n % kHeaderRows) * gridDim.x;
-            if (n % kHeaderRows < rows)
-                values[n] = n < kHeaderRows ? p.rstd[p.c.rows + r]
-                          : n < 2 * kHeaderRows ? (p.c.post_norm ? p.rstd[r] : 1.0f) : gate_of_row<T>(p.c, r);
+        if (threadIdx.x < rows) {
+            const int64_t r = row + (int64_t)threadIdx.x * gridDim.x;
+            values[threadIdx.x] = make_float4(p.rstd[p.c.rows + r], p.c.post_norm ? p.rstd[r] : 1.0f,
+                                              gate_of_row<T>(p.c, r), 0.0f);
         }
         if constexpr (CKPT) {
             load_scales(0, p.stream_ckpt, row, rows);
@@ -299,7 +302,8 @@ struct Header {
     // flight per thread: a batch costs about 1 us, byte by byte about 4.
     __device__ __forceinline__ void load_scales(int which, const ptoc_ckpt8& k, int64_t row, uint32_t rows)
     {
-        uint16_t* to = scales + which * kHeaderRows * blocks;
+        uint16_t* to = scales + which * width;
+        const uint32_t pitch = 2 * (uint32_t)width;
         const uint32_t words = (uint32_t)blocks / 4;
         if (words && words * 4 == (uint32_t)blocks && words <= blockDim.x &&
             (((uintptr_t)k.exps | (uintptr_t)k.ld_exps) & 3u) == 0) {
@@ -316,7 +320,7 @@ struct Header {
 #pragma unroll
                 for (int q = 0; q < kAtOnce; ++q)
                     if (i + q * step < rows)
-                        *(uint2*)(to + (i + q * step) * blocks + 4 * w) =
+                        *(uint2*)(to + (i + q * step) * pitch + 4 * w) =
                             make_uint2(scale_bits(v[q] & 255u) | scale_bits(v[q] >> 8 & 255u) << 16,
                                        scale_bits(v[q] >> 16 & 255u) | scale_bits(v[q] >> 24) << 16);
             }
@@ -332,40 +336,50 @@ struct Header {
             }
 #pragma unroll
             for (int q = 0; q < kAtOnce; ++q)
-                if (n0 + q * blockDim.x < rows * blocks) to[n0 + q * blockDim.x] = (uint16_t)scale_bits(byte[q]);
+            {
+                const uint32_t n = n0 + q * blockDim.x, i = n / (uint32_t)blocks;
+                if (n < rows * blocks) to[i * pitch + (n - i * blocks)] = (uint16_t)scale_bits(byte[q]);
+            }
         }
     }
     __device__ __forceinline__ RowScalars scalars() const
     {
-        return RowScalars{values[kHeaderRows + turn], values[turn], values[2 * kHeaderRows + turn]};
+        const float4 v = values[turn];
+        return RowScalars{v.y, v.x, v.z};
     }
-    __device__ __forceinline__ float scale(int which, uint32_t b) const
+    // Of the block that is n after the thread's first one.
+    __device__ __forceinline__ float scale(int which, int n) const
     {
-        return __uint_as_float((uint32_t)scales[(which * kHeaderRows + turn) * blocks + b] << 16);
+        uint16_t h;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(mine + (which ? 2 * width : 0) + 2 * n) : "memory");
+        return __uint_as_float((uint32_t)h << 16);
     }
 };
 
 // Chunks from the thread's queue. A row has four items: stream, dy, du (empty
-// without du) and block. The queue holds kRows rows of them, so the slot that
-// an item leaves is filled with the same item of the row kRows turns later.
-// CKPT: stream and block are checkpoints; else both are matrices.
-template <class T, int C, int kRows, bool CKPT, bool ODD>
+// without du) and block. Each has a slot, which is filled with the next row's
+// as soon as it has been read. CKPT: stream and block are checkpoints; else
+// both are matrices.
+template <class T, int C, bool CKPT, bool ODD>
 struct QueueLoader {
-    using Q = Queue<T, C, 4 * kRows, ODD>;
+    enum Item { kStream = 0, kDy = 1, kDu = 2, kBlockOut = 3 };
+    using Q = Queue<T, C, 4, ODD>;
     static constexpr int G = Q::G;
     const NormBackParams& p;
     Q queue;
-    const uint32_t (&col)[C];
+    const int32_t (&col)[C];
     const uint32_t (&mask)[C];
     int64_t ahead;                          // the row whose items are copied next
+    bool more;                              // whether there is one
     const char *stream_row, *dy_row, *du_row, *block_row;               // in that row
     uint32_t shift;                         // where the current item's row begins in its words
     uint32_t row;
     Header<kHeaderRowsOf<T>> head;
 
-    __device__ __forceinline__ QueueLoader(const NormBackParams& q, unsigned char* smem, const uint32_t (&c)[C],
+    __device__ __forceinline__ QueueLoader(const NormBackParams& q, unsigned char* smem, const int32_t (&c)[C],
                                            const uint32_t (&m)[C])
-        : p(q), queue(smem), col(c), mask(m), ahead(blockIdx.x), head(q.c, smem + Q::bytes(blockDim.x))
+        : p(q), queue(smem, m), col(c), mask(m), ahead(blockIdx.x), more(ahead < q.c.rows),
+          head(q.c, smem + Q::bytes(blockDim.x), std::integral_constant<int, G>())
     {
         const int64_t row = blockIdx.x;
         stream_row = CKPT ? (const char*)(p.stream_ckpt.codes + row * p.stream_ckpt.ld_codes)
@@ -374,68 +388,57 @@ struct QueueLoader {
                          : (const char*)((const T*)p.block + row * p.ld_block);
         dy_row = (const char*)((const T*)p.dy + row * p.ld_dy);
         du_row = (const char*)((const T*)p.du + row * p.ld_du);
-#pragma unroll 1
-        for (int k = 0; k < kRows; ++k) {
-            end_stream();
-            end_dy();
-            end_du();
-            end_block();
-        }
+        end_stream();
+        end_dy();
+        end_du();
+        end_block();
     }
     __device__ __forceinline__ RowScalars begin_row(int64_t row)
     {
         head.template advance<T, CKPT>(p, row);
         this->row = (uint32_t)row;
-        begin(CKPT ? p.stream_ckpt.ld_codes : p.ld_stream, CKPT ? 1 : sizeof(T));
+        begin(kStream, CKPT ? p.stream_ckpt.ld_codes : p.ld_stream, CKPT ? 1 : sizeof(T));
         return head.scalars();
     }
-    // The next item's slot: wait for it.
-    __device__ __forceinline__ void begin(int64_t ld, uint32_t size)
+    // The next item: wait for it.
+    __device__ __forceinline__ void begin(Item item, int64_t ld, uint32_t size)
     {
+        queue.go(item);
         queue.wait();
         if constexpr (ODD) shift = row * (uint32_t)ld * size & 15u;
     }
-    __device__ __forceinline__ void push(const char*& at, int64_t ld)
-    {
-        queue.done();
-        if (ahead < p.c.rows) {
-            queue.copy_row((const T*)at, col, mask, p.c.cols);
-            at += gridDim.x * ld * (int64_t)sizeof(T);
-        }
-        queue.next();
-    }
-    __device__ __forceinline__ void push_codes(const char*& at, int64_t ld)
-    {
-        queue.done();
-        if (ahead < p.c.rows) {
-            queue.copy_codes((const int8_t*)at, col, mask, p.c.cols);
-            at += gridDim.x * ld;
-        }
-        queue.next();
-    }
     // An item is read: its slot takes the next of its kind.
-    __device__ __forceinline__ void end_stream()
+    __device__ __forceinline__ void push(Item item, const char*& at, int64_t step)
     {
-        if constexpr (CKPT) push_codes(stream_row, p.stream_ckpt.ld_codes);
-        else push(stream_row, p.ld_stream);
+        queue.go(item);
+        queue.done();
+        if (more) {
+            if (CKPT && (item == kStream || item == kBlockOut))
+                queue.copy_codes((const int8_t*)at, col, mask, p.c.cols);
+            else
+                queue.copy_row((const T*)at, col, mask, p.c.cols);
+            at += step;
+        }
+        queue.commit();
     }
-    __device__ __forceinline__ void end_dy() { push(dy_row, p.ld_dy); }
+    __device__ __forceinline__ void end_stream() { push(kStream, stream_row, p.step_stream); }
+    __device__ __forceinline__ void end_dy() { push(kDy, dy_row, p.step_dy); }
     __device__ __forceinline__ void end_du()
     {
-        if (p.du) push(du_row, p.ld_du);
-        else queue.next();
+        if (p.du) push(kDu, du_row, p.step_du);
+        else queue.commit();
     }
     __device__ __forceinline__ void end_block()
     {
-        if constexpr (CKPT) push_codes(block_row, p.block_ckpt.ld_codes);
-        else push(block_row, p.ld_block);
+        push(kBlockOut, block_row, p.step_block);
         ahead += gridDim.x;
+        more = ahead < p.c.rows;
     }
-    __device__ __forceinline__ void begin_dy() { begin(p.ld_dy, sizeof(T)); }
-    __device__ __forceinline__ void begin_du() { begin(p.ld_du, sizeof(T)); }
+    __device__ __forceinline__ void begin_dy() { begin(kDy, p.ld_dy, sizeof(T)); }
+    __device__ __forceinline__ void begin_du() { begin(kDu, p.ld_du, sizeof(T)); }
     __device__ __forceinline__ void begin_block()
     {
-        begin(CKPT ? p.block_ckpt.ld_codes : p.ld_block, CKPT ? 1 : sizeof(T));
+        begin(kBlockOut, CKPT ? p.block_ckpt.ld_codes : p.ld_block, CKPT ? 1 : sizeof(T));
     }
     __device__ __forceinline__ Raw8<T, G> matrix(int i) const { return queue.chunk(i, shift); }
     __device__ __forceinline__ F8 saved(int i, int which, float factor) const
@@ -444,14 +447,10 @@ struct QueueLoader {
         if constexpr (CKPT) {
             uint32_t w[ODD ? 8 : 2];
             queue.codes(i, shift, w);
-            // a block past the row's end has codes 0; its scale is not read
             constexpr int kRuns = 8 / G;
             float scale[kRuns];
 #pragma unroll
-            for (int q = 0; q < kRuns; ++q) {
-                const uint32_t b = (ODD ? col[i] - queue.lane : col[i]) / 32 + q * G;
-                scale[q] = b < (uint32_t)head.blocks ? head.scale(which, b) * factor : 0.0f;
-            }
+            for (int q = 0; q < kRuns; ++q) scale[q] = head.scale(which, 8 * i + q * G) * factor;
             Pair by[ODD ? 4 : kRuns];
 #pragma unroll
             for (int q = 0; q < (ODD ? 4 : kRuns); ++q)
@@ -470,7 +469,7 @@ struct QueueLoader {
 
 constexpr int kQueueThreads = 512;
 
-template <class T, int kRows, bool CKPT, bool ODD>
+template <class T, bool CKPT, bool ODD>
 __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(const NormBackParams p)
 {
     constexpr int C = 2, G = ODD ? 1 : kVector<T>;
@@ -478,14 +477,16 @@ __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(cons
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ __align__(16) float slots[2 * 3 * 32];
     SumSlots<3> sums(slots);
-    uint32_t col[C], mask[C];
+    int32_t col[C];
+    uint32_t mask[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        col[i] = first_col<G>(i);
+        col[i] = first_col<G, C>(i);
         mask[i] = runs_below<G>(col[i], p.c.cols);
     }
-    QueueLoader<T, C, kRows, CKPT, ODD> in(p, smem + (size_t)blockDim.x * C * 64, col, mask);
-    const Columns<T, G, C, true> cols{p.c, col, mask, (uint32_t)__cvta_generic_to_shared(smem) + threadIdx.x * 16};
+    QueueLoader<T, C, CKPT, ODD> in(p, smem + (size_t)blockDim.x * C * 64, col, mask);
+    const Columns<T, G, C, true> cols{p.c, col, mask, (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * (C * 2048) +
+                                             (threadIdx.x & 31) * 16};
     const Columns<T, G, C, false> memory{p.c, col, mask, 0};
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(cons
 template <class T, int G, int C>
 struct DirectLoader {
     const NormBackParams& p;
-    const uint32_t (&col)[C];
+    const int32_t (&col)[C];
     const uint32_t (&mask)[C];
     int64_t row;
     CkptRaw<G> codes[C];
@@ -559,10 +560,11 @@ __global__ void __launch_bounds__(C == 2 ? 512 : 1024) norm_backward_kernel(cons
     pdl_enter();
     __shared__ __align__(16) float slots[2 * 3 * 32];
     SumSlots<3> sums(slots);
-    uint32_t col[C], mask[C];
+    int32_t col[C];
+    uint32_t mask[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        col[i] = first_col<G>(i);
+        col[i] = first_col<G, C>(i);
         mask[i] = runs_below<G>(col[i], p.c.cols);
     }
     const Columns<T, G, C, false> cols{p.c, col, mask, 0};
@@ -623,28 +625,30 @@ __global__ void __launch_bounds__(kSumThreads) norm_backward_sum_kernel(const No
     }
 }
 
-// The queue form: rows in flight and its rule. Two chunks per thread and 512
-// threads on an SM; wider rows leave no room for a row of copies ahead. (Two
-// rows ahead of 16-bit elements: 8192 x 4096 from matrices 83 us instead of 76,
-// from checkpoints the same.)
-template <class T>
-constexpr int kRowsAhead = 1;
+// The queue form: two chunks per thread and 512 threads on an SM; wider rows
+// leave no room for a row of copies ahead. (Two rows ahead of 16-bit elements:
+// 8192 x 4096 from matrices 83 us instead of 76, from checkpoints the same.)
 constexpr int64_t kQueueCols = kQueueThreads * 16;
 // Shared memory of a block: the columns' parameters, the queues, the header.
 template <class T, bool ODD>
-size_t queue_bytes(int64_t threads, int64_t cols)
+size_t queue_bytes(int64_t threads)
 {
-    return threads * 2 * 64 + Queue<T, 2, 4 * kRowsAhead<T>, ODD>::bytes(threads) +
-           Header<kHeaderRowsOf<T>>::size(cols);
+    return threads * 2 * 64 + Queue<T, 2, 4, ODD>::bytes(threads) + Header<kHeaderRowsOf<T>>::size(threads);
 }
 
 template <class T, bool CKPT, bool ODD>
 cudaError_t launch_queue(const NormBackParams& p, dim3 grid, unsigned threads, cudaStream_t s)
 {
-    auto kernel = norm_backward_queue_kernel<T, kRowsAhead<T>, CKPT, ODD>;
+    auto kernel = norm_backward_queue_kernel<T, CKPT, ODD>;
     const cudaError_t e = cudaFuncSetAttribute((const void*)kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)queue_bytes<T, ODD>(kQueueThreads, kQueueCols));
-    return e == cudaSuccess ? launch_kernel(kernel, grid, threads, queue_bytes<T, ODD>(threads, p.c.cols), s, p) : e;
+                                               (int)queue_bytes<T, ODD>(kQueueThreads));
+    NormBackParams q = p;
+    const int64_t saved = grid.x * (CKPT ? 1 : (int64_t)sizeof(T)), elements = grid.x * (int64_t)sizeof(T);
+    q.step_stream = saved * (CKPT ? p.stream_ckpt.ld_codes : p.ld_stream);
+    q.step_block = saved * (CKPT ? p.block_ckpt.ld_codes : p.ld_block);
+    q.step_dy = elements * p.ld_dy;
+    q.step_du = elements * p.ld_du;
+    return e == cudaSuccess ? launch_kernel(kernel, grid, threads, queue_bytes<T, ODD>(threads), s, q) : e;
 }
 
 template <class T, int G, int C>

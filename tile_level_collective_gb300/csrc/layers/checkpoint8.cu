@@ -28,7 +28,8 @@ __global__ void __launch_bounds__(kBlock) ckpt8_kernel(const Ckpt8Params p)
     const uint32_t unit0 = blockIdx.x * (kUnits * kBlock / 32) + (threadIdx.x >> 5);
     const Ckpt k{p.ckpt.codes, p.ckpt.exps, p.ckpt.ld_codes, p.ckpt.ld_exps};
     int64_t row[kUnits];
-    uint32_t col[kUnits], mask[kUnits];
+    int32_t col[kUnits];
+    uint32_t mask[kUnits];
     Raw8<T, G> raw[kUnits];
     CkptRaw<G> codes[kUnits];
 #pragma unroll
@@ -36,7 +37,7 @@ __global__ void __launch_bounds__(kBlock) ckpt8_kernel(const Ckpt8Params p)
         const uint32_t unit = unit0 + q * (kBlock / 32);
         const uint32_t r = unit / per_row;
         row[q] = r;
-        col[q] = (unit - r * per_row) * 256 + (threadIdx.x & 31) * G;
+        col[q] = (int32_t)((unit - r * per_row) * 256 + (threadIdx.x & 31) * G);
         mask[q] = unit < units ? runs_below<G>(col[q], p.cols) : 0u;
         if constexpr (RESTORE) codes[q] = ckpt_load8<G>(k, row[q], col[q], mask[q]);
         else raw[q] = load8<T, G>((const T*)p.x + row[q] * p.ld, col[q], mask[q]);
@@ -45,7 +46,7 @@ __global__ void __launch_bounds__(kBlock) ckpt8_kernel(const Ckpt8Params p)
     for (int q = 0; q < kUnits; ++q) {
         if (unit0 + q * (kBlock / 32) >= units) break;         // the whole warp
         if constexpr (RESTORE) store8<T, G>((T*)p.x + row[q] * p.ld, col[q], mask[q], ckpt_values<G>(codes[q], 1.0f));
-        else ckpt_store8<G>(k, row[q], col[q], mask[q], raw[q].expand());
+        else ckpt_store8<G>(k, row[q], col[q], 0, mask[q], raw[q].expand());
     }
 }
 

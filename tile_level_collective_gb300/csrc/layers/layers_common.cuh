@@ -78,8 +78,9 @@ struct F8 {
 };
 
 // ---- 8 columns per thread ----------------------------------------------------------------
-// A row is cut into groups of 256 columns, one per warp; a lane holds 8 of
-// them (chunk c = 32 * group + lane) as 8 / G runs of G neighbouring columns:
+// A row is cut into groups of 256 columns, C neighbouring groups to a warp (so
+// that the addresses of a lane's chunks differ by constants); of a group a lane
+// holds a chunk of 8 columns as 8 / G runs of G neighbouring columns:
 // G = 8, one 16-byte word of 16-bit elements; G = 4, two words of binary32;
 // G = 1, element-wide accesses, for rows at any address and of any length. Run
 // q of lane l starts at column 32 * G * q + G * l of the group, so that a warp
@@ -90,16 +91,16 @@ struct F8 {
 template <class T>
 constexpr int kVector = 16 / (int)sizeof(T);
 
-// The first column of lane `threadIdx.x` in the chunk i * blockDim.x + threadIdx.x.
-template <int G>
-__device__ __forceinline__ uint32_t first_col(int i)
+// The first column of this thread's chunk i of C. Signed, so that it is known
+// not to wrap and its constant part stays one in 64-bit addresses.
+template <int G, int C>
+__device__ __forceinline__ int32_t first_col(int i)
 {
-    const uint32_t c = (uint32_t)i * blockDim.x + threadIdx.x;
-    return (c & ~31u) * 8 + (c & 31u) * G;
+    return (int32_t)(threadIdx.x >> 5) * (C * 256) + (int32_t)(threadIdx.x & 31) * G + i * 256;
 }
 // Which of the chunk's runs, from column `col` on, lie below `cols`.
 template <int G>
-__device__ __forceinline__ uint32_t runs_below(uint32_t col, int64_t cols)
+__device__ __forceinline__ uint32_t runs_below(int32_t col, int64_t cols)
 {
     uint32_t m = 0;
 #pragma unroll
@@ -140,7 +141,7 @@ struct Raw8 {
 // outside the mask give zeros. Ordinary loads: the wait for the previous
 // kernel is a barrier for them, which it would not be for read-only loads.
 template <class T, int G>
-__device__ __forceinline__ Raw8<T, G> load8(const T* row, uint32_t col, uint32_t mask)
+__device__ __forceinline__ Raw8<T, G> load8(const T* row, int32_t col, uint32_t mask)
 {
     Raw8<T, G> r;
     const T* p = row + col;
@@ -195,7 +196,7 @@ __device__ __forceinline__ Raw8<T, G> round8(const F8& v)
 }
 
 template <class T, int G>
-__device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, const Raw8<T, G>& r)
+__device__ __forceinline__ void store8(T* row, int32_t col, uint32_t mask, const Raw8<T, G>& r)
 {
     T* p = row + col;
     if constexpr (G == 1) {
@@ -217,7 +218,7 @@ __device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, cons
 }
 
 template <class T, int G>
-__device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, const F8& v)
+__device__ __forceinline__ void store8(T* row, int32_t col, uint32_t mask, const F8& v)
 {
     store8<T, G>(row, col, mask, round8<T, G>(v));
 }
@@ -225,7 +226,7 @@ __device__ __forceinline__ void store8(T* row, uint32_t col, uint32_t mask, cons
 // Parameters (weights, gates) in the mapping of the activations: of their type
 // or binary32; one where null, zero outside the mask.
 template <class T, int G>
-__device__ __forceinline__ F8 load_param8(const void* base, bool f32, uint32_t col, uint32_t mask)
+__device__ __forceinline__ F8 load_param8(const void* base, bool f32, int32_t col, uint32_t mask)
 {
     F8 f;
     if (!base) {
@@ -249,48 +250,51 @@ __device__ __forceinline__ F8 load_param8(const void* base, bool f32, uint32_t c
 // ---- block-wide sums ---------------------------------------------------------------
 
 // Sums of N values over the block, the same bits in every thread: lanes by a
-// fixed exchange tree, then the warps' sums by one. `slot` is shared memory of
-// N * 32 floats that held zeros before the first call; two calls in a row need
-// two slots (one barrier per call).
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float* slot)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (blockDim.x == 32) return;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-        for (int k = 0; k < N; ++k) slot[32 * k + (threadIdx.x >> 5)] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const float4* w = (const float4*)(slot + 32 * k);
-        auto four = [&](int i) {
-            const float4 q = w[i];
-            return (q.x + q.y) + (q.z + q.w);
-        };
-        v[k] = four(0) + four(1);
-        if (blockDim.x > 256) v[k] += four(2) + four(3);
-        if (blockDim.x > 512) v[k] += (four(4) + four(5)) + (four(6) + four(7));
-    }
-}
-
-// The two slots that calls of block_sum take in turn.
+// fixed exchange tree, then the warps' sums by one. `begin` sums over the
+// warp; what is done until `end` hides the wait for the other warps. The
+// slots (2 * N * 32 floats, zeros at first) are taken in turn, so one barrier
+// per sum suffices.
 template <int N>
 struct SumSlots {
-    float* slot;                            // 2 * N * 32 floats
+    float* slot;
     int turn = 0;
     __device__ __forceinline__ explicit SumSlots(float* s) : slot(s)
     {
         for (int i = threadIdx.x; i < 2 * N * 32; i += blockDim.x) s[i] = 0.0f;
         __syncthreads();
     }
+    __device__ __forceinline__ void begin(float (&v)[N])
+    {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int k = 0; k < N; ++k) slot[(turn * N + k) * 32 + (threadIdx.x >> 5)] = v[k];
+    }
+    __device__ __forceinline__ void end(float (&v)[N])
+    {
+        const float* s = slot + turn * N * 32;
+        turn ^= 1;
+        if (blockDim.x == 32) return;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float4* w = (const float4*)(s + 32 * k);
+            auto four = [&](int i) {
+                const float4 q = w[i];
+                return (q.x + q.y) + (q.z + q.w);
+            };
+            v[k] = four(0) + four(1);
+            if (blockDim.x > 256) v[k] += four(2) + four(3);
+            if (blockDim.x > 512) v[k] += (four(4) + four(5)) + (four(6) + four(7));
+        }
+    }
     __device__ __forceinline__ void sum(float (&v)[N])
     {
-        block_sum(v, slot + turn * N * 32);
-        turn ^= 1;
+        begin(v);
+        end(v);
     }
 };
 
@@ -324,11 +328,17 @@ __device__ __forceinline__ float ckpt_scale(uint32_t byte)
 // leaves no fraction bits, so the one rounding is that of the sum.
 constexpr float kCodeBias = 12582912.0f;
 
-// Largest magnitude, or NaN if either is one.
+// Largest magnitude, or NaN if any is one.
 __device__ __forceinline__ float max_abs(float a, float b)
 {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
+}
+__device__ __forceinline__ float max_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -338,41 +348,41 @@ struct Ckpt {
     int64_t ld_codes, ld_exps;
 };
 
-// Write a chunk (zeros outside the mask) of one row. Every lane of the warp
-// takes part, also those whose mask is empty.
+// Write a chunk (zeros outside the mask) of one row: 256 * i columns after
+// column `col0`. Every lane of the warp takes part, also those whose mask is
+// empty.
 template <int G>
-__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, uint32_t col, uint32_t mask, const F8& f)
+__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int32_t col0, int i, uint32_t mask, const F8& f)
 {
-    int8_t* codes = k.codes + row * k.ld_codes + col;
-    uint8_t* exps = k.exps + row * k.ld_exps;
+    int8_t* codes = k.codes + row * k.ld_codes + col0 + 256 * i;
+    uint8_t* exps = k.exps + row * k.ld_exps + 8 * i;
     float v[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split(f.p[i], v[2 * i], v[2 * i + 1]);
     if constexpr (G > 1) {
 #pragma unroll
         for (int q = 0; q < 8 / G; ++q) {
-            float top = max_abs(v[G * q], v[G * q + 1]);
-#pragma unroll
-            for (int j = 2; j < G; ++j) top = max_abs(top, v[G * q + j]);
+            float top = max_abs(v[G * q], v[G * q + 1], v[G * q + 2]);
+            if constexpr (G == 4) top = max_abs(top, v[G * q + 3]);
+            else top = max_abs(max_abs(top, v[3], v[4]), max_abs(v[5], v[6], v[7]));
 #pragma unroll
             for (int o = 1; o < 32 / G; o <<= 1) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o));
             const uint32_t byte = ckpt_exponent(__float_as_uint(top));
             const Pair inv = both(ckpt_inverse(byte)), bias = both(kCodeBias);
             uint32_t w[G / 4];
 #pragma unroll
-            for (int i = 0; i < G / 4; ++i) {
+            for (int n = 0; n < G / 4; ++n) {
                 float c[4];
-                split(fma2(f.p[(G * q + 4 * i) / 2], inv, bias), c[0], c[1]);
-                split(fma2(f.p[(G * q + 4 * i) / 2 + 1], inv, bias), c[2], c[3]);
-                w[i] = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
+                split(fma2(f.p[(G * q + 4 * n) / 2], inv, bias), c[0], c[1]);
+                split(fma2(f.p[(G * q + 4 * n) / 2 + 1], inv, bias), c[2], c[3]);
+                w[n] = __byte_perm(__byte_perm(__float_as_uint(c[0]), __float_as_uint(c[1]), 0x0040),
                                    __byte_perm(__float_as_uint(c[2]), __float_as_uint(c[3]), 0x0040), 0x5410);
-                if (byte == 255u) w[i] = 0u;
+                if (byte == 255u) w[n] = 0u;
             }
             if (mask >> q & 1) {
                 if constexpr (G == 8) *(uint2*)codes = make_uint2(w[0], w[G / 4 - 1]);
                 else *(uint32_t*)(codes + 32 * G * q) = w[0];
-                const uint32_t at = col + q * 32 * G;
-                if ((at & 31u) == 0) exps[at >> 5] = (uint8_t)byte;
+                if ((threadIdx.x & (32 / G - 1)) == 0) exps[(col0 >> 5) + q * G] = (uint8_t)byte;
             }
         }
     } else {
@@ -395,7 +405,7 @@ __device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, uint32_t
                 if (mask >> j & 1) codes[32 * j] = (int8_t)code[j];
         }
         const uint32_t any = __shfl_sync(0xffffffffu, mask, 0);        // a block exists where its first column does
-        if (lane < 8 && (any >> lane & 1)) exps[((col - lane) >> 5) + lane] = (uint8_t)keep;
+        if (lane < 8 && (any >> lane & 1)) exps[((col0 - (int32_t)lane) >> 5) + (int32_t)lane] = (uint8_t)keep;
     }
 }
 
@@ -408,7 +418,7 @@ struct CkptRaw {
 };
 
 template <int G>
-__device__ __forceinline__ CkptRaw<G> ckpt_load8(const Ckpt& k, int64_t row, uint32_t col, uint32_t mask)
+__device__ __forceinline__ CkptRaw<G> ckpt_load8(const Ckpt& k, int64_t row, int32_t col, uint32_t mask)
 {
     const int8_t* codes = k.codes + row * k.ld_codes + col;
     const uint8_t* exps = k.exps + row * k.ld_exps;
@@ -431,7 +441,7 @@ __device__ __forceinline__ CkptRaw<G> ckpt_load8(const Ckpt& k, int64_t row, uin
     if constexpr (G == 1) {
         const uint32_t any = __shfl_sync(0xffffffffu, mask, 0), lane = threadIdx.x & 31;
         r.byte[0] = 0;
-        if (lane < 8 && (any >> lane & 1)) r.byte[0] = exps[((col - lane) >> 5) + lane];
+        if (lane < 8 && (any >> lane & 1)) r.byte[0] = exps[((col - (int32_t)lane) >> 5) + (int32_t)lane];
     } else {
 #pragma unroll
         for (int q = 0; q < 8 / G; ++q) {
@@ -492,10 +502,12 @@ __device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
 // ---- queues of copies in shared memory -----------------------------------------------------
 // Items (C chunks per thread of one row of one tensor) are copied ahead of
 // their use, in the order of their use: K of them are always in flight or
-// waiting. A warp copies and reads the bytes of its own columns only. What
-// lies past the row's end is filled with zeros.
+// waiting. A warp copies and reads the bytes of its own columns only, in a
+// part of the shared memory of its own. What lies past the row's end reads as
+// zeros.
 // Aligned rows (ODD = false): each lane copies and reads its own words, so
-// that its own wait for the copy suffices. Rows at any pitch (ODD; the base is
+// that its own wait for the copy suffices; its words outside the mask are
+// zeroed once and never copied to. Rows at any pitch (ODD; the base is
 // 16-byte aligned): the lanes copy the aligned words that hold the warp's
 // columns, one more than it has, and read elements where the row's address
 // puts them; the lanes then wait for one another too. The word that holds the
@@ -505,17 +517,26 @@ struct Queue {
     static constexpr int G = ODD ? 1 : kVector<T>;
     static constexpr int W = (int)sizeof(T) / 2;             // words of 16 bytes per lane and chunk
     static constexpr uint32_t kChunk = (32 * W + (ODD ? 1 : 0)) * 16;       // bytes per warp
-    static __host__ __device__ constexpr size_t bytes(size_t threads) { return K * C * (threads / 32) * kChunk; }
-    uint32_t at, begin, end;                                 // this warp's current slot; the first; past the last
+    static constexpr uint32_t kItem = C * kChunk, kWarp = K * kItem;
+    static __host__ __device__ constexpr size_t bytes(size_t threads) { return threads / 32 * kWarp; }
+    uint32_t at, first;                                      // the current slot; the first (of this lane, if !ODD)
     uint32_t lane;
 
-    __device__ __forceinline__ Queue(void* smem)
+    __device__ __forceinline__ Queue(void* smem, const uint32_t (&mask)[C])
     {
         lane = threadIdx.x & 31;
-        begin = at = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kChunk;
-        end = begin + (uint32_t)bytes(blockDim.x);
+        first = at = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * kWarp + (ODD ? 0 : lane * 16);
+        if constexpr (!ODD)
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int q = 0; q < W; ++q)
+                    if (!(mask[i] >> q & 1))
+                        for (int n = 0; n < K; ++n)
+                            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                                         ::"r"(first + n * kItem + i * kChunk + q * 512), "r"(0) : "memory");
     }
-    __device__ __forceinline__ uint32_t chunk_at(int i) const { return at + (uint32_t)i * (blockDim.x >> 5) * kChunk; }
+    __device__ __forceinline__ uint32_t chunk_at(int i) const { return at + (uint32_t)i * kChunk; }
     static __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t size)
     {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(size) : "memory");
@@ -529,7 +550,7 @@ struct Queue {
         copy16(dst, word0 + (bytes > 0 ? o : 0), (uint32_t)bytes);
     }
     // Start the copies of this warp's columns of a row of T.
-    __device__ __forceinline__ void copy_row(const T* row, const uint32_t (&col)[C], const uint32_t (&mask)[C],
+    __device__ __forceinline__ void copy_row(const T* row, const int32_t (&col)[C], const uint32_t (&mask)[C],
                                              int64_t cols)
     {
 #pragma unroll
@@ -537,20 +558,21 @@ struct Queue {
             if constexpr (ODD) {
                 const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
                 const int32_t total = (int32_t)((uintptr_t)row & 15) + (int32_t)cols * (int32_t)sizeof(T);
-                const int32_t o = (int32_t)((col[i] - lane) * (uint32_t)sizeof(T) + lane * 16);
+                const int32_t o = (col[i] - (int32_t)lane) * (int32_t)sizeof(T) + (int32_t)lane * 16;
 #pragma unroll
                 for (int q = 0; q <= W; ++q)
                     if (q < W || lane == 0) copy_part(chunk_at(i) + (lane + 32 * q) * 16, word0, o + 512 * q, total);
             } else {
 #pragma unroll
                 for (int q = 0; q < W; ++q)
-                    copy16(chunk_at(i) + (lane + 32 * q) * 16, row + (mask[i] >> q & 1 ? col[i] + 32 * G * q : 0u),
-                           mask[i] >> q & 1 ? 16 : 0);
+                    if (mask[i] >> q & 1)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;"
+                                     ::"r"(chunk_at(i) + 512 * q), "l"(row + col[i] + 32 * G * q) : "memory");
             }
         }
     }
     // The same of a checkpoint's codes (aligned: one word of 8, or two of 4 bytes per lane).
-    __device__ __forceinline__ void copy_codes(const int8_t* row, const uint32_t (&col)[C], const uint32_t (&mask)[C],
+    __device__ __forceinline__ void copy_codes(const int8_t* row, const int32_t (&col)[C], const uint32_t (&mask)[C],
                                                int64_t cols)
     {
 #pragma unroll
@@ -559,25 +581,26 @@ struct Queue {
                 const char* word0 = (const char*)((uintptr_t)row & ~(uintptr_t)15);
                 const int32_t total = (int32_t)((uintptr_t)row & 15) + (int32_t)cols;
                 if (lane < 17)
-                    copy_part(chunk_at(i) + lane * 16, word0, (int32_t)(col[i] - lane + lane * 16), total);
+                    copy_part(chunk_at(i) + lane * 16, word0, col[i] - (int32_t)lane + (int32_t)lane * 16, total);
             } else {
 #pragma unroll
                 for (int q = 0; q < W; ++q)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;"
-                                 ::"r"(chunk_at(i) + (lane + 32 * q) * 16),
-                                 "l"(row + (mask[i] >> q & 1 ? col[i] + 32 * G * q : 0u)),
-                                 "r"(mask[i] >> q & 1 ? G : 0), "n"(ODD ? 8 : G)
-                                 : "memory");
+                    if (mask[i] >> q & 1)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                                     ::"r"(chunk_at(i) + 512 * q), "l"(row + col[i] + 32 * G * q), "n"(ODD ? 8 : G)
+                                     : "memory");
             }
         }
     }
     // The current slot is filled (or left as it is at the end): go on.
     __device__ __forceinline__ void next()
     {
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        at += C * (blockDim.x >> 5) * kChunk;
-        if (at >= end) at -= K * C * (blockDim.x >> 5) * kChunk;
+        commit();
+        at = at == first + kWarp - kItem ? first : at + kItem;
     }
+    // Go to slot n (where the order of the items is known when compiling).
+    __device__ __forceinline__ void go(int n) { at = first + (uint32_t)n * kItem; }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
     // Wait until the oldest item, which lies in the current slot, has landed.
     __device__ __forceinline__ void wait() const
     {
@@ -619,7 +642,7 @@ struct Queue {
             for (int q = 0; q < W; ++q)
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(r.w[4 * q]), "=r"(r.w[4 * q + 1]), "=r"(r.w[4 * q + 2]), "=r"(r.w[4 * q + 3])
-                             : "r"(chunk_at(i) + (lane + 32 * q) * 16)
+                             : "r"(chunk_at(i) + 512 * q)
                              : "memory");
         }
         return r;
@@ -636,12 +659,12 @@ struct Queue {
                          : "r"(from) : "memory");
         } else if constexpr (W == 1) {
             asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
-                         : "=r"(w[0]), "=r"(w[1]) : "r"(chunk_at(i) + lane * 16) : "memory");
+                         : "=r"(w[0]), "=r"(w[1]) : "r"(chunk_at(i)) : "memory");
         } else {
 #pragma unroll
             for (int q = 0; q < W; ++q)
                 asm volatile("ld.shared.u32 %0, [%1];"
-                             : "=r"(w[q]) : "r"(chunk_at(i) + (lane + 32 * q) * 16) : "memory");
+                             : "=r"(w[q]) : "r"(chunk_at(i) + 512 * q) : "memory");
         }
     }
 };

@@ -44,6 +44,7 @@ struct NormParams {
     int64_t ld_out, ld_normed, ld_block;
     ptoc_ckpt8 block_ckpt, stream_ckpt;  // codes null: not written
     float* rstd;                         // may be null
+    int64_t step_part, step_x;           // elements from a block's row to its next one
     int32_t nparts;
 };
 
@@ -61,6 +62,7 @@ struct NormBackParams {
     float* partial;                      // the blocks' column sums: [2][grid, cols], then [grid] scalars
     int32_t gate_kind;                   // GateKind of d_gate
     int32_t need_q;                      // the second column sum is asked for
+    int64_t step_stream, step_block, step_dy, step_du;       // bytes from a block's row to its next one
     int32_t grid;
 };
 
