@@ -53,8 +53,8 @@ typedef struct {
  * depend on how it is computed, and a restored value (code * 2^e) has at most
  * 7 significant bits: it is exact in every element type where it is in that
  * type's range (a value within 2^-7 of the largest float can round up to 2^128
- * and come back as infinity). A block that holds an infinity or a NaN has exponent byte 255 and
- * is restored as NaN. ld_codes >= cols, ld_exps >= ceil(cols / 32). */
+ * and come back as infinity). A block that holds an infinity or a NaN has
+ * exponent byte 255 and is restored as NaN. ld_codes >= cols, ld_exps >= ceil(cols / 32). */
 typedef struct {
     int8_t* codes;
     int64_t ld_codes;
@@ -63,8 +63,8 @@ typedef struct {
 } ptoc_ckpt8;
 
 /* ptoc_checkpoint8 - x [rows, cols] -> out. x and out must not overlap. Both
- * calls take up to 2^31 - 1 pieces of 256 columns (rows * ceil(cols / 256)),
- * else PTOC_ERR_UNSUPPORTED. */
+ * calls take up to 2^31 - 256 columns and 2^31 - 1 pieces of 256 columns (rows
+ * * ceil(cols / 256)), else PTOC_ERR_UNSUPPORTED. */
 ptoc_status ptoc_checkpoint8(const ptoc_matrix* x, const ptoc_ckpt8* out, int64_t rows, int64_t cols,
                              ptoc_dtype dtype, cudaStream_t stream);
 

@@ -677,6 +677,66 @@ def test_moe_recovers_from_waits_that_gave_up(monkeypatch):
     assert P.ptoc_wait_faults() == 0 and torch.equal(got, want)
 
 
+# ---- offsets past 32 bits -----------------------------------------------------------------
+
+def rows_at(pitch, dtype=torch.bfloat16, cols=1000):
+    """Three rows at any pitch, whose memory between them stays untouched."""
+    raw = torch.empty(2 * pitch + cols, dtype=dtype, device="cuda")
+    return torch.as_strided(raw, (3, cols), (pitch, 1))
+
+
+@pytest.mark.parametrize("near, far", [(1008, 2 ** 30 + 8), (1001, 2 ** 30 + 1)])
+def test_rows_past_32_bits_have_the_same_bits(near, far):
+    g, cols = gen(5), 1000
+    given = [rnd(g, (3, cols), torch.bfloat16) for _ in range(4)]
+    w = rnd(g, (cols,), torch.bfloat16, 0.2, 1.0)
+    results = []
+    for pitch in (near, far):
+        part, x, dy, du = (rows_at(pitch).copy_(v) for v in given)
+        out, normed, restored, dx, da = (rows_at(pitch) for _ in range(5))
+        bk, sk, nk = (P.Checkpoint8.of(rows_at(pitch, torch.int8), rows_at(pitch, torch.uint8, 32)) for _ in range(3))
+        rstd, dw = torch.empty(2, 3, device="cuda"), torch.empty(cols, device="cuda")
+        P.block_norm([part], x, out, normed, post_weight=w, pre_weight=w, gate=w, block_ckpt=bk, stream_ckpt=sk,
+                     rstd=rstd)
+        P.checkpoint8(normed, nk)
+        P.restore8(nk, restored)
+        P.block_norm_backward(bk, sk, rstd, dy, dx, da, dw, d_stream=du, post_weight=w, pre_weight=w, gate=w,
+                              workspace=P.block_norm_backward_workspace(3, cols))
+        results.append([v.clone() for v in (out, normed, restored, dx, da, rstd, dw, bk.codes, bk.exps, sk.codes,
+                                            sk.exps, nk.codes, nk.exps)])
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    f = norm64([given[0]], given[1], w, w, w, 1.0, 1.0, 1e-6, True)
+    close(results[1][0], f["s"], U[torch.bfloat16] * f["s"].abs() + (CHAIN + 1) * E * f["size"])
+
+
+def test_many_rows():
+    """More than 2^31 elements; the rows at the end are compared."""
+    rows, cols, t = 2 ** 21 + 3, 1032, torch.bfloat16
+    g = gen(6)
+    part, x = rnd(g, (rows, cols), t), rnd(g, (rows, cols), t)
+    out, normed, k = torch.empty_like(x), torch.empty_like(x), P.Checkpoint8(rows, cols)
+    rstd = torch.empty(2, rows, device="cuda")
+    P.block_norm([part], x, out, normed, rstd=rstd)
+    f = norm64([part[-50:]], x[-50:], None, None, None, 1.0, 1.0, 1e-6, True)
+    close(out[-50:], f["s"], U[t] * f["s"].abs() + (CHAIN + 1) * E * f["size"])
+    close(normed[-50:], f["y"], U[t] * f["y"].abs() + (CHAIN + 1) * E * f["ysize"])
+    P.checkpoint8(out, k)
+    codes, exps = encode64(out[-50:])
+    assert torch.equal(k.codes[-50:], codes) and torch.equal(k.exps[-50:], exps)
+    dx, da = x, torch.empty_like(x)
+    P.block_norm_backward(part, out, rstd, normed, dx, da, workspace=P.block_norm_backward_workspace(rows, cols))
+    b = back64(part[-50:], out[-50:], rstd[0, -50:], rstd[1, -50:], normed[-50:], None, None, None, None, 1.0, 1.0, True)
+    close(dx[-50:], b["dx"], U[t] * b["dx"].abs() + 2 * CHAIN * E * b["mdx"])
+    close(da[-50:], b["da"], U[t] * b["da"].abs() + 2 * CHAIN * E * b["mda"])
+    P.restore8(k, dx)
+    assert same_values(dx[-50:], decode64(codes, exps).to(t))
+
+
+def test_moe_weights_past_32_bits():
+    ids, _ = moe_case(8, 8192, 2048, 72, 0, 72, 16, "bf16")
+    assert int(ids.max()) >= 64                                        # past 2^31 elements of w_in
+
+
 # ---- streams, graphs, repeats ---------------------------------------------------------
 
 def test_repeats_have_the_same_bits_and_streams_and_graphs_work():

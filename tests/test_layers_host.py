@@ -82,6 +82,10 @@ def test_checkpoint_rejects(call):
     assert ck(call=call, k=P.ptoc_ckpt8(at(1), 64, None, 2)) == P.ERR_INVALID_ARG
     assert ck(call=call, k=P.ptoc_ckpt8(at(0) + 512, 64, at(2), 2)) == P.ERR_ALIAS
     assert ck(call=call, rows=2 ** 50, cols=2 ** 20, x=m(0, 2 ** 20), k=k8(1, 2 ** 20, 2 ** 15)) == P.ERR_INVALID_ARG
+    far = dict(x=P.ptoc_matrix(1 << 40, 2 ** 33), k=P.ptoc_ckpt8(1 << 41, 2 ** 33, 1 << 42, 2 ** 28))
+    assert ck(call=call, rows=1, cols=2 ** 33, **far) == P.ERR_UNSUPPORTED      # columns are counted in 32 bits
+    assert ck(call=call, rows=2 ** 24, cols=2 ** 16, x=P.ptoc_matrix(1 << 50, 2 ** 16),
+              k=P.ptoc_ckpt8(1 << 51, 2 ** 16, 1 << 52, 2 ** 11)) == P.ERR_UNSUPPORTED
     assert ck(call=call, rows=0) == P.OK and ck(call=call, cols=0) == P.OK
 
 

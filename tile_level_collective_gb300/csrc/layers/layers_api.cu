@@ -93,8 +93,8 @@ ptoc_status ckpt8_call(const ptoc_matrix* x, const ptoc_ckpt8* k, int64_t rows, 
     const ptoc_status al = o.disjoint();
     if (al != PTOC_OK) return al;
     if (rows == 0 || cols == 0) return PTOC_OK;
-    // work units of 256 columns are counted in 32 bits
-    if (rows > INT32_MAX / ((cols + 255) / 256)) return PTOC_ERR_UNSUPPORTED;
+    // columns and work units of 256 columns are counted in 32 bits
+    if (cols > INT32_MAX - 255 || rows > INT32_MAX / ((cols + 255) / 256)) return PTOC_ERR_UNSUPPORTED;
     Ckpt8Params p;
     p.x = x->data;
     p.ld = x->ld;
