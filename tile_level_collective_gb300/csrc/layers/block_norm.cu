@@ -10,11 +10,13 @@
 // walks the rows, and every warp keeps a queue of copies of its own columns
 // (the parts and the residual of this row and the next ones) in shared memory.
 //
-// Measured on GB300 (bf16; of 6.68 TB/s copied): 16384 x 8192 of 8 parts 444 us
-// (6.65 TB/s; one block per row without a queue: 650 us); of 1 part 172 us (6.2
-// TB/s); 8192 x 4096 of 1 part 46 us (5.8 TB/s), with both checkpoints 66 us (5.1
-// TB/s: 46 million instructions, 60 % of the issue slots at 16 warps per SM).
-// One row of 7168 columns of 8 parts: 4.9 us on the device.
+// Measured on GB300 (bf16; of 6.68 TB/s copied): 16384 x 8192 of 8 parts 436 us
+// (6.8 TB/s; one block per row without a queue: 650 us); of 1 part 167 us (6.4
+// TB/s), with both checkpoints 212 us (6.4 TB/s); 8192 x 4096 of 1 part 46 us (5.8
+// TB/s), with both checkpoints 58 us (5.8 TB/s: 36 million instructions, 58 % of
+// the issue slots at 16 warps per SM), of 4095 columns 117 us (8 accesses where
+// an aligned row takes one). One row of 7168 columns of 8 parts: 4.9 us on the
+// device.
 #include "layers/layers_common.cuh"
 #include "layers/layers_internal.h"
 

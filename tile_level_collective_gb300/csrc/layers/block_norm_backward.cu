@@ -21,13 +21,14 @@
 // adds the partial rows in order (about 4 us).
 //
 // Measured on GB300 (bf16, both launches; of 6.68 TB/s copied): 8192 x 4096
-// from checkpoints 73 us (4.6 TB/s), from matrices 76 us (5.3 TB/s); 16384 x
-// 8192 from checkpoints 247 us (5.5 TB/s); f32 8192 x 4096 128 us (6.3 TB/s).
-// With 16-bit elements and codes the issue rate comes before HBM: 700
-// instructions per thread and row of 16 columns, 57 % of the issue slots at 16
-// warps per SM, which the registers allow (two column sums, three arrays of
-// the row: 120). One chunk per thread in 64 registers took 96 us, four chunks
-// in 255 registers 104 us, where two took 81.
+// from checkpoints 71 us (4.8 TB/s), from matrices 77 us (5.2 TB/s), from
+// checkpoints of 4095 columns 99 us; 16384 x 8192 from checkpoints 237 us (5.7
+// TB/s); f32 8192 x 4096 136 us (5.9 TB/s). With 16-bit elements and codes
+// instructions and their latency come before HBM: 580 instructions per thread
+// and row of 16 columns, 50 % of the issue slots at 16 warps per SM, which the
+// registers allow (two column sums, three arrays of the row: 120). One chunk
+// per thread in 64 registers took 96 us, four chunks in 255 registers 104 us,
+// where two took 81.
 #include "layers/layers_common.cuh"
 #include "layers/layers_internal.h"
 
@@ -627,7 +628,9 @@ __global__ void __launch_bounds__(kSumThreads) norm_backward_sum_kernel(const No
 
 // The queue form: two chunks per thread and 512 threads on an SM; wider rows
 // leave no room for a row of copies ahead. (Two rows ahead of 16-bit elements:
-// 8192 x 4096 from matrices 83 us instead of 76, from checkpoints the same.)
+// 8192 x 4096 from matrices 81 us instead of 77; 16384 x 8192 from checkpoints
+// the same; issuing all of a row's copies during its exchange: 8192 x 4096 from
+// checkpoints 74 us instead of 71.)
 constexpr int64_t kQueueCols = kQueueThreads * 16;
 // Shared memory of a block: the columns' parameters, the queues, the header.
 template <class T, bool ODD>

@@ -33,7 +33,7 @@
 //
 // Measured on GB300 (bf16, of 6.68 TB/s copied): 64 tokens x 128 experts of 4096
 // x 1536 756 us (6.3 TB/s); 32 tokens 658 us (6.4 TB/s); 1 token, 8 of 64 experts
-// of 7168 x 2048, 126 us (5.6 TB/s); 1 token, 8 of 128 of 4096 x 1536, 67 us
+// of 7168 x 2048, 128 us (5.5 TB/s); 1 token, 8 of 128 of 4096 x 1536, 67 us
 // (4.5 TB/s). What a call costs beside its stream of weights is 15 us at 1 token
 // and 22 us at 64: five or six grid barriers of 1.2 us, the latency of the first
 // copies of either phase (3 us each), the choice (2 us) and the epilogues.
