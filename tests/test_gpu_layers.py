@@ -128,6 +128,26 @@ def test_checkpoint_of_special_values():
         assert same_values(out, decode64(c, e).float())            # the largest floats round up to 2^128
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cols", [5, 37, 263, 1001, 1030])
+def test_checkpoint_of_special_values_at_odd_rows(dtype, cols):
+    """Infinities and NaN in the run that the end of a row cuts, in the first
+    run and between, at every place of a row in its 16 bytes."""
+    g, t = gen(cols), DT[dtype]
+    src, dst = Box(17, cols, t, 1, 1), Box(17, cols, t, 1, 1)
+    src.view.copy_(rnd(g, (17, cols), torch.float32))
+    for r, c in ((1, cols - 1), (4, 0), (6, cols // 2), (9, cols - 2)):
+        src.view[r, c] = float("nan") if r % 3 else float("inf")
+    src.view[12] = 0
+    k = P.Checkpoint8(17, cols)
+    P.checkpoint8(src.view, k)
+    codes, exps = encode64(src.view)
+    assert torch.equal(k.codes, codes) and torch.equal(k.exps, exps)
+    P.restore8(k, dst.view)
+    assert same_values(dst.view, decode64(codes, exps).to(t))
+    assert dst.outside_intact()
+
+
 # ---- block_norm ------------------------------------------------------------------
 
 def gate_shape(kind, rows, cols):

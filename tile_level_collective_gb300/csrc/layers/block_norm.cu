@@ -14,7 +14,7 @@
 // (6.8 TB/s; one block per row without a queue: 650 us); of 1 part 167 us (6.4
 // TB/s), with both checkpoints 212 us (6.4 TB/s); 8192 x 4096 of 1 part 46 us (5.8
 // TB/s), with both checkpoints 58 us (5.8 TB/s: 36 million instructions, 58 % of
-// the issue slots at 16 warps per SM), of 4095 columns 117 us (8 accesses where
+// the issue slots at 16 warps per SM), of 4095 columns 110 us (8 accesses where
 // an aligned row takes one). One row of 7168 columns of 8 parts: 4.9 us on the
 // device.
 #include "layers/layers_common.cuh"

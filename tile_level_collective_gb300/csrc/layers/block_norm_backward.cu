@@ -486,8 +486,8 @@ __global__ void __launch_bounds__(kQueueThreads) norm_backward_queue_kernel(cons
         mask[i] = runs_below<G>(col[i], p.c.cols);
     }
     QueueLoader<T, C, CKPT, ODD> in(p, smem + (size_t)blockDim.x * C * 64, col, mask);
-    const Columns<T, G, C, true> cols{p.c, col, mask, (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * (C * 2048) +
-                                             (threadIdx.x & 31) * 16};
+    const uint32_t kept = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.x >> 5) * (C * 2048);
+    const Columns<T, G, C, true> cols{p.c, col, mask, kept + (threadIdx.x & 31) * 16};
     const Columns<T, G, C, false> memory{p.c, col, mask, 0};
 #pragma unroll
     for (int i = 0; i < C; ++i) {

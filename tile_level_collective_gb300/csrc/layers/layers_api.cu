@@ -101,7 +101,8 @@ ptoc_status ckpt8_call(const ptoc_matrix* x, const ptoc_ckpt8* k, int64_t rows, 
     p.ckpt = *k;
     p.rows = rows;
     p.cols = cols;
-    p.vec = o.vec && cols % (16 / elem_size(dtype)) == 0;
+    const bool words = ((uintptr_t)k->codes & 7u) == 0 && (rows == 1 || k->ld_codes % 8 == 0);
+    p.access = o.vec && cols % (16 / elem_size(dtype)) == 0 ? kAligned : words ? kOddPitch : kAnywhere;
     return status_of(restore ? launch_restore8(p, dtype, stream) : launch_checkpoint8(p, dtype, stream));
 }
 

@@ -350,9 +350,11 @@ struct Ckpt {
 
 // Write a chunk (zeros outside the mask) of one row: 256 * i columns after
 // column `col0`. Every lane of the warp takes part, also those whose mask is
-// empty.
+// empty. A run that the row's end cuts (G > 1) is not in the mask: the run
+// after those that are has `cut` columns.
 template <int G>
-__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int32_t col0, int i, uint32_t mask, const F8& f)
+__device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int32_t col0, int i, uint32_t mask, const F8& f,
+                                            int32_t cut = 0)
 {
     int8_t* codes = k.codes + row * k.ld_codes + col0 + 256 * i;
     uint8_t* exps = k.exps + row * k.ld_exps + 8 * i;
@@ -383,18 +385,38 @@ __device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int32_t 
                 if constexpr (G == 8) *(uint2*)codes = make_uint2(w[0], w[G / 4 - 1]);
                 else *(uint32_t*)(codes + 32 * G * q) = w[0];
                 if ((threadIdx.x & (32 / G - 1)) == 0) exps[(col0 >> 5) + q * G] = (uint8_t)byte;
+            } else if (cut > 0 && __popc(mask) == q) {
+#pragma unroll
+                for (int j = 0; j < G - 1; ++j)
+                    if (j < cut) codes[32 * G * q + j] = (int8_t)(w[j / 4] >> 8 * (j & 3));
+                if ((threadIdx.x & (32 / G - 1)) == 0) exps[(col0 >> 5) + q * G] = (uint8_t)byte;
             }
         }
     } else {
-        // lane j keeps the byte of element j's block and stores it
+        // each exchange halves the elements whose largest a lane keeps, until the
+        // lanes 4 j to 4 j + 3 share element j's: one exponent per lane, and the
+        // lanes' inverses are handed back
         const uint32_t lane = threadIdx.x & 31;
-        uint32_t keep = 0, code[8];
+        uint32_t top[8], code[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top[j] = __float_as_uint(v[j]) & 0x7fffffffu;
+#pragma unroll
+        for (int n = 4; n > 0; n /= 2) {
+            const bool upper = lane & (4 * n);
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                const uint32_t give = upper ? top[j] : top[j + n], keep = upper ? top[j + n] : top[j];
+                top[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 4 * n));
+            }
+        }
+        top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], 2));
+        top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], 1));
+        const uint32_t byte = ckpt_exponent(top[0]);
+        const float inverse = byte == 255u ? 0.0f : ckpt_inverse(byte);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu);
-            const uint32_t byte = ckpt_exponent(top);
-            code[j] = byte == 255u ? 0u : __float_as_uint(__fmaf_rn(v[j], ckpt_inverse(byte), kCodeBias));
-            if (lane == j) keep = byte;
+            const float inv = __shfl_sync(0xffffffffu, inverse, 4 * j);
+            code[j] = inv == 0.0f ? 0u : __float_as_uint(__fmaf_rn(v[j], inv, kCodeBias));
         }
         if (mask == 0xffu) {
 #pragma unroll
@@ -405,7 +427,8 @@ __device__ __forceinline__ void ckpt_store8(const Ckpt& k, int64_t row, int32_t 
                 if (mask >> j & 1) codes[32 * j] = (int8_t)code[j];
         }
         const uint32_t any = __shfl_sync(0xffffffffu, mask, 0);        // a block exists where its first column does
-        if (lane < 8 && (any >> lane & 1)) exps[((col0 - (int32_t)lane) >> 5) + (int32_t)lane] = (uint8_t)keep;
+        if ((lane & 3) == 0 && (any >> (lane >> 2) & 1))
+            exps[((col0 - (int32_t)lane) >> 5) + (int32_t)(lane >> 2)] = (uint8_t)byte;
     }
 }
 
@@ -486,10 +509,10 @@ __device__ __forceinline__ F8 ckpt_values(const CkptRaw<G>& r, float factor)
 {
     if constexpr (G == 1) {
         Pair scale[4];
+        const float mine = ckpt_scale(r.byte[0]) * factor;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            scale[i] = pair(ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i)) * factor,
-                            ckpt_scale(__shfl_sync(0xffffffffu, r.byte[0], 2 * i + 1)) * factor);
+            scale[i] = pair(__shfl_sync(0xffffffffu, mine, 2 * i), __shfl_sync(0xffffffffu, mine, 2 * i + 1));
         return code_values<1>(r.w, scale);
     } else {
         Pair scale[8 / G];

@@ -11,17 +11,17 @@ namespace ptoc {
 
 struct Ckpt;
 
+// How rows can be read: at any address, at any pitch from 16-byte aligned
+// bases, or in 16-byte aligned words throughout.
+enum Access : int { kAnywhere = 0, kOddPitch = 1, kAligned = 2 };
+
 struct Ckpt8Params {
     void* x;
     int64_t ld;
     ptoc_ckpt8 ckpt;
     int64_t rows, cols;
-    int32_t vec;                  // 16-byte aligned bases and pitches
+    int32_t access;               // Access; kOddPitch: the codes' rows are 8-byte aligned, x anywhere
 };
-
-// How rows can be read: at any address, at any pitch from 16-byte aligned
-// bases, or in 16-byte aligned words throughout.
-enum Access : int { kAnywhere = 0, kOddPitch = 1, kAligned = 2 };
 
 // The element types of the norms' parameters are dtype, or binary32 where
 // param_f32 is set.

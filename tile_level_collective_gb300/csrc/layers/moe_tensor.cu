@@ -463,7 +463,8 @@ __device__ __noinline__ float own_sum(const MoeTensorParams& p, const Shared& sh
 // `sums`, which is NaN then: 0 times each of them) are taken again, for tokens
 // [t0, t1) of a column that this thread has stored.
 template <class T, int N>
-__device__ __forceinline__ void mend(const MoeTensorParams& p, const Shared& sh, float sums, int t0, int t1, int64_t col)
+__device__ __forceinline__ void mend(const MoeTensorParams& p, const Shared& sh, float sums, int t0, int t1,
+                                     int64_t col)
 {
     if (sums == 0.0f) return;
     for (int t = t0; t < t1; ++t) {
