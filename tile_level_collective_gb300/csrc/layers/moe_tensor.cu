@@ -89,6 +89,7 @@ struct Shared {
     uint32_t tmem;
     int32_t active;                         // active local experts
     int32_t fault;                          // a bounded wait gave up
+    uint32_t armed;                         // stages whose copies were started, over both phases
     int32_t ids[PTOC_MOE_MAX_TOKENS * PTOC_MOE_MAX_TOP_K];
     float weights[PTOC_MOE_MAX_TOKENS * PTOC_MOE_MAX_TOP_K];
     int16_t expert[PTOC_MOE_MAX_EXPERTS];   // the active local experts, ascending
@@ -541,6 +542,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 
     // the roles' places in the ring and in the two accumulators, kept over both phases
     uint32_t turn = 0, acc = 0;
+    // A wait that gives up ends its role for good, also for the phase that follows:
+    // the places go on by what a phase should have done, so the parity of a later
+    // wait could be that of a turn which the barrier never saw, and a stage would
+    // be armed twice. A role that has not given up has seen every turn before, and
+    // its waits for the others end by their bound.
+    bool alive = true;
+    uint32_t armed = 0;
     for (int phase = 1; phase <= 2 && active > 0; ++phase) {
         const Split& split = phase == 1 ? in : out;
         const uint32_t first = split.begin(blockIdx.x), last = split.begin(blockIdx.x + 1);
@@ -550,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             const uint32_t dst = ring + slot * kStage;
             uint64_t* bar = &sh.full[slot];
             bar_expect(bar, kStage);
+            ++armed;
             if (phase == 1) {
                 const uint32_t a = tile / in_tiles;
                 const int i0 = (int)(tile - a * in_tiles) * kHalfRows, e = 2 * sh.expert[a];
@@ -577,10 +586,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             // the first weights do not wait for the other blocks
             if (warp == 0) {
                 if (lane == 0)
-                    for (const uint32_t ahead = min(kStages, last - first); sent < ahead; ++sent) {
+                    for (const uint32_t ahead = min(kStages, last - first); alive && sent < ahead;) {
                         const uint32_t u = turn + sent;
-                        if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
-                        weights(first + sent, u % kStages);
+                        alive = wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns);
+                        if (alive) weights(first + sent++, u % kStages);
                     }
                 __syncwarp();
             }
@@ -611,9 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         }
         if (warp == 0 && lane == 0) {
             for (uint32_t s = 0; s < sent; ++s) tokens(first + s, (turn + s) % kStages);
-            for (uint32_t x = first + sent; x < last; ++x) {
+            for (uint32_t x = first + sent; alive && x < last; ++x) {
                 const uint32_t u = turn + (x - first);
-                if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
+                alive = wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns);
+                if (!alive) break;
                 weights(x, u % kStages);
                 tokens(x, u % kStages);
             }
@@ -621,17 +631,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 
         if (warp == 1 && lane == 0) {
             uint32_t at = acc;
-            bool ok = true;
-            for (uint32_t x = first; x < last && ok;) {
+            for (uint32_t x = first; alive && x < last;) {
                 // one segment: this block's stages of one tile
                 const uint32_t end = min(last, (x / split.depth + 1) * split.depth);
                 const uint32_t b = at & 1, d = tmem + b * 2 * N;
-                if (!wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns)) break;
+                alive = wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns);
+                if (!alive) break;
                 fence_after();
                 for (const uint32_t from = x; x < end; ++x) {
                     const uint32_t u = turn + (x - first), slot = u % kStages;
-                    ok = wait(sh, &sh.full[slot], u / kStages & 1, p.wait_ns);
-                    if (!ok) break;
+                    alive = wait(sh, &sh.full[slot], u / kStages & 1, p.wait_ns);
+                    if (!alive) break;
                     fence_after();
                     const uint32_t a = ring + slot * kStage;
 #pragma unroll
@@ -642,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                     }
                     commit(&sh.empty[slot]);
                 }
-                if (ok) commit(&sh.acc_full[b]);
+                if (alive) commit(&sh.acc_full[b]);
                 ++at;
             }
         }
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         if (warp >= 4) {
             const int row = threadIdx.x - 128;                       // of either half
             uint32_t at = acc;
-            for (uint32_t x = first; x < last;) {
+            for (uint32_t x = first; alive && x < last;) {
                 const uint32_t tile = x / split.depth, head = tile * split.depth;
                 const uint32_t end = min(last, head + split.depth);
                 const bool whole = x == head && end == head + split.depth;
@@ -665,7 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                         sh.row_weight[row] = w;
                     }
                 }
-                if (!epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns)) break;
+                alive = epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns);
+                if (!alive) break;
                 fence_after();
                 const uint32_t d = tmem + b * 2 * N + ((uint32_t)(warp & 3) << 21);
                 float* mine = p.partial + (2 * (int64_t)blockIdx.x + (x == head)) * 2 * m.tokens * kHalfRows + row;
@@ -736,12 +747,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         }
     }
 
+    if (threadIdx.x == 0) sh.armed = armed;
     __syncthreads();
     if (sh.fault) {
-        // a wait gave up: let what is in flight land before the memory is given back
-        if (threadIdx.x < kStages) {
-            const uint64_t until = globaltimer_ns() + kStageWaitNs;
-            for (uint32_t q = 0; q < 2; ++q) stage_wait(smem_u32(&sh.full[threadIdx.x]), q, until, kStageWaitNs);
+        // a wait gave up: let what is in flight land before the memory is given
+        // back, which for a slot is the last stage that it was armed for
+        if (threadIdx.x < kStages && threadIdx.x < sh.armed) {
+            const uint32_t turns = (sh.armed - 1 - threadIdx.x) / kStages;
+            stage_wait(smem_u32(&sh.full[threadIdx.x]), turns & 1, globaltimer_ns() + kStageWaitNs, kStageWaitNs);
         }
         if (warp == 1 && lane == 0) {
             commit(&sh.drained);
