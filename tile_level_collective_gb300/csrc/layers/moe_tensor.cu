@@ -231,15 +231,19 @@ struct Split {
     }
 };
 
-// A bounded wait on a barrier of this block; false once any wait gave up. The
-// clock is read only after a number of polls (each of which may be suspended
-// for a while): read by all SMs at once it takes a microsecond or more.
+// A bounded wait on a barrier of this block; false once any wait of the block
+// gave up, and then for good: the places in the ring go on by what a phase
+// should have done, so the parity of a later wait could be that of a turn which
+// its barrier never saw, and a stage would be armed twice. (The same by a flag
+// in a register of each role cost 4 us a call.) The clock is read only after a
+// number of polls (each of which may be suspended for a while): read by all SMs
+// at once it takes a microsecond or more.
 __device__ __forceinline__ bool wait(Shared& sh, uint64_t* bar, uint32_t parity, uint64_t bound_ns)
 {
     constexpr int kPolls = 64;
+    if (*(volatile int32_t*)&sh.fault) return false;
     for (int i = 0; i < kPolls; ++i)
         if (stage_ready(smem_u32(bar), parity)) return true;
-    if (*(volatile int32_t*)&sh.fault) return false;
     if (stage_wait(smem_u32(bar), parity, globaltimer_ns() + bound_ns, bound_ns)) return true;
     if (atomicExch(&sh.fault, 1) == 0) atomicAdd(&g_stage_faults, 1u);
     return false;
@@ -497,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         bar_init(&sh.drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         sh.fault = 0;
+        sh.armed = 0;
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
@@ -542,13 +547,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 
     // the roles' places in the ring and in the two accumulators, kept over both phases
     uint32_t turn = 0, acc = 0;
-    // A wait that gives up ends its role for good, also for the phase that follows:
-    // the places go on by what a phase should have done, so the parity of a later
-    // wait could be that of a turn which the barrier never saw, and a stage would
-    // be armed twice. A role that has not given up has seen every turn before, and
-    // its waits for the others end by their bound.
-    bool alive = true;
-    uint32_t armed = 0;
     for (int phase = 1; phase <= 2 && active > 0; ++phase) {
         const Split& split = phase == 1 ? in : out;
         const uint32_t first = split.begin(blockIdx.x), last = split.begin(blockIdx.x + 1);
@@ -558,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             const uint32_t dst = ring + slot * kStage;
             uint64_t* bar = &sh.full[slot];
             bar_expect(bar, kStage);
-            ++armed;
+            ++sh.armed;
             if (phase == 1) {
                 const uint32_t a = tile / in_tiles;
                 const int i0 = (int)(tile - a * in_tiles) * kHalfRows, e = 2 * sh.expert[a];
@@ -586,10 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             // the first weights do not wait for the other blocks
             if (warp == 0) {
                 if (lane == 0)
-                    for (const uint32_t ahead = min(kStages, last - first); alive && sent < ahead;) {
+                    for (const uint32_t ahead = min(kStages, last - first); sent < ahead; ++sent) {
                         const uint32_t u = turn + sent;
-                        alive = wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns);
-                        if (alive) weights(first + sent++, u % kStages);
+                        if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
+                        weights(first + sent, u % kStages);
                     }
                 __syncwarp();
             }
@@ -620,10 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         }
         if (warp == 0 && lane == 0) {
             for (uint32_t s = 0; s < sent; ++s) tokens(first + s, (turn + s) % kStages);
-            for (uint32_t x = first + sent; alive && x < last; ++x) {
+            for (uint32_t x = first + sent; x < last; ++x) {
                 const uint32_t u = turn + (x - first);
-                alive = wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns);
-                if (!alive) break;
+                if (!wait(sh, &sh.empty[u % kStages], (u / kStages & 1) ^ 1, p.wait_ns)) break;
                 weights(x, u % kStages);
                 tokens(x, u % kStages);
             }
@@ -631,17 +628,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 
         if (warp == 1 && lane == 0) {
             uint32_t at = acc;
-            for (uint32_t x = first; alive && x < last;) {
+            bool ok = true;
+            for (uint32_t x = first; x < last && ok;) {
                 // one segment: this block's stages of one tile
                 const uint32_t end = min(last, (x / split.depth + 1) * split.depth);
                 const uint32_t b = at & 1, d = tmem + b * 2 * N;
-                alive = wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns);
-                if (!alive) break;
+                if (!wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns)) break;
                 fence_after();
                 for (const uint32_t from = x; x < end; ++x) {
                     const uint32_t u = turn + (x - first), slot = u % kStages;
-                    alive = wait(sh, &sh.full[slot], u / kStages & 1, p.wait_ns);
-                    if (!alive) break;
+                    ok = wait(sh, &sh.full[slot], u / kStages & 1, p.wait_ns);
+                    if (!ok) break;
                     fence_after();
                     const uint32_t a = ring + slot * kStage;
 #pragma unroll
@@ -652,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                     }
                     commit(&sh.empty[slot]);
                 }
-                if (alive) commit(&sh.acc_full[b]);
+                if (ok) commit(&sh.acc_full[b]);
                 ++at;
             }
         }
@@ -660,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         if (warp >= 4) {
             const int row = threadIdx.x - 128;                       // of either half
             uint32_t at = acc;
-            for (uint32_t x = first; alive && x < last;) {
+            for (uint32_t x = first; x < last;) {
                 const uint32_t tile = x / split.depth, head = tile * split.depth;
                 const uint32_t end = min(last, head + split.depth);
                 const bool whole = x == head && end == head + split.depth;
@@ -675,8 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                         sh.row_weight[row] = w;
                     }
                 }
-                alive = epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns);
-                if (!alive) break;
+                if (!epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns)) break;
                 fence_after();
                 const uint32_t d = tmem + b * 2 * N + ((uint32_t)(warp & 3) << 21);
                 float* mine = p.partial + (2 * (int64_t)blockIdx.x + (x == head)) * 2 * m.tokens * kHalfRows + row;
@@ -747,7 +743,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         }
     }
 
-    if (threadIdx.x == 0) sh.armed = armed;
     __syncthreads();
     if (sh.fault) {
         // a wait gave up: let what is in flight land before the memory is given
