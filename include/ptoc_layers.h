@@ -178,10 +178,12 @@ typedef struct {
  *            w_e * w_out[e] (silu(w_gate[e] x) * (w_up[e] x))
  * Rows none of whose experts are local are zero: the ranks' y are the parts
  * that ptoc_block_norm (or ptoc_allreduce) sums. The hidden activations
- * w_e * silu(..) * (..) are rounded once to dtype before the second product.
+ * w_e * silu(..) * (..) enter the second product as two numbers of dtype whose
+ * sum keeps 16 (bf16) or 22 (f16) significant bits, in f16 down to steps of
+ * 2^-35; y is rounded once.
  * ids ([tokens, top_k] int32) and weights ([tokens, top_k] floats) may be null.
  * dtype is PTOC_F16 or PTOC_BF16 (PTOC_F32 is PTOC_ERR_UNSUPPORTED).
- * An f16 activation beyond 65504 becomes infinite. An infinity or a NaN in x
+ * An f16 hidden activation beyond 65504 becomes infinite. An infinity or a NaN in x
  * stays with its token, and one in an expert's weights with the tokens that
  * chose the expert.
  * y must not overlap an input. tokens, experts or top_k above the limits are

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import tile_level_collective_gb300 as P
-from test_gpu_layers import gen, rnd
+from test_gpu_layers import DT, E, TINY, U, close, gen, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,91 @@ def test_moe_waits_that_give_up_end_the_call(monkeypatch, tokens, hidden, inter,
         layer(x, got, workspace=ws)
         torch.cuda.synchronize()
         assert P.ptoc_wait_faults() == 0 and torch.equal(got, want)
+
+
+# ---- the experts' activations keep more bits than their type ----------------------------
+
+def check_moe_parts(tokens, hidden, inter, experts, top_k, dtype, scale=1.0, renorm=True, w_lead=0, spread=1.0):
+    """y against 64 bits, given the kernel's own choice and weights. A sum of n
+    products in binary32 is off by n * 2^-24 of their magnitudes, silu's slope
+    is at most 1.1, and an activation is kept to 2^-17 (bf16) or 2^-22 (f16) of
+    itself, in steps of 2^-35 in f16: without a rounding to the type."""
+    g, t = gen(tokens * 31 + hidden), DT[dtype]
+    x = rnd(g, (tokens, hidden), t)
+    router = rnd(g, (experts, hidden), t, spread * hidden ** -0.5)
+
+    def packed(shape, std):
+        n = shape[0] * shape[1] * shape[2]
+        return rnd(g, (n + w_lead,), t, std)[w_lead:].view(shape)
+
+    w_in, w_out = packed((experts, 2 * inter, hidden), hidden ** -0.5), packed((experts, hidden, inter), inter ** -0.5)
+    layer = P.MoeLayer(router, w_in, w_out, top_k, renormalize=renorm, scale=scale)
+    y = torch.empty_like(x)
+    ids = torch.empty(tokens, top_k, dtype=torch.int32, device="cuda")
+    w = torch.empty(tokens, top_k, device="cuda")
+    layer(x, y, ids=ids, weights=w, workspace=layer.workspace(tokens))
+    keep, step = (2.0 ** -17, 0.0) if dtype == "bf16" else (2.0 ** -22, 2.0 ** -36)
+    want, bound = (torch.zeros(tokens, hidden, dtype=torch.float64, device="cuda") for _ in range(2))
+    for tok in range(tokens):
+        for k in range(top_k):
+            e, we, v = int(ids[tok, k]), float(w[tok, k]), x[tok].double()
+            wi, wo = w_in[e].double(), w_out[e].double()
+            gu, mag = wi @ v, wi.abs() @ v.abs()
+            gate, up = gu[:inter], gu[inter:]
+            act = gate / (1 + torch.exp(-gate))
+            h = we * act * up
+            dh = we * hidden * E * (1.1 * mag[:inter] * up.abs() + act.abs() * mag[inter:]) + \
+                h.abs() * (8 * E + keep) + step
+            want[tok] += wo @ h
+            bound[tok] += wo.abs() @ dh + (top_k * inter + 8) * E * (wo.abs() @ h.abs())
+    close(y, want, bound * 1.01 + U[t] * want.abs() + (TINY if dtype == "f16" else 0.0), "y")
+    return w
+
+
+@pytest.mark.parametrize("tokens", [1, 8, 9, 33, 64])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_moe_activations_are_not_rounded_to_the_type(tokens, dtype):
+    check_moe_parts(tokens, 512, 200, 12, 3, dtype)
+    check_moe_parts(tokens, 200, 72, 6, 2, dtype, w_lead=1)              # weights at odd places
+
+
+@pytest.mark.parametrize("tokens", [2, 40])
+@pytest.mark.parametrize("w_lead", [0, 1])
+def test_moe_small_f16_weights(tokens, w_lead):
+    """Routing weights that push activations below the smallest normal f16
+    (2^-14): softmax scores over 256 experts, not renormalised, times 2^-6."""
+    w = check_moe_parts(tokens, 256, 104, 256, 4, "f16", scale=2.0 ** -6, renorm=False, w_lead=w_lead, spread=0.25)
+    assert float(w.max()) < 2.0 ** -12
+
+
+@pytest.mark.parametrize("w_lead", [0, 1])
+def test_moe_f16_activations_beyond_the_range_are_infinite(w_lead):
+    """One huge activation of one token: its row has infinities or NaN where
+    the output weights are not zero, the other tokens' rows are those of a call
+    without it."""
+    g, t = gen(77), torch.float16
+    tokens, hidden, inter, experts = 5, 256, 64, 4
+    x = rnd(g, (tokens, hidden), t)
+    router = rnd(g, (experts, hidden), t, 0.1)
+
+    def packed(shape, std):
+        n = shape[0] * shape[1] * shape[2]
+        return rnd(g, (n + w_lead,), t, std)[w_lead:].view(shape)
+
+    w_in, w_out = packed((experts, 2 * inter, hidden), 0.06), packed((experts, hidden, inter), 0.1)
+    layer = P.MoeLayer(router, w_in, w_out, 2)
+    clean, y = torch.empty_like(x), torch.empty_like(x)
+    ids = torch.empty(tokens, 2, dtype=torch.int32, device="cuda")
+    layer(x, clean, ids=ids, workspace=layer.workspace(tokens))
+    x[3] *= 30
+    x[3].clamp_(-100, 100)
+    w_in[:, 5] = torch.sign(x[3].float()).to(t) * 4                       # gate and up of activation 5
+    w_in[:, inter + 5] = w_in[:, 5]
+    layer(x, clean, ids=ids, workspace=layer.workspace(tokens))
+    assert float((w_in[0, 5].double() @ x[3].double())) > 2000            # so activation 5 is beyond 65504
+    x2 = x.clone()
+    x2[3] = 0
+    layer(x2, y, workspace=layer.workspace(tokens))
+    others = [0, 1, 2, 4]
+    assert torch.equal(clean[others], y[others]) and bool(torch.isfinite(y[others]).all())
+    assert not bool(torch.isfinite(clean[3]).any())

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kBlock) moe_in_kernel(const MoePlainParams p)
             const int pair = list[q0 + q];
             if (lane == 0)
                 p.w.hidden[pair * p.m.inter + i] =
-                    to_f32(from_f32<T>(p.w.weights[pair] * (gs / (1.0f + expf(-gs)) * us)));
+                    split_parts<T>(p.w.weights[pair] * (gs / (1.0f + expf(-gs)) * us)).value();
         }
     }
 }

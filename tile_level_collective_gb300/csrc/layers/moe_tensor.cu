@@ -4,9 +4,11 @@
 // Bound by HBM: the active experts' 3 * inter * hidden weights, read once.
 // The kernel is therefore one stream of weight tiles through shared memory
 // (tensor-map copies, a ring of stages deep enough to cover the latency of
-// HBM) into tcgen05.mma, whose rows are rows of weights and whose N = 16 to 64
-// columns are all the call's tokens, padded to 16: an expert multiplies every
-// token, and the epilogue keeps those that chose it. The tensor cores are
+// HBM) into tcgen05.mma, whose rows are rows of weights and whose columns are
+// all the call's tokens, padded to N = 8, 16, 32, 48 or 64: an expert multiplies
+// every token, and the epilogue keeps those that chose it. The second product
+// has 2 N columns: the activations are split into an upper and a lower part of
+// the type (moe_common.cuh), which the epilogue adds up. The tensor cores are
 // nearly idle at any N (4 % busy at 1 token), so gathering tokens would save
 // nothing that is short. A stage is 256 rows of weights (two accumulators of
 // 128 rows) by 64 elements of depth, and the tokens' elements of that depth.
@@ -15,8 +17,8 @@
 //   routing  few tokens: every block chooses for every token (the same bits
 //            everywhere); more: one block per token         | grid barrier
 //   phase 1  tiles of 128 gate rows and the matching 128 up rows x hidden;
-//            epilogue: h[expert][token] = w * silu(gate) * up in the
-//            activations' type, zero for tokens that did not choose the
+//            epilogue: h[expert][token] = w * silu(gate) * up in its two
+//            parts, zero for tokens that did not choose the
 //            expert                                         | grid barrier
 //            the same for tiles of several parts            | grid barrier
 //   phase 2  tiles of 256 output columns x (inter of every active expert):
@@ -31,15 +33,19 @@
 // barrier, 3 parts of 64 tokens took 22 us instead of 3.) The weights of phase
 // 2's first stages are on their way before the barriers in front of it.
 //
-// Measured on GB300 (bf16, of 6.68 TB/s copied): 64 tokens x 128 experts of 4096
-// x 1536 756 us (6.3 TB/s); 32 tokens 658 us (6.4 TB/s); 1 token, 8 of 64 experts
-// of 7168 x 2048, 128 us (5.5 TB/s); 1 token, 8 of 128 of 4096 x 1536, 67 us
-// (4.5 TB/s). What a call costs beside its stream of weights is 15 us at 1 token
-// and 22 us at 64: five or six grid barriers of 1.2 us, the latency of the first
-// copies of either phase (3 us each), the choice (2 us) and the epilogues.
-// Stages of 128 rows (two per tile of gate and up rows) took 829 us at 64 tokens,
-// as the tokens' elements then pass L2 twice as often; boxes without promotion
-// to 256 bytes in L2 872 us; stages of 128 elements of depth the same as 64.
+// Measured on GB300 (bf16, of 6.79 TB/s copied): 64 tokens x 128 experts of 4096
+// x 1536 772 us (6.2 TB/s); 32 tokens 660 us; 1 token, 8 of 64 experts of 7168 x
+// 2048, 129 us (5.5 TB/s); 1 token, 8 of 128 of 4096 x 1536, 72 us (4.2 TB/s).
+// With one rounded activation in place of two parts: 749, 651, 129 and 71 us; the
+// second part passes L2 with every tile of weights and takes a stage of the
+// ring. What a call costs beside its stream of weights is about 25 us at 1 token
+// and 60 us at 64: four grid barriers (five with more than 8 tokens) of 1.2 us,
+// the latency of the first copies of either phase (3 us each), the choice (2
+// us), the epilogues, and at 64 tokens the partial tiles and both parts.
+// Stages of 128 rows (two per tile of gate and up rows) took 829 us at 64 tokens
+// when these took 756, as the tokens' elements then pass L2 twice as often;
+// boxes without promotion to 256 bytes in L2 872 us; stages of 128 elements of
+// depth the same as 64.
 #include <cooperative_groups.h>
 
 #include "host/host_checks.h"
@@ -66,7 +72,7 @@ struct MoeTensorParams {
     CUtensorMap w_in, w_out, x, h;
     MoeParams m;
     float* logits;                          // [tokens, experts]
-    char* act;                              // [active, N, inter] activations (the h map)
+    char* act;                              // [active, 2 N, inter] activations, their upper and lower parts (the h map)
     float* partial;                         // [2 * grid][2][tokens][128] binary32 partial tiles
     int32_t* ids;                           // [tokens, top_k], where one block chooses per token
     float* weights;
@@ -104,15 +110,21 @@ struct Shared {
 };
 
 constexpr size_t kSharedHead = (sizeof(Shared) + 1023) / 1024 * 1024;
-// bytes of dynamic shared memory: the head, the ring, and room to align it
-constexpr size_t shared_bytes(int stages, int n)
-{
-    return kSharedHead + 1024 + (size_t)stages * (kTileBytes + n * kDepth * 2);
-}
-constexpr size_t kSharedMost = 227 * 1024;
+// The call's tokens are padded to N = 8, 16, 32, 48 or 64. The first product
+// multiplies them as they are (with the 16 columns that an mma has at least),
+// the second one both parts of their activations.
 template <int N>
-constexpr int kRing = (int)((kSharedMost - kSharedHead - 1024) / (kTileBytes + N * kDepth * 2)) < kMaxStages
-                          ? (int)((kSharedMost - kSharedHead - 1024) / (kTileBytes + N * kDepth * 2))
+constexpr int kInColumns = N < 16 ? 16 : N;
+template <int N>
+constexpr int kOutColumns = 2 * N;
+constexpr int kRowBytes = kDepth * 2;
+template <int N>
+constexpr uint32_t kStageBytes = kTileBytes + kOutColumns<N> * kRowBytes;
+constexpr size_t kSharedMost = 227 * 1024;
+// stages of the ring: what the head, and room to align it, leave
+template <int N>
+constexpr int kRing = (int)((kSharedMost - kSharedHead - 1024) / kStageBytes<N>) < kMaxStages
+                          ? (int)((kSharedMost - kSharedHead - 1024) / kStageBytes<N>)
                           : kMaxStages;
 
 // ---- tensor-core and copy instructions ------------------------------------------------
@@ -454,10 +466,13 @@ __device__ __noinline__ float own_sum(const MoeTensorParams& p, const Shared& sh
     for (int a = 0; a < sh.active; ++a) {
         float w;
         if (!chosen(m, sh, t, m.first + sh.expert[a], w)) continue;
-        const unsigned short* h = (const unsigned short*)p.act + ((int64_t)a * N + t) * m.inter;
+        const unsigned short* h = (const unsigned short*)p.act + ((int64_t)a * 2 * N + t) * m.inter;
+        const unsigned short* low = h + N * m.inter;
         const T* row = (const T*)m.w_out + ((int64_t)sh.expert[a] * m.hidden + col) * m.inter;
-        for (int64_t i = 0; i < m.inter && sum == sum; ++i)
-            sum = fmaf(to_f32(bitcast<T>((uint16_t)__ldcg(h + i))), to_f32(row[i]), sum);
+        for (int64_t i = 0; i < m.inter && sum == sum; ++i) {
+            const Parts<T> v{bitcast<T>((uint16_t)__ldcg(h + i)), bitcast<T>((uint16_t)__ldcg(low + i))};
+            sum = fmaf(v.value(), to_f32(row[i]), sum);
+        }
     }
     return sum;
 }
@@ -484,13 +499,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
     extern __shared__ unsigned char raw[];
     Shared& sh = *(Shared*)raw;
     const uint32_t ring = (smem_u32(raw) + (uint32_t)kSharedHead + 1023u) & ~1023u;
-    constexpr uint32_t kStage = kTileBytes + N * kDepth * 2;
+    constexpr uint32_t kStage = kStageBytes<N>;
     constexpr uint32_t kStages = kRing<N>;
-    constexpr uint32_t kColumns = 4 * N;                     // two accumulators in turn, of two halves
-    constexpr uint32_t kTmem = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : 256;
-    // f32 accumulator, both operands T, both K-major, 128 x N
+    constexpr int kIn = kInColumns<N>, kOut = kOutColumns<N>;
+    constexpr uint32_t kColumns = 4 * kOut;                  // two accumulators in turn, of two halves
+    constexpr uint32_t kTmem = kColumns <= 64 ? 64 : kColumns <= 128 ? 128 : kColumns <= 256 ? 256 : 512;
+    // f32 accumulator, both operands T, both K-major, 128 rows
     constexpr uint32_t kType = std::is_same<T, __half>::value ? 0u : 1u;
-    constexpr uint32_t kKind = 1u << 4 | kType << 7 | kType << 10 | (uint32_t)(N >> 3) << 17 | (kHalfRows >> 4) << 24;
+    constexpr uint32_t kKind = 1u << 4 | kType << 7 | kType << 10 | (kHalfRows >> 4) << 24;
     const MoeParams& m = p.m;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const cg::grid_group grid = cg::this_grid();
@@ -550,12 +566,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
     for (int phase = 1; phase <= 2 && active > 0; ++phase) {
         const Split& split = phase == 1 ? in : out;
         const uint32_t first = split.begin(blockIdx.x), last = split.begin(blockIdx.x + 1);
+        const uint32_t columns = phase == 1 ? kIn : kOut;
         // Copies of stage x: the weights' tile, then the tokens' rows of the same depth.
         auto weights = [&](uint32_t x, uint32_t slot) {
             const uint32_t tile = x / split.depth, d = x - tile * split.depth;
             const uint32_t dst = ring + slot * kStage;
             uint64_t* bar = &sh.full[slot];
-            bar_expect(bar, kStage);
+            bar_expect(bar, kTileBytes + columns * kRowBytes);
             ++sh.armed;
             if (phase == 1) {
                 const uint32_t a = tile / in_tiles;
@@ -608,8 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 } else {
                     lo = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 }
-                store4((T*)p.act + ((int64_t)a * N + t) * m.inter,
-                       (int64_t)(part.tile - a * in_tiles) * kHalfRows + quad, m.inter, lo);
+                const Parts<T> v[4] = {split_parts<T>(lo.x), split_parts<T>(lo.y), split_parts<T>(lo.z),
+                                       split_parts<T>(lo.w)};
+                T* row = (T*)p.act + ((int64_t)a * 2 * N + t) * m.inter;
+                const int64_t col = (int64_t)(part.tile - a * in_tiles) * kHalfRows + quad;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (col + j < m.inter) row[col + j] = v[j].high, row[N * m.inter + col + j] = v[j].low;
             }
             // h, here and in the epilogue, was written with ordinary stores, and is
             // read by the tensor-map copies after the barrier
@@ -632,7 +654,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             for (uint32_t x = first; x < last && ok;) {
                 // one segment: this block's stages of one tile
                 const uint32_t end = min(last, (x / split.depth + 1) * split.depth);
-                const uint32_t b = at & 1, d = tmem + b * 2 * N;
+                const uint32_t b = at & 1, d = tmem + b * 2 * kOut;
+                const uint32_t kind = kKind | columns >> 3 << 17;
                 if (!wait(sh, &sh.acc_empty[b], (at >> 1 & 1) ^ 1, p.wait_ns)) break;
                 fence_after();
                 for (const uint32_t from = x; x < end; ++x) {
@@ -644,8 +667,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 #pragma unroll
                     for (int k = 0; k < kDepth / 16; ++k) {
                         const uint64_t tok = operand(a + kTileBytes + k * 32);
-                        mma(d, operand(a + k * 32), tok, kKind, x > from || k > 0);
-                        mma(d + N, operand(a + kHalfBytes + k * 32), tok, kKind, x > from || k > 0);
+                        mma(d, operand(a + k * 32), tok, kind, x > from || k > 0);
+                        mma(d + kOut, operand(a + kHalfBytes + k * 32), tok, kind, x > from || k > 0);
                     }
                     commit(&sh.empty[slot]);
                 }
@@ -663,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 const bool whole = x == head && end == head + split.depth;
                 const uint32_t b = at & 1, a = tile / in_tiles;      // a: the expert, in phase 1
                 const int64_t i0 = (int64_t)(tile - a * in_tiles) * kHalfRows, col0 = (int64_t)tile * kTileRows;
-                T* h = (T*)p.act + (int64_t)a * N * m.inter;
+                T* h = (T*)p.act + (int64_t)a * 2 * N * m.inter;
                 if (phase == 1) {
                     const int expert = m.first + sh.expert[a];
                     float w = 0.0f;
@@ -674,12 +697,29 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 }
                 if (!epilogue_wait(sh, &sh.acc_full[b], at >> 1 & 1, p.wait_ns)) break;
                 fence_after();
-                const uint32_t d = tmem + b * 2 * N + ((uint32_t)(warp & 3) << 21);
+                const uint32_t d = tmem + b * 2 * kOut + ((uint32_t)(warp & 3) << 21);
                 float* mine = p.partial + (2 * (int64_t)blockIdx.x + (x == head)) * 2 * m.tokens * kHalfRows + row;
 #pragma unroll 1
-                for (int n0 = 0; n0 < N && n0 < m.tokens; n0 += 16) {
+                for (int n0 = 0; n0 < m.tokens; n0 += 16) {
                     float lo[16], hi[16];
-                    load_columns(d + n0, d + N + n0, lo, hi);
+                    load_columns(d + n0, d + kOut + n0, lo, hi);
+                    if (phase == 2) {                                // the lower parts' sums
+                        if constexpr (N == 8) {
+#pragma unroll
+                            for (int n = 0; n < 8; ++n) {
+                                lo[n] = fmaf(kLowUnit<T>, lo[n + 8], lo[n]);
+                                hi[n] = fmaf(kLowUnit<T>, hi[n + 8], hi[n]);
+                            }
+                        } else {
+                            float u[16], v[16];
+                            load_columns(d + N + n0, d + kOut + N + n0, u, v);
+#pragma unroll
+                            for (int n = 0; n < 16; ++n) {
+                                lo[n] = fmaf(kLowUnit<T>, u[n], lo[n]);
+                                hi[n] = fmaf(kLowUnit<T>, v[n], hi[n]);
+                            }
+                        }
+                    }
                     const int count = m.tokens - n0;                 // columns that are tokens
                     if (!whole) {
                         float* to = mine + n0 * kHalfRows;
@@ -692,8 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                         if (i0 + row < m.inter)
                             each<16>(count, [&](int n) {
                                 const int t = n0 + n;
-                                to[n * m.inter] =
-                                    from_f32<T>(sh.chosen[t] ? activation(sh.row_weight[t], lo[n], hi[n]) : 0.0f);
+                                const Parts<T> v =
+                                    split_parts<T>(sh.chosen[t] ? activation(sh.row_weight[t], lo[n], hi[n]) : 0.0f);
+                                to[n * m.inter] = v.high;
+                                to[(n + N) * m.inter] = v.low;
                             });
                     } else {
                         auto put = [&](const float (&v)[16], int64_t col) {
@@ -770,7 +812,7 @@ struct TensorPlan {
     int64_t most, in_tiles, out_tiles;
 };
 
-int padded_tokens(int64_t tokens) { return (int)((tokens + 15) / 16 * 16); }
+int padded_tokens(int64_t tokens) { return tokens <= 8 ? 8 : (int)((tokens + 15) / 16 * 16); }
 
 TensorPlan tensor_plan(int64_t tokens, int64_t hidden, int64_t inter, int experts, int top_k)
 {
@@ -781,7 +823,7 @@ TensorPlan tensor_plan(int64_t tokens, int64_t hidden, int64_t inter, int expert
     t.out_tiles = (hidden + kTileRows - 1) / kTileRows;
     size_t at = 0;
     t.logits = at, at += up((size_t)tokens * experts * 4);
-    t.act = at, at += up((size_t)t.most * padded_tokens(tokens) * inter * 2);
+    t.act = at, at += up((size_t)t.most * 2 * padded_tokens(tokens) * inter * 2);
     t.partial = at, at += up((size_t)2 * kGrid * tokens * kTileRows * 4);
     t.ids = at, at += up((size_t)tokens * top_k * 4);
     t.weights = at, at += up((size_t)tokens * top_k * 4);
@@ -810,7 +852,7 @@ bool encode_matrices(CUtensorMap* map, const void* base, int64_t count, int64_t 
 template <class T, int N>
 cudaError_t launch(MoeTensorParams& p, cudaStream_t s)
 {
-    const size_t smem = shared_bytes(kRing<N>, N);
+    const size_t smem = kSharedHead + 1024 + (size_t)kRing<N> * kStageBytes<N>;
     const void* kernel = (const void*)moe_tensor_kernel<T, N>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -824,6 +866,7 @@ template <class T>
 cudaError_t launch_for(MoeTensorParams& p, cudaStream_t s)
 {
     switch (padded_tokens(p.m.tokens)) {
+    case 8: return launch<T, 8>(p, s);
     case 16: return launch<T, 16>(p, s);
     case 32: return launch<T, 32>(p, s);
     case 48: return launch<T, 48>(p, s);
@@ -858,8 +901,8 @@ bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_
     p.wait_ns = copy_wait_ns();
     if (!encode_matrices(&p.w_in, m.w_in, 2 * (int64_t)m.local, m.inter, m.hidden, m.hidden, kHalfRows, f16) ||
         !encode_matrices(&p.w_out, m.w_out, m.local, m.hidden, m.inter, m.inter, kHalfRows, f16) ||
-        !encode_matrices(&p.x, m.x, 1, m.tokens, m.hidden, m.tokens > 1 ? m.ld_x : m.hidden, n, f16) ||
-        !encode_matrices(&p.h, p.act, t.most, n, m.inter, m.inter, n, f16))
+        !encode_matrices(&p.x, m.x, 1, m.tokens, m.hidden, m.tokens > 1 ? m.ld_x : m.hidden, n < 16 ? 16 : n, f16) ||
+        !encode_matrices(&p.h, p.act, t.most, 2 * n, m.inter, m.inter, 2 * n, f16))
         return false;
     *e = f16 ? launch_for<__half>(p, s) : launch_for<__nv_bfloat16>(p, s);
     return true;
