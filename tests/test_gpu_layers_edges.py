@@ -137,3 +137,77 @@ def test_moe_f16_activations_beyond_the_range_are_infinite(w_lead):
     others = [0, 1, 2, 4]
     assert torch.equal(clean[others], y[others]) and bool(torch.isfinite(y[others]).all())
     assert not bool(torch.isfinite(clean[3]).any())
+
+
+def exact_inputs(tokens, hidden, inter, experts, dtype, g):
+    """Tokens with two elements other than 0, so that the first product has no
+    rounding to speak of."""
+    x = torch.zeros(tokens, hidden, dtype=DT[dtype], device="cuda")
+    x[:, 3] = rnd(g, (tokens,), DT[dtype], 0.5, 2.0)
+    x[:, 10] = rnd(g, (tokens,), DT[dtype])
+    return x, rnd(g, (experts, 2 * inter, hidden), DT[dtype]), rnd(g, (experts, hidden, inter), DT[dtype], 4.0)
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -9], ids=["ordinary", "small"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("tokens", [1, 8, 20, 64])
+@pytest.mark.parametrize("hidden", [256, 252])
+def test_moe_second_product_of_nearly_exact_activations(tokens, hidden, dtype, scale):
+    """With a first product of two terms and a second one of 32, the bound is
+    that of y's rounding and little else; `small`: activations around 2^-14,
+    where f16 has steps of 2^-24. 252 columns take the plain kernels."""
+    inter, experts, top_k = 16, 8, 2
+    g, t = gen(tokens + hidden), DT[dtype]
+    x, w_in, w_out = exact_inputs(tokens, hidden, inter, experts, dtype, g)
+    layer = P.MoeLayer(rnd(g, (experts, hidden), t, 0.1), w_in, w_out, top_k, scale=scale)
+    y = torch.empty_like(x)
+    ids = torch.empty(tokens, top_k, dtype=torch.int32, device="cuda")
+    w = torch.empty(tokens, top_k, device="cuda")
+    layer(x, y, ids=ids, weights=w, workspace=layer.workspace(tokens))
+    keep, step = (2.0 ** -17, 0.0) if dtype == "bf16" else (2.0 ** -22, 2.0 ** -36)
+    want, bound = (torch.zeros(tokens, hidden, dtype=torch.float64, device="cuda") for _ in range(2))
+    for k in range(top_k):
+        e, v = ids[:, k].long(), x.double()
+        gu, mag = (torch.einsum("tih,th->ti", f(w_in[e].double()), f(v)) for f in (lambda z: z, torch.abs))
+        gate, up = gu[:, :inter], gu[:, inter:]
+        act = gate / (1 + torch.exp(-gate))
+        h = w[:, k:k + 1].double() * act * up
+        dh = w[:, k:k + 1].double() * 2 * E * (1.1 * mag[:, :inter] * up.abs() + act.abs() * mag[:, inter:]) + \
+            h.abs() * (8 * E + keep) + step
+        wo = w_out[e].double()
+        want += torch.einsum("thi,ti->th", wo, h)
+        bound += torch.einsum("thi,ti->th", wo.abs(), dh + (top_k * inter + 8) * E * h.abs())
+    close(y, want, bound * 1.01 + U[t] * want.abs() + (TINY if dtype == "f16" else 0.0), "y")
+
+
+# ---- values that are not finite cost no more than others ---------------------------------
+
+def elapsed_ms(f):
+    times = []
+    for _ in range(4):
+        torch.cuda.synchronize()
+        start = time.monotonic()
+        f()
+        torch.cuda.synchronize()
+        times.append((time.monotonic() - start) * 1e3)
+    return min(times)
+
+
+@pytest.mark.parametrize("tokens, hidden, inter, experts", [(1, 2048, 1024, 8), (64, 2048, 1024, 8), (64, 40960, 128, 4)])
+def test_moe_activations_beyond_the_range_take_no_longer(tokens, hidden, inter, experts):
+    """One f16 activation of every token beyond 65504, with finite weights: the
+    sums over experts need no second look. (Ten times the time of a call with
+    ordinary values, and a millisecond, are far above the noise.)"""
+    g, t = gen(hidden + tokens), torch.float16
+    x = rnd(g, (tokens, hidden), t)
+    x[:, 0] = 60.0
+    router, w_in = rnd(g, (experts, hidden), t, 0.02), rnd(g, (experts, 2 * inter, hidden), t, hidden ** -0.5)
+    layer = P.MoeLayer(router, w_in, rnd(g, (experts, hidden, inter), t, 0.05), 4)
+    y, ws = torch.empty_like(x), layer.workspace(tokens)
+    ordinary = elapsed_ms(lambda: layer(x, y, workspace=ws))
+    assert bool(torch.isfinite(y).all())
+    w_in[:, 7, 0] = 60.0
+    w_in[:, inter + 7, 0] = 60.0
+    took = elapsed_ms(lambda: layer(x, y, workspace=ws))
+    assert not bool(torch.isfinite(y).any()) and bool(torch.isinf(y).any())
+    assert took <= 10 * ordinary + 1, (took, ordinary)

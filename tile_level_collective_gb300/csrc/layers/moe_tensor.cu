@@ -74,6 +74,7 @@ struct MoeTensorParams {
     float* logits;                          // [tokens, experts]
     char* act;                              // [active, 2 N, inter] activations, their upper and lower parts (the h map)
     float* partial;                         // [2 * grid][2][tokens][128] binary32 partial tiles
+    uint32_t* bad;                          // [tiles of phase 2] 1: of several parts, over weights that are not finite
     int32_t* ids;                           // [tokens, top_k], where one block chooses per token
     float* weights;
     uint64_t wait_ns;
@@ -456,40 +457,53 @@ __device__ __forceinline__ void store4(T* row, int64_t col, int64_t n, const flo
         if (col + j < n) row[col + j] = from_f32<T>(e[j]);
 }
 
-// y of one token and column from the token's own experts alone. NaN is final:
-// a token whose own activations are NaN ends the loop at once.
+// y of one token and column from the token's own experts alone, by a warp: the
+// lanes share each expert's elements, and their sums are added in order.
 template <class T, int N>
 __device__ __noinline__ float own_sum(const MoeTensorParams& p, const Shared& sh, int t, int64_t col)
 {
     const MoeParams& m = p.m;
+    const int lane = threadIdx.x & 31;
     float sum = 0.0f;
-    for (int a = 0; a < sh.active; ++a) {
+    for (int a0 = 0; a0 < sh.active; a0 += 32) {
         float w;
-        if (!chosen(m, sh, t, m.first + sh.expert[a], w)) continue;
-        const unsigned short* h = (const unsigned short*)p.act + ((int64_t)a * 2 * N + t) * m.inter;
-        const unsigned short* low = h + N * m.inter;
-        const T* row = (const T*)m.w_out + ((int64_t)sh.expert[a] * m.hidden + col) * m.inter;
-        for (int64_t i = 0; i < m.inter && sum == sum; ++i) {
-            const Parts<T> v{bitcast<T>((uint16_t)__ldcg(h + i)), bitcast<T>((uint16_t)__ldcg(low + i))};
-            sum = fmaf(v.value(), to_f32(row[i]), sum);
+        const bool hit = a0 + lane < sh.active && chosen(m, sh, t, m.first + sh.expert[a0 + lane], w);
+        for (uint32_t hits = __ballot_sync(0xffffffffu, hit); hits; hits &= hits - 1) {
+            const int a = a0 + __ffs(hits) - 1;
+            const unsigned short* h = (const unsigned short*)p.act + ((int64_t)a * 2 * N + t) * m.inter;
+            const unsigned short* low = h + N * m.inter;
+            const T* row = (const T*)m.w_out + ((int64_t)sh.expert[a] * m.hidden + col) * m.inter;
+#pragma unroll 4
+            for (int64_t i = lane; i < m.inter; i += 32) {
+                const Parts<T> v{bitcast<T>((uint16_t)__ldcg(h + i)), bitcast<T>((uint16_t)__ldcg(low + i))};
+                sum = fmaf(v.value(), to_f32(row[i]), sum);
+            }
         }
     }
-    return sum;
+    return warp_sum(sum);
 }
 
 // The sums of phase 2 run over the experts of all tokens, with an activation
 // of 0 for those that a token did not choose: an infinity or a NaN in the
-// w_out of such an expert makes them NaN. So sums that are not finite (in
-// `sums`, which is NaN then: 0 times each of them) are taken again, for tokens
-// [t0, t1) of a column that this thread has stored.
+// w_out of such an expert makes them NaN. Sums over such weights are taken
+// again, for tokens [t0, t1) of this lane's column if its weights are `bad`; the
+// warp does it together, for one lane after the other. What tells is the sum of
+// any token's lower parts: they are finite whatever the activations are, so it
+// is finite unless a weight is not. (Asked of y instead, calls with finite
+// weights and one f16 activation beyond the range took 108 ms instead of 0.24:
+// 64 tokens, 4 of 8 experts of 40960 x 512. A tile may not take longer than the
+// other roles wait for it.)
 template <class T, int N>
-__device__ __forceinline__ void mend(const MoeTensorParams& p, const Shared& sh, float sums, int t0, int t1,
-                                     int64_t col)
+__device__ __forceinline__ void mend(const MoeTensorParams& p, const Shared& sh, bool bad, int t0, int t1, int64_t col)
 {
-    if (sums == 0.0f) return;
-    for (int t = t0; t < t1; ++t) {
-        T* y = (T*)p.m.y + t * p.m.ld_y + col;
-        if (!isfinite(to_f32(*y))) *y = from_f32<T>(own_sum<T, N>(p, sh, t, col));
+    const int lane = threadIdx.x & 31;
+    for (uint32_t all = __ballot_sync(0xffffffffu, bad && col < p.m.hidden); all; all &= all - 1) {
+        const int src = __ffs(all) - 1;
+        const int64_t c = __shfl_sync(0xffffffffu, col, src);
+        for (int t = t0; t < t1; ++t) {
+            const float sum = own_sum<T, N>(p, sh, t, c);
+            if (lane == src) ((T*)p.m.y)[t * p.m.ld_y + c] = from_f32<T>(sum);
+        }
     }
 }
 
@@ -526,6 +540,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         fence_before();
     }
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i * kTileRows < m.hidden;
+         i += (int64_t)gridDim.x * kThreads)
+        p.bad[i] = 0;
     // one or two tokens: all loads of a row at once, an expert to a block
     if (m.tokens <= 2) router_logits<T, 1, 2>(p, sh);
     else router_logits<T, 2, 8>(p, sh);
@@ -703,8 +720,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                 for (int n0 = 0; n0 < m.tokens; n0 += 16) {
                     float lo[16], hi[16];
                     load_columns(d + n0, d + kOut + n0, lo, hi);
+                    float low_lo = 0.0f, low_hi = 0.0f;              // those of the first token
                     if (phase == 2) {                                // the lower parts' sums
                         if constexpr (N == 8) {
+                            low_lo = lo[8], low_hi = hi[8];
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
                                 lo[n] = fmaf(kLowUnit<T>, lo[n + 8], lo[n]);
@@ -713,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                         } else {
                             float u[16], v[16];
                             load_columns(d + N + n0, d + kOut + N + n0, u, v);
+                            low_lo = u[0], low_hi = v[0];
 #pragma unroll
                             for (int n = 0; n < 16; ++n) {
                                 lo[n] = fmaf(kLowUnit<T>, u[n], lo[n]);
@@ -726,6 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                         each<16>(count, [&](int n) { to[n * kHalfRows] = lo[n]; });
                         to += m.tokens * kHalfRows;
                         each<16>(count, [&](int n) { to[n * kHalfRows] = hi[n]; });
+                        if (phase == 2 && !isfinite(low_lo + low_hi)) p.bad[tile] = 1;
                     } else if (phase == 1) {
                         // of an expert that the token did not choose it is 0, whatever the sums hold
                         T* to = h + (int64_t)n0 * m.inter + i0 + row;
@@ -738,18 +759,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
                                 to[(n + N) * m.inter] = v.low;
                             });
                     } else {
-                        auto put = [&](const float (&v)[16], int64_t col) {
-                            if (col >= m.hidden) return;
-                            T* to = (T*)m.y + n0 * m.ld_y + col;
-                            float sums = 0.0f;
-                            each<16>(count, [&](int n) {
-                                to[n * m.ld_y] = from_f32<T>(v[n]);
-                                sums = fmaf(0.0f, v[n], sums);
-                            });
-                            mend<T, N>(p, sh, sums, n0, min(n0 + 16, m.tokens), col);
+                        auto put = [&](const float (&v)[16], float low, int64_t col) {
+                            if (col < m.hidden) {
+                                T* to = (T*)m.y + n0 * m.ld_y + col;
+                                each<16>(count, [&](int n) { to[n * m.ld_y] = from_f32<T>(v[n]); });
+                            }
+                            mend<T, N>(p, sh, !isfinite(low), n0, min(n0 + 16, m.tokens), col);
                         };
-                        put(lo, col0 + row);
-                        put(hi, col0 + kHalfRows + row);
+                        put(lo, low_lo, col0 + row);
+                        put(hi, low_hi, col0 + kHalfRows + row);
                     }
                 }
                 fence_before();
@@ -775,10 +793,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
             float4 lo, hi;
             add_parts(p, part.c0, part.c1, t, quad, lo, hi);
             T* y = (T*)m.y + t * m.ld_y;
+            const bool bad = __ldcg(p.bad + part.tile) != 0;             // somewhere in the tile
             auto put = [&](const float4& v, int64_t col) {
                 store4(y, col, m.hidden, v);
-                const float sums = 0.0f * v.x + 0.0f * v.y + 0.0f * v.z + 0.0f * v.w;
-                for (int j = 0; j < 4 && col + j < m.hidden; ++j) mend<T, N>(p, sh, sums, t, t + 1, col + j);
+                if (!bad) return;
+                const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mend<T, N>(p, sh, !isfinite(e[j]), t, t + 1, col + j);
             };
             put(lo, (int64_t)part.tile * kTileRows + quad);
             put(hi, (int64_t)part.tile * kTileRows + kHalfRows + quad);
@@ -808,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_tensor_kernel(const __grid_co
 // ---- host side --------------------------------------------------------------------
 
 struct TensorPlan {
-    size_t logits, act, partial, ids, weights, bytes;
+    size_t logits, act, partial, bad, ids, weights, bytes;
     int64_t most, in_tiles, out_tiles;
 };
 
@@ -825,6 +846,7 @@ TensorPlan tensor_plan(int64_t tokens, int64_t hidden, int64_t inter, int expert
     t.logits = at, at += up((size_t)tokens * experts * 4);
     t.act = at, at += up((size_t)t.most * 2 * padded_tokens(tokens) * inter * 2);
     t.partial = at, at += up((size_t)2 * kGrid * tokens * kTileRows * 4);
+    t.bad = at, at += up((size_t)t.out_tiles * 4);
     t.ids = at, at += up((size_t)tokens * top_k * 4);
     t.weights = at, at += up((size_t)tokens * top_k * 4);
     t.bytes = at;
@@ -896,6 +918,7 @@ bool launch_moe_tensor(const MoeParams& m, int dtype, cudaStream_t s, cudaError_
     p.logits = (float*)(m.ws + t.logits);
     p.act = m.ws + t.act;
     p.partial = (float*)(m.ws + t.partial);
+    p.bad = (uint32_t*)(m.ws + t.bad);
     p.ids = (int32_t*)(m.ws + t.ids);
     p.weights = (float*)(m.ws + t.weights);
     p.wait_ns = copy_wait_ns();
