@@ -134,16 +134,16 @@ assert struct.calcsize("iiPPPqqfff4x") == ctypes.sizeof(ptoc_block_norm_params)
 _group_bytes = struct.Struct("Pii").pack
 _array_types = {}
 _codes = {}
-_raw_stream = None
+_raw_stream = _current_device = None
 
 
 def _torch_names():
     """Fill what depends on torch, which the package imports on first use."""
     import torch
-    global _raw_stream, _float32, _int32
+    global _raw_stream, _current_device, _float32, _int32
     _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
     _float32, _int32 = torch.float32, torch.int32
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 def _code(dtype):
@@ -157,10 +157,13 @@ def _code(dtype):
 
 def _stream_of(stream, device):
     """The given stream, or torch's current one on the tensors' device (an
-    index; -1 for the host's memory)."""
-    if stream is None and device >= 0:
-        return _raw_stream(device)
-    return _stream(stream)
+    index; -1 for the host's memory). The kernels run on the current device:
+    tensors elsewhere are refused (last, after every check of the layouts)."""
+    if device < 0:
+        raise ValueError("expected tensors on a CUDA device")
+    if device != _current_device():
+        raise ValueError("the tensors' device cuda:%d is not the current one" % device)
+    return _raw_stream(device) if stream is None else _stream(stream)
 
 
 def _call(status, where):
@@ -208,6 +211,13 @@ def _packed(t, shape, dtype, device, what):
 def _workspace(nbytes, device):
     import torch
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
+
+
+def _space(workspace, device):
+    """Address and bytes of a workspace argument."""
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace: expected a packed tensor on the activations' device")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 class Checkpoint8:
@@ -372,13 +382,14 @@ def block_norm_backward(block, saved_stream, rstd, d_normed, d_residual, d_block
     columns = (cols,)
     s = _saved_bytes(*held[0], *held[1], *held[2], *held[3],
                      _packed(rstd, (2, rows), _float32, device, "rstd") or 0)
+    space, nbytes = _space(workspace, device)
     st = _lib.ptoc_block_norm_backward(
         s, p, _like(d_normed, kind, "d_normed"), _like(d_stream, kind, "d_stream"),
         _like(d_residual, kind, "d_residual"), _like(d_block, kind, "d_block"),
         _packed(d_pre_weight, columns, _float32, device, "d_pre_weight"),
         _packed(d_post_weight, columns, _float32, device, "d_post_weight"),
-        _packed(d_gate, None if gate is None else gate.shape, _float32, device, "d_gate"), workspace.data_ptr(),
-        workspace.nbytes, rows, cols, code, _stream_of(stream, device))
+        _packed(d_gate, None if gate is None else gate.shape, _float32, device, "d_gate"), space, nbytes, rows, cols,
+        code, _stream_of(stream, device))
     return _call(st, "ptoc_block_norm_backward")
 
 
@@ -426,8 +437,9 @@ class MoeLayer:
         if (dtype, device) != self._kind or hidden != self.hidden:
             raise ValueError("MoeLayer: x needs the weights' width, dtype and device")
         choice = (tokens, self.top_k)
+        space, nbytes = _space(workspace, device)
         st = _lib.ptoc_moe_few_tokens(
             _like(x, kind, "x"), ctypes.byref(self.params), _like(y, kind, "y"),
             _packed(ids, choice, _int32, device, "ids"), _packed(weights, choice, _float32, device, "weights"),
-            workspace.data_ptr(), workspace.nbytes, tokens, hidden, self.inter, self.code, _stream_of(stream, device))
+            space, nbytes, tokens, hidden, self.inter, self.code, _stream_of(stream, device))
         return _call(st, "ptoc_moe_few_tokens")
