@@ -1,5 +1,5 @@
 """The layer operators' binding without a GPU: tensors that a kernel could not
-use."""
+use, and first calls from several threads."""
 import pytest
 import torch
 
@@ -49,3 +49,23 @@ def test_workspaces_elsewhere_or_with_gaps_are_refused():
         layers._space(ws, 0)                                     # a host tensor for tensors on device 0
     with pytest.raises(ValueError, match="workspace"):
         layers._space(ws[::2], -1)
+
+
+# ---- the first call ------------------------------------------------------------------
+
+def test_names_are_complete_before_the_first_code_is_seen(monkeypatch):
+    """A second thread takes the codes as the sign that every name is set."""
+    names = ("_float32", "_int32", "_raw_stream", "_current_device")
+    layers._code(torch.bfloat16)
+    seen = []
+
+    class Codes(dict):
+        def update(self, *a):
+            seen.append([getattr(layers, n, None) is not None for n in names])
+            super().update(*a)
+
+    for n in names:
+        monkeypatch.setattr(layers, n, None)
+    monkeypatch.setattr(layers, "_codes", Codes())
+    assert layers._code(torch.float16) == P.F16
+    assert seen == [[True] * len(names)]

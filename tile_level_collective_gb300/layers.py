@@ -141,9 +141,9 @@ def _torch_names():
     """Fill what depends on torch, which the package imports on first use."""
     import torch
     global _raw_stream, _current_device, _float32, _int32
-    _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})
     _float32, _int32 = torch.float32, torch.int32
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})     # last: tells that all is there
 
 
 def _code(dtype):
