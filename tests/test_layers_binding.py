@@ -1,5 +1,5 @@
 """The layer operators' binding without a GPU: tensors that a kernel could not
-use, and first calls from several threads."""
+use, first calls from several threads, tensors whose storage is replaced."""
 import pytest
 import torch
 
@@ -69,3 +69,39 @@ def test_names_are_complete_before_the_first_code_is_seen(monkeypatch):
     monkeypatch.setattr(layers, "_codes", Codes())
     assert layers._code(torch.float16) == P.F16
     assert seen == [[True] * len(names)]
+
+
+# ---- tensors whose storage is replaced -----------------------------------------------
+
+def test_checkpoints_follow_their_tensors():
+    k = P.Checkpoint8(4, 70, device="cpu")
+    kind = (k.shape, 4, 70, torch.bfloat16, -1)
+    packed = lambda: layers._ckpt(k, kind, "ckpt")
+    assert packed() == layers._ckpt_bytes(k.codes.data_ptr(), 96, k.exps.data_ptr(), 3)
+    k.codes.data = torch.zeros(4, 80, dtype=torch.int8)[:, :70]
+    assert packed() == layers._ckpt_bytes(k.codes.data_ptr(), 80, k.exps.data_ptr(), 3)
+    k.exps.data = torch.zeros(4, 8, dtype=torch.uint8)[:, :3]
+    assert packed() == layers._ckpt_bytes(k.codes.data_ptr(), 80, k.exps.data_ptr(), 8)
+    k.codes = torch.zeros(4, 64, dtype=torch.int8)                  # other columns than its exponents
+    with pytest.raises(ValueError):
+        packed()
+    k.codes, k.exps = torch.zeros(3, 70, dtype=torch.int8), torch.zeros(3, 3, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        packed()
+
+
+@pytest.mark.parametrize("name", ["router", "w_in", "w_out", "bias"])
+def test_layers_follow_their_weights(name):
+    h = torch.bfloat16
+    w = dict(router=torch.zeros(8, 64, dtype=h), w_in=torch.zeros(8, 64, 64, dtype=h),
+             w_out=torch.zeros(8, 64, 32, dtype=h), bias=torch.zeros(8))
+    layer = P.MoeLayer(w["router"], w["w_in"], w["w_out"], 2, bias=w["bias"])
+    at = lambda: {k: getattr(layer._weights(), k) for k in w}
+    assert at() == {k: v.data_ptr() for k, v in w.items()}
+    old = w[name].detach()
+    w[name].data = torch.ones_like(old)
+    assert at() == {k: v.data_ptr() for k, v in w.items()} and w[name].data_ptr() != old.data_ptr()
+    for bad in (old[:4].clone(), old.double()):
+        w[name].data = bad
+        with pytest.raises(ValueError, match=name):
+            layer._weights()

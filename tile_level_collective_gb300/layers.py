@@ -228,23 +228,23 @@ class Checkpoint8:
         import torch
         blocks = (cols + CKPT_BLOCK - 1) // CKPT_BLOCK
         self._hold(torch.empty(rows, blocks * CKPT_BLOCK, dtype=torch.int8, device=device)[:, :cols],
-                   torch.empty(rows, blocks, dtype=torch.uint8, device=device))
+                   torch.empty(rows, blocks, dtype=torch.uint8, device=device), cols)
 
     @classmethod
     def of(cls, codes, exps, cols=None):
         """A checkpoint over given codes [rows, cols] and exponent bytes."""
-        import torch
         cols = codes.shape[-1] if cols is None else cols
+        k = cls.__new__(cls)
+        k._hold(codes, exps, cols)
+        return k
+
+    def _hold(self, codes, exps, cols):
+        import torch
         if codes.dtype != torch.int8 or exps.dtype != torch.uint8 or codes.device != exps.device:
             raise ValueError("checkpoint: expected int8 codes and uint8 exponents on one device")
         if codes.dim() != 2 or codes.shape[1] != cols or \
                 tuple(exps.shape) != (codes.shape[0], (cols + CKPT_BLOCK - 1) // CKPT_BLOCK):
             raise ValueError("checkpoint: expected codes [rows, cols] and exponents [rows, ceil(cols / 32)]")
-        k = cls.__new__(cls)
-        k._hold(codes, exps)
-        return k
-
-    def _hold(self, codes, exps):
         self.codes, self.exps = codes, exps
         self.shape, self.device = codes.shape, codes.get_device()
         self.c = (codes.data_ptr(), _pitch(codes, *codes.shape, "codes"), exps.data_ptr(),
@@ -256,7 +256,18 @@ def _ckpt(k, kind, what):
         return None
     if k.shape != kind[0] or k.device != kind[4]:
         raise ValueError("%s: the checkpoint needs the shape and device of the activations" % what)
-    return _ckpt_bytes(*k.c)
+    return _ckpt_bytes(*_held(k, what))
+
+
+def _held(k, what):
+    """The C fields of a checkpoint, whose tensors may have got other storage
+    since they were last looked at."""
+    if k.codes.data_ptr() != k.c[0] or k.exps.data_ptr() != k.c[2]:
+        shape, device = k.shape, k.device
+        k._hold(k.codes, k.exps, shape[1])
+        if k.shape != shape or k.device != device:
+            raise ValueError("%s: the checkpoint's tensors were replaced by others of another kind" % what)
+    return k.c
 
 
 def checkpoint8(x, ckpt, stream=None):
@@ -375,7 +386,7 @@ def block_norm_backward(block, saved_stream, rstd, d_normed, d_residual, d_block
     for i, (t, what) in enumerate(((block, "block"), (saved_stream, "stream"))):
         if isinstance(t, Checkpoint8):
             _ckpt(t, kind, what)
-            held[2 + i] = t.c
+            held[2 + i] = _held(t, what)
         else:
             _like(t, kind, what)
             held[i] = (t.data_ptr(), _pitch(t, rows, cols, what))
@@ -397,7 +408,8 @@ class MoeLayer:
     """A mixture-of-experts layer over given weights: ``router`` [experts,
     hidden], ``w_in`` [local, 2 * inter, hidden] (gate rows, then up rows) and
     ``w_out`` [local, hidden, inter], where ``local`` counts the experts held
-    here, from ``first_expert`` on. The weights are used in place."""
+    here, from ``first_expert`` on. The weights are used in place, where they
+    are at each call."""
 
     def __init__(self, router, w_in, w_out, top_k, *, bias=None, first_expert=0, score="softmax", renormalize=True,
                  scale=1.0):
@@ -407,21 +419,42 @@ class MoeLayer:
         local, hidden, inter = w_out.shape
         dtype, device = w_in.dtype, w_in.get_device()
         self.code = _code(dtype)
-        _packed(w_in, (local, 2 * inter, hidden), dtype, device, "w_in")
-        _packed(w_out, (local, hidden, inter), dtype, device, "w_out")
-        if router.dtype not in (dtype, _float32):
-            raise ValueError("MoeLayer: the router needs the experts' dtype or float32")
-        _packed(router, (router.shape[0], hidden), router.dtype, device, "router")
-        _packed(bias, (router.shape[0],), _float32, device, "bias")
         if score not in SCORES:
             raise ValueError("MoeLayer: score is one of %s" % sorted(SCORES))
+        if router.dtype not in (dtype, _float32):
+            raise ValueError("MoeLayer: the router needs the experts' dtype or float32")
         self.router, self.w_in, self.w_out, self.bias = router, w_in, w_out, bias
         self.dtype, self.device = dtype, w_in.device
         self._kind = (dtype, device)
         self.hidden, self.inter, self.experts, self.top_k = hidden, inter, router.shape[0], top_k
-        self.params = ptoc_moe_params(_addr(router), _addr(bias), _addr(w_in), _addr(w_out), _code(router.dtype),
-                                      self.experts, first_expert, local, top_k, SCORES[score], int(bool(renormalize)),
-                                      scale)
+        self._shapes = ((self.experts, hidden), (self.experts,), (local, 2 * inter, hidden), (local, hidden, inter))
+        self._router_dtype = router.dtype
+        self.params = ptoc_moe_params(None, None, None, None, _code(router.dtype), self.experts, first_expert, local,
+                                      top_k, SCORES[score], int(bool(renormalize)), scale)
+        self._take(self._addresses())
+
+    def _addresses(self):
+        return (self.router.data_ptr(), None if self.bias is None else self.bias.data_ptr(), self.w_in.data_ptr(),
+                self.w_out.data_ptr())
+
+    def _take(self, at):
+        """Use the weights at these addresses, which are theirs."""
+        dtype, device = self._kind
+        router, bias, w_in, w_out = self._shapes
+        _packed(self.router, router, self._router_dtype, device, "router")
+        _packed(self.bias, bias, _float32, device, "bias")
+        _packed(self.w_in, w_in, dtype, device, "w_in")
+        _packed(self.w_out, w_out, dtype, device, "w_out")
+        q = self.params
+        q.router, q.bias, q.w_in, q.w_out = self._at = at
+
+    def _weights(self):
+        """The C parameters. The weights may have got other storage since the
+        last call."""
+        at = self._addresses()
+        if at != self._at:
+            self._take(at)
+        return self.params
 
     def workspace(self, tokens):
         """A workspace tensor for calls of up to `tokens` tokens."""
@@ -439,7 +472,7 @@ class MoeLayer:
         choice = (tokens, self.top_k)
         space, nbytes = _space(workspace, device)
         st = _lib.ptoc_moe_few_tokens(
-            _like(x, kind, "x"), ctypes.byref(self.params), _like(y, kind, "y"),
+            _like(x, kind, "x"), ctypes.byref(self._weights()), _like(y, kind, "y"),
             _packed(ids, choice, _int32, device, "ids"), _packed(weights, choice, _float32, device, "weights"),
             space, nbytes, tokens, hidden, self.inter, self.code, _stream_of(stream, device))
         return _call(st, "ptoc_moe_few_tokens")
