@@ -134,7 +134,8 @@ typedef struct {
  * norm after the block and d_gate a gate (else PTOC_ERR_INVALID_ARG).
  * d_residual may be exactly du, and d_block exactly block (both by pointer and
  * pitch); other overlaps of an output are PTOC_ERR_ALIAS. Limits as
- * ptoc_block_norm. With rows == 0 the weight gradients are set to zero.
+ * ptoc_block_norm. With rows == 0 or cols == 0 the gradients of the weights and
+ * of the gate, sums over nothing, are set to zero.
  */
 size_t ptoc_block_norm_backward_workspace(int64_t rows, int64_t cols);
 ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* saved, const ptoc_block_norm_params* params,

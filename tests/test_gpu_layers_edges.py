@@ -1,13 +1,14 @@
-"""The layer operators where they are easily wrong: waits that give up, outputs
-over their inputs, mixed saved forms, odd pitches of codes, empty sums. The
-definitions and bounds are those of test_gpu_layers.py."""
+"""The layer operators where they are easily wrong: waits that give up, bits
+of activations, empty sums. The definitions and bounds are those of
+test_gpu_layers.py."""
 import time
 
 import pytest
 import torch
 
 import tile_level_collective_gb300 as P
-from test_gpu_layers import DT, E, TINY, U, close, gen, rnd
+from test_gpu_layers import DT, E, FILL, TINY, U, close, gate_shape, gen, rnd
+
 
 pytestmark = pytest.mark.gpu
 
@@ -211,3 +212,17 @@ def test_moe_activations_beyond_the_range_take_no_longer(tokens, hidden, inter, 
     took = elapsed_ms(lambda: layer(x, y, workspace=ws))
     assert not bool(torch.isfinite(y).any()) and bool(torch.isinf(y).any())
     assert took <= 10 * ordinary + 1, (took, ordinary)
+
+
+# ---- empty sums ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows, cols", [(5, 0), (0, 40), (0, 0)])
+@pytest.mark.parametrize("gate", ["scalar", "one", "channel", "token"])
+def test_gradients_of_an_empty_matrix_are_zero(rows, cols, gate):
+    """What is summed over no element is zero, also where the rows have no columns."""
+    z = lambda: torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    given = torch.ones(gate_shape(gate, rows, cols), dtype=torch.bfloat16, device="cuda")
+    dpre, dpost, dgate = (torch.full(s, FILL, device="cuda") for s in ((cols,), (cols,), given.shape))
+    P.block_norm_backward(z(), z(), torch.empty(2, rows, device="cuda"), z(), z(), z(), dpre, d_post_weight=dpost,
+                          d_gate=dgate, gate=given, workspace=P.block_norm_backward_workspace(rows, cols))
+    assert all(bool((v == 0).all()) for v in (dpre, dpost, dgate))

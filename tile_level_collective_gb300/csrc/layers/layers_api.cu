@@ -293,16 +293,16 @@ extern "C" ptoc_status ptoc_block_norm_backward(const ptoc_block_norm_saved* sav
     }
     st = o.disjoint();
     if (st != PTOC_OK) return st;
-    if (cols == 0) return PTOC_OK;
-    if (rows == 0) {
-        // no rows: the sums over them are zero
-        if (d_pre_weight && cudaMemsetAsync(d_pre_weight, 0, (size_t)cols * 4, stream) != cudaSuccess)
-            return PTOC_ERR_CUDA;
-        if (d_post_weight && cudaMemsetAsync(d_post_weight, 0, (size_t)cols * 4, stream) != cudaSuccess)
-            return PTOC_ERR_CUDA;
-        const size_t gate_bytes = p.gate_kind == kGateScalar ? 4 : p.gate_kind == kGateChannel ? (size_t)cols * 4 : 0;
-        if (gate_bytes && cudaMemsetAsync(d_gate, 0, gate_bytes, stream) != cudaSuccess) return PTOC_ERR_CUDA;
-        return PTOC_OK;
+    if (rows == 0 || cols == 0) {
+        // no elements: the sums over them are zero
+        const size_t column_bytes = (size_t)cols * 4, row_bytes = (size_t)rows * 4;
+        const size_t gate_bytes = p.gate_kind == kGateScalar ? 4 : p.gate_kind == kGateChannel ? column_bytes
+                                                                 : p.gate_kind == kGateToken   ? row_bytes : 0;
+        auto clear = [&](float* sums, size_t bytes) {
+            return !sums || !bytes || cudaMemsetAsync(sums, 0, bytes, stream) == cudaSuccess;
+        };
+        return clear(d_pre_weight, column_bytes) && clear(d_post_weight, column_bytes) && clear(d_gate, gate_bytes)
+                   ? PTOC_OK : PTOC_ERR_CUDA;
     }
     p.c.access = o.access(cols, eb);
     p.block = sv.block.data;
