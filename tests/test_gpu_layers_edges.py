@@ -1,14 +1,14 @@
 """The layer operators where they are easily wrong: waits that give up, bits
-of activations, empty sums. The definitions and bounds are those of
-test_gpu_layers.py."""
+of activations, empty sums, outputs over their inputs, mixed saved forms, odd
+pitches of codes. The definitions and bounds are those of test_gpu_layers.py."""
 import time
 
 import pytest
 import torch
 
 import tile_level_collective_gb300 as P
-from test_gpu_layers import DT, E, FILL, TINY, U, close, gate_shape, gen, rnd
-
+from test_gpu_layers import (CHAIN, DT, E, FILL, TINY, U, Box, back64, close, decode64, encode64, gate_shape, gen,
+                             norm_inputs, reduce_gate, rnd, rows_at, same_values)
 
 pytestmark = pytest.mark.gpu
 
@@ -226,3 +226,183 @@ def test_gradients_of_an_empty_matrix_are_zero(rows, cols, gate):
     P.block_norm_backward(z(), z(), torch.empty(2, rows, device="cuda"), z(), z(), z(), dpre, d_post_weight=dpost,
                           d_gate=dgate, gate=given, workspace=P.block_norm_backward_workspace(rows, cols))
     assert all(bool((v == 0).all()) for v in (dpre, dpost, dgate))
+
+
+# ---- outputs over their inputs, and what the forward pass saved -------------------------
+
+# the forms of both passes: aligned rows, odd pitches, odd bases, a gate for each element, wide rows
+FORMS = [
+    ("bf16", 333, 1024, 2, "channel", True, 0, 0),
+    ("f16", 500, 1003, 1, "token", True, 2, 0),
+    ("f32", 320, 2051, 2, "scalar", True, 0, 0),
+    ("bf16", 60, 515, 1, "token", True, 4, 3),
+    ("f16", 40, 1000, 2, "element", True, 8, 0),
+    ("f32", 21, 8200, 1, "channel", True, 0, 0),
+    ("bf16", 9, 9001, 2, "one", False, 0, 0),
+    ("bf16", 350, 4097, 1, "none", False, 0, 0),
+]
+IDS = lambda c: "-".join(str(v) for v in c)
+
+
+def backward_inputs(case, seed=0):
+    dtype, rows, cols, _, gate, post, pad, lead = case
+    t, d = DT[dtype], norm_inputs(*case)
+    g = gen(99 + cols + seed)
+    a, s = d["parts"][0], d["x"]
+    rstd = torch.stack([1 / (v.float().square().mean(1) + 1e-5).sqrt() for v in (a, s)])
+    boxes = [Box(rows, cols, t, pad, lead) for _ in range(4)]
+    for b in boxes[:2]:
+        b.view.copy_(rnd(g, (rows, cols), torch.float32))
+    return d, a, s, rstd, boxes
+
+
+def backward(case, d, a, s, rstd, dy, du, dx, da):
+    """One call; the gradients of the weights and the gate."""
+    _, rows, cols, _, _, post, _, _ = case
+    sums = dict(d_post_weight=torch.full((cols,), FILL, device="cuda") if post else None,
+                d_gate=None if d["gate"] is None else torch.full(d["gate"].shape, FILL, device="cuda"))
+    dpre = torch.full((cols,), FILL, device="cuda")
+    P.block_norm_backward(a, s, rstd, dy, dx, da, dpre, d_stream=du, post_norm=post, post_weight=d["wpost"],
+                          pre_weight=d["wpre"], gate=d["gate"], residual_scale=0.75, branch_scale=-1.5,
+                          workspace=P.block_norm_backward_workspace(rows, cols), **sums)
+    return dict(sums, dpre=dpre)
+
+
+def check_gradients(case, d, a, s, rstd, dy, du, dx, da, sums):
+    """Against 64 bits, with the bounds of test_gpu_layers.check_back."""
+    dtype, rows, _, _, _, post, _, _ = case
+    f = back64(a, s, rstd[0], rstd[1], dy, du, d["wpost"], d["wpre"], d["gate"], 0.75, -1.5, post)
+    u, c = U[DT[dtype]], 2 * CHAIN * E
+    close(dx, f["dx"], u * f["dx"].abs() + c * f["mdx"] + TINY, "d_residual")
+    close(da, f["da"], u * f["da"].abs() + c * f["mda"] + TINY, "d_block")
+    per = c + (rows + 8) * E
+    close(sums["dpre"], f["dpre"], per * f["mpre"], "d_pre_weight")
+    if post:
+        close(sums["d_post_weight"], f["dpost"], per * f["mpost"], "d_post_weight")
+    if d["gate"] is not None:
+        shape = d["gate"].shape
+        close(sums["d_gate"], reduce_gate(f["dg"], shape), (per + CHAIN * E) * reduce_gate(f["mdg"], shape), "d_gate")
+
+
+@pytest.mark.parametrize("case", FORMS, ids=IDS)
+def test_block_norm_over_its_residual(case):
+    dtype, rows, cols, _, _, post, pad, lead = case
+    d = norm_inputs(*case)
+    call = lambda x, out, normed: P.block_norm(d["parts"], x, out, normed, post_norm=post, post_weight=d["wpost"],
+                                               pre_weight=d["wpre"], gate=d["gate"], residual_scale=0.75)
+    apart, normed, over, normed2 = (Box(rows, cols, DT[dtype], pad, lead) for _ in range(4))
+    call(d["x"], apart.view, normed.view)
+    over.view.copy_(d["x"])
+    call(over.view, over.view, normed2.view)
+    assert torch.equal(over.view, apart.view) and torch.equal(normed2.view, normed.view)
+    assert over.outside_intact()
+
+
+@pytest.mark.parametrize("ckpt", [False, True], ids=["saved", "ckpt"])
+@pytest.mark.parametrize("case", FORMS, ids=IDS)
+def test_block_norm_backward_over_its_inputs(case, ckpt):
+    """d_residual over du, and d_block over the saved block output: the bits of
+    a call with outputs of their own, which is compared with 64 bits."""
+    d, a, s, rstd, (dy, du, dx, da) = backward_inputs(case)
+    rows, cols = a.shape
+    saved = a, s
+    if ckpt:
+        saved = P.Checkpoint8(rows, cols), P.Checkpoint8(rows, cols)
+        P.checkpoint8(a, saved[0])
+        P.checkpoint8(s, saved[1])
+        a, s = (decode64(k.codes, k.exps) for k in saved)
+    sums = backward(case, d, *saved, rstd, dy.view, du.view, dx.view, da.view)
+    check_gradients(case, d, a, s, rstd, dy.view, du.view, dx.view, da.view, sums)
+    block = Box(rows, cols, DT[case[0]], case[6], case[7]).view if ckpt else saved[0]
+    again = backward(case, d, *saved, rstd, dy.view, du.view, du.view, block)
+    assert torch.equal(du.view, dx.view) and torch.equal(block, da.view)
+    assert all(v is None or torch.equal(v, sums[k]) for k, v in again.items())
+    assert du.outside_intact()
+
+
+@pytest.mark.parametrize("kept", ["block", "stream"])
+@pytest.mark.parametrize("case", FORMS, ids=IDS)
+def test_block_norm_backward_from_one_matrix_and_one_checkpoint(case, kept):
+    d, a, s, rstd, (dy, du, dx, da) = backward_inputs(case)
+    k = P.Checkpoint8(*a.shape)
+    P.checkpoint8(s if kept == "block" else a, k)
+    small = decode64(k.codes, k.exps)
+    saved, exact = ((a, k), (a, small)) if kept == "block" else ((k, s), (small, s))
+    sums = backward(case, d, *saved, rstd, dy.view, du.view, dx.view, da.view)
+    check_gradients(case, d, *exact, rstd, dy.view, du.view, dx.view, da.view, sums)
+    assert dx.outside_intact() and da.outside_intact()
+
+
+# ---- codes and exponents at any pitch ---------------------------------------------------
+
+class CodeBox:
+    """A Checkpoint8 whose rows lie `pad` bytes apart, from byte `lead` on, in
+    filled memory."""
+
+    def __init__(self, rows, cols, pad, lead, exps_pad=0, exps_lead=0):
+        nb = (cols + 31) // 32
+        self.parts = []
+        for width, more, first, dtype in ((cols, pad, lead, torch.int8), (nb, exps_pad, exps_lead, torch.uint8)):
+            raw = torch.full((first + (rows + 1) * (width + more) + 32,), 7, dtype=dtype, device="cuda")
+            self.parts.append((raw, raw.as_strided((rows, width), (width + more, 1), first)))
+        self.k = P.Checkpoint8.of(self.parts[0][1], self.parts[1][1], cols)
+
+    def outside_intact(self):
+        ok = True
+        for raw, view in self.parts:
+            keep = raw.clone()
+            keep.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(7)
+            ok = ok and bool((keep == 7).all())
+        return ok
+
+
+CODES = [(1, 0, 0, 0), (5, 0, 1, 0), (0, 0, 3, 0), (8, 0, 0, 0), (3, 5, 0, 0), (0, 8, 0, 4), (0, 0, 0, 1), (11, 1, 2, 3)]
+
+
+@pytest.mark.parametrize("codes", CODES, ids=IDS)
+@pytest.mark.parametrize("dtype, rows, cols, pad", [("bf16", 37, 1003, 0), ("f16", 330, 520, 8), ("f32", 41, 2047, 1),
+                                                    ("f32", 19, 96, 0), ("bf16", 11, 9001, 0), ("bf16", 40, 4096, 0)])
+def test_codes_at_any_pitch(dtype, rows, cols, pad, codes):
+    """Kept, restored, written by the forward pass and read by the backward
+    pass, with rows of codes that begin anywhere in their 16 bytes."""
+    case = (dtype, rows, cols, 1, "channel", True, pad, 0)
+    d, a, s, rstd, (dy, du, dx, da) = backward_inputs(case)
+    bk, sk, again = (CodeBox(rows, cols, *codes) for _ in range(3))
+    for k, x in ((bk, a), (sk, s)):
+        P.checkpoint8(x, k.k)
+        want = encode64(x)
+        assert torch.equal(k.k.codes, want[0]) and torch.equal(k.k.exps, want[1]) and k.outside_intact()
+        back = Box(rows, cols, DT[dtype], pad)
+        P.restore8(k.k, back.view)
+        assert same_values(back.view, decode64(*want).to(DT[dtype])) and back.outside_intact()
+    sums = backward(case, d, bk.k, sk.k, rstd, dy.view, du.view, dx.view, da.view)
+    a8, s8 = (decode64(k.k.codes, k.k.exps) for k in (bk, sk))
+    check_gradients(case, d, a8, s8, rstd, dy.view, du.view, dx.view, da.view, sums)
+    assert dx.outside_intact() and da.outside_intact()
+    # the forward pass's checkpoints of the sum of one part, and of the stream
+    out = Box(rows, cols, DT[dtype], pad)
+    P.block_norm([a], s, out.view, post_weight=d["wpost"], gate=d["gate"], block_ckpt=again.k, stream_ckpt=sk.k)
+    for k, x in ((again, a), (sk, out.view)):
+        want = encode64(x)
+        assert torch.equal(k.k.codes, want[0]) and torch.equal(k.k.exps, want[1]) and k.outside_intact()
+
+
+@pytest.mark.parametrize("pitch", [2 ** 30 + 8, 2 ** 30 + 1])
+def test_rows_past_32_bits_against_the_definition(pitch):
+    """What test_rows_past_32_bits_have_the_same_bits compares between pitches,
+    against 64 bits at the far one."""
+    cols = 1000
+    case = ("bf16", 3, cols, 1, "channel", True, 0, 0)
+    d, a, s, rstd, (dy, du, _, _) = backward_inputs(case)
+    part, x, y, v = (rows_at(pitch).copy_(m) for m in (a, s, dy.view, du.view))
+    dx, da, restored = (rows_at(pitch) for _ in range(3))
+    bk, sk = (P.Checkpoint8.of(rows_at(pitch, torch.int8), rows_at(pitch, torch.uint8, 32)) for _ in range(2))
+    for k, m in ((bk, part), (sk, x)):
+        P.checkpoint8(m, k)
+        want = encode64(m)
+        assert torch.equal(k.codes, want[0]) and torch.equal(k.exps, want[1])
+        P.restore8(k, restored)
+        assert same_values(restored, decode64(*want).to(torch.bfloat16))
+    sums = backward(case, d, bk, sk, rstd, y, v, dx, da)
+    a8, s8 = (decode64(k.codes, k.exps) for k in (bk, sk))
+    check_gradients(case, d, a8, s8, rstd, y, v, dx, da, sums)
