@@ -14,9 +14,11 @@
  * PTOC_ERR_UNSUPPORTED). Sums, norm statistics and gradients of weights are
  * held in binary32; an element is rounded once, when it is stored.
  * Results do not depend on scheduling: the same call on the same GPU gives
- * the same bits. Rows are fastest where bases are 16-byte aligned, pitches too
- * and rows of whole 16-byte words; an odd pitch alone costs up to half the
- * speed, odd bases more.
+ * the same bits. Rows are fastest where bases are 16-byte aligned (a
+ * checkpoint's codes: 8-byte), pitches too and rows of whole 16-byte words; odd
+ * pitches, lengths or weights cost up to half the speed, odd bases more (bases
+ * and pitches of exponents, and gates of one number or one per row, cost
+ * nothing). One operand decides for the call.
  */
 #ifndef PTOC_LAYERS_H
 #define PTOC_LAYERS_H

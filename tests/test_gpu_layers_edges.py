@@ -406,3 +406,43 @@ def test_rows_past_32_bits_against_the_definition(pitch):
     sums = backward(case, d, bk, sk, rstd, y, v, dx, da)
     a8, s8 = (decode64(k.codes, k.exps) for k in (bk, sk))
     check_gradients(case, d, a8, s8, rstd, y, v, dx, da, sums)
+
+
+# ---- alignments that no kernel needs cost nothing ---------------------------------------
+
+def device_us(f):
+    """The shortest of several stretches of calls, per call."""
+    times = []
+    for _ in range(6):
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        start.record()
+        for _ in range(10):
+            f()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(start.elapsed_time(end) * 100)
+    return min(times)
+
+
+@pytest.mark.parametrize("odd", ["gate", "exponents", "codes"])
+def test_alignments_that_no_kernel_needs_cost_nothing(odd):
+    """A gate of one number at an odd element, exponents from an odd byte on,
+    codes from a multiple of 8 on: the time is that of the same call with all
+    of them aligned (with the element-wide kernels 115 us where these take 62)."""
+    rows, cols, t = 4096, 4096, torch.bfloat16
+    g = gen(4)
+    a, s, dy, out, normed, dx, da = (rnd(g, (rows, cols), t) for _ in range(7))
+    rstd, gates = torch.ones(2, rows, device="cuda"), torch.ones(16, dtype=t, device="cuda")
+    ws = P.block_norm_backward_workspace(rows, cols)
+    times = []
+    for shifted in (False, True):
+        at = dict(gate=(1, 0, 0), exponents=(0, 0, 3), codes=(0, 8, 0))[odd] if shifted else (0, 0, 0)
+        gate = gates[at[0]:at[0] + 1]
+        bk, sk = (CodeBox(rows, cols, 0, at[1], 0, at[2]) for _ in range(2))
+
+        def step():
+            P.block_norm([a], s, out, normed, gate=gate, rstd=rstd, block_ckpt=bk.k, stream_ckpt=sk.k)
+            P.block_norm_backward(bk.k, sk.k, rstd, dy, dx, da, gate=gate, workspace=ws)
+
+        times.append(device_us(step))
+    assert times[1] <= 1.4 * times[0], times

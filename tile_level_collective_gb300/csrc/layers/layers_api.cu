@@ -17,7 +17,7 @@ struct Operands {
     int nw = 0, nr = 0;
     bool ok = true;               // sizes, pitches and alignments so far
     bool vec = true;              // every base and pitch allows 16-byte vectors
-    bool bases = true;            // every matrix begins at a multiple of 16 bytes
+    bool bases = true;            // everything copied in words of rows at any pitch begins at a multiple of 16 bytes
 
     void add(bool write, const void* p, int64_t bytes)
     {
@@ -25,8 +25,8 @@ struct Operands {
         if (write) writes[nw++] = Span{p, (uintptr_t)(bytes > 0 ? bytes : 0)};
         else reads[nr++] = Span{p, (uintptr_t)(bytes > 0 ? bytes : 0)};
     }
-    // A matrix operand. `group`: 8 elements are moved as aligned words of
-    // this many bytes (16, or 8 for codes).
+    // A matrix operand. `word`: 8 elements are moved as aligned words of this
+    // many bytes (16, or 8 for codes; exponents go byte by byte).
     void rows(bool write, const void* p, int64_t ld, int64_t rows, int64_t cols, int eb, int word)
     {
         if ((!p && rows > 0 && cols > 0) || ld < cols || !aligned(p, eb)) {
@@ -34,7 +34,7 @@ struct Operands {
             return;
         }
         if (((uintptr_t)p | (uintptr_t)(rows > 1 ? ld * eb : 0)) & (uintptr_t)(word - 1)) vec = false;
-        if ((uintptr_t)p & 15u) bases = false;
+        if (word > 1 && ((uintptr_t)p & 15u)) bases = false;
         add(write, p, footprint(rows, cols, ld, eb));
     }
     void matrix(bool write, const ptoc_matrix* m, int64_t nrows, int64_t cols, int eb)
@@ -62,7 +62,7 @@ struct Operands {
     }
     int access(int64_t cols, int eb) const
     {
-        return !bases ? kAnywhere : vec && cols % (16 / eb) == 0 ? kAligned : kOddPitch;
+        return vec && cols % (16 / eb) == 0 ? kAligned : bases ? kOddPitch : kAnywhere;
     }
     ptoc_status disjoint() const { return check_disjoint_outputs(writes, nw, reads, nr); }
 };
@@ -135,7 +135,6 @@ ptoc_status norm_common(const ptoc_block_norm_params* q, int64_t rows, int64_t c
             o.param(q->gate, cols, eb);
         } else {
             if (!aligned(q->gate, eb)) return PTOC_ERR_INVALID_ARG;
-            if ((uintptr_t)q->gate & 3u) o.vec = o.bases = false;
             o.add(false, q->gate, footprint(kind == kGateToken ? rows : 1, 1, q->gate_row_stride, eb));
         }
     }
