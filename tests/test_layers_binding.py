@@ -34,6 +34,7 @@ def test_host_tensors_are_refused():
 
 def test_another_device_than_the_current_one_is_refused(monkeypatch):
     layers._code(torch.bfloat16)
+    monkeypatch.setattr(layers, "_one_device", False)
     monkeypatch.setattr(layers, "_current_device", lambda: 0)
     monkeypatch.setattr(layers, "_raw_stream", lambda device: 1234)
     assert layers._stream_of(None, 0) == 1234
@@ -55,7 +56,7 @@ def test_workspaces_elsewhere_or_with_gaps_are_refused():
 
 def test_names_are_complete_before_the_first_code_is_seen(monkeypatch):
     """A second thread takes the codes as the sign that every name is set."""
-    names = ("_float32", "_int32", "_raw_stream", "_current_device")
+    names = ("_float32", "_int32", "_raw_stream", "_current_device", "_one_device")
     layers._code(torch.bfloat16)
     seen = []
 

@@ -134,15 +134,16 @@ assert struct.calcsize("iiPPPqqfff4x") == ctypes.sizeof(ptoc_block_norm_params)
 _group_bytes = struct.Struct("Pii").pack
 _array_types = {}
 _codes = {}
-_raw_stream = _current_device = None
+_raw_stream = _current_device = _one_device = None
 
 
 def _torch_names():
     """Fill what depends on torch, which the package imports on first use."""
     import torch
-    global _raw_stream, _current_device, _float32, _int32
+    global _raw_stream, _current_device, _one_device, _float32, _int32
     _float32, _int32 = torch.float32, torch.int32
     _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _one_device = torch.cuda.device_count() == 1
     _codes.update({torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16})     # last: tells that all is there
 
 
@@ -161,7 +162,7 @@ def _stream_of(stream, device):
     tensors elsewhere are refused (last, after every check of the layouts)."""
     if device < 0:
         raise ValueError("expected tensors on a CUDA device")
-    if device != _current_device():
+    if not _one_device and device != _current_device():
         raise ValueError("the tensors' device cuda:%d is not the current one" % device)
     return _raw_stream(device) if stream is None else _stream(stream)
 
@@ -249,6 +250,7 @@ class Checkpoint8:
         self.shape, self.device = codes.shape, codes.get_device()
         self.c = (codes.data_ptr(), _pitch(codes, *codes.shape, "codes"), exps.data_ptr(),
                   _pitch(exps, *exps.shape, "exps"))
+        self.packed = _ckpt_bytes(*self.c)
 
 
 def _ckpt(k, kind, what):
@@ -256,18 +258,13 @@ def _ckpt(k, kind, what):
         return None
     if k.shape != kind[0] or k.device != kind[4]:
         raise ValueError("%s: the checkpoint needs the shape and device of the activations" % what)
-    return _ckpt_bytes(*_held(k, what))
-
-
-def _held(k, what):
-    """The C fields of a checkpoint, whose tensors may have got other storage
-    since they were last looked at."""
-    if k.codes.data_ptr() != k.c[0] or k.exps.data_ptr() != k.c[2]:
-        shape, device = k.shape, k.device
-        k._hold(k.codes, k.exps, shape[1])
-        if k.shape != shape or k.device != device:
+    c = k.c
+    if k.codes.data_ptr() != c[0] or k.exps.data_ptr() != c[2]:
+        # its tensors have got other storage
+        k._hold(k.codes, k.exps, kind[2])
+        if k.shape != kind[0] or k.device != kind[4]:
             raise ValueError("%s: the checkpoint's tensors were replaced by others of another kind" % what)
-    return k.c
+    return k.packed
 
 
 def checkpoint8(x, ckpt, stream=None):
@@ -386,7 +383,7 @@ def block_norm_backward(block, saved_stream, rstd, d_normed, d_residual, d_block
     for i, (t, what) in enumerate(((block, "block"), (saved_stream, "stream"))):
         if isinstance(t, Checkpoint8):
             _ckpt(t, kind, what)
-            held[2 + i] = _held(t, what)
+            held[2 + i] = t.c
         else:
             _like(t, kind, what)
             held[i] = (t.data_ptr(), _pitch(t, rows, cols, what))
@@ -431,14 +428,20 @@ class MoeLayer:
         self._router_dtype = router.dtype
         self.params = ptoc_moe_params(None, None, None, None, _code(router.dtype), self.experts, first_expert, local,
                                       top_k, SCORES[score], int(bool(renormalize)), scale)
-        self._take(self._addresses())
+        self._at = None
+        self._weights()
 
-    def _addresses(self):
-        return (self.router.data_ptr(), None if self.bias is None else self.bias.data_ptr(), self.w_in.data_ptr(),
-                self.w_out.data_ptr())
+    def _weights(self):
+        """The C parameters. The weights may have got other storage since the
+        last call."""
+        bias = self.bias
+        at = (self.router.data_ptr(), bias if bias is None else bias.data_ptr(), self.w_in.data_ptr(),
+              self.w_out.data_ptr())
+        if at != self._at:
+            self._take(at)
+        return self.params
 
     def _take(self, at):
-        """Use the weights at these addresses, which are theirs."""
         dtype, device = self._kind
         router, bias, w_in, w_out = self._shapes
         _packed(self.router, router, self._router_dtype, device, "router")
@@ -447,14 +450,6 @@ class MoeLayer:
         _packed(self.w_out, w_out, dtype, device, "w_out")
         q = self.params
         q.router, q.bias, q.w_in, q.w_out = self._at = at
-
-    def _weights(self):
-        """The C parameters. The weights may have got other storage since the
-        last call."""
-        at = self._addresses()
-        if at != self._at:
-            self._take(at)
-        return self.params
 
     def workspace(self, tokens):
         """A workspace tensor for calls of up to `tokens` tokens."""
