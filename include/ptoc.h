@@ -387,10 +387,12 @@ ptoc_status ptoc_signal_reset(const ptoc_group* signals, cudaStream_t stream);
 /*
  * ptoc_wait_faults - failure detection for the waits inside the library's
  * kernels (no counterpart in the pages). Every wait of the staged and tensor
- * reduction forms on a copy is bounded (2 s, or PTOC_WAIT_NS); a block whose
- * wait gives up stores nothing more and counts one fault on its device. *count receives the faults counted
+ * reduction forms, and of ptoc_moe_few_tokens (ptoc_layers.h), on a copy is
+ * bounded (2 s, or PTOC_WAIT_NS); a block whose wait gives up stores nothing
+ * more (of ptoc_moe_few_tokens: none of its tiles) and counts one fault on its
+ * device. *count receives the faults counted
  * on the current device since the previous call, and the count restarts at
- * zero. 0 means every staged tile of every earlier call was stored. The
+ * zero. 0 means every tile of every earlier call was stored. The
  * read is a synchronous copy on the legacy default stream: call it when the
  * device is idle (after cudaDeviceSynchronize) to include every earlier call.
  * The credit barrier reports its own waits through its status array.

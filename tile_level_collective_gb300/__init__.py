@@ -240,8 +240,9 @@ def ptoc_signal_reset(signals, stream=None, check=True):
 
 
 def ptoc_wait_faults(check=True):
-    """The count of staged-reduction waits that gave up on the current device
-    since the previous call (the count then restarts at zero)."""
+    """The count of waits of the staged reductions and of the mixture of experts
+    that gave up on the current device since the previous call (the count then
+    restarts at zero)."""
     n = ctypes.c_uint32(0)
     st = _lib.ptoc_wait_faults(ctypes.byref(n))
     _done(st, "ptoc_wait_faults", check)

@@ -9,14 +9,18 @@
 // idle unless the next rows are already on their way: one wave of blocks
 // walks the rows, and every warp keeps a queue of copies of its own columns
 // (the parts and the residual of this row and the next ones) in shared memory.
+// That holds up to 8,192 columns. Wider rows take four chunks per thread in 64
+// registers, some of them spilled, and queues of three items (16-bit types) or
+// one (binary32, which is waited for at once).
 //
-// Measured on GB300 (bf16; of 6.68 TB/s copied): 16384 x 8192 of 8 parts 436 us
+// Measured on GB300 (bf16; of 6.79 TB/s copied): 16384 x 8192 of 8 parts 436 us
 // (6.8 TB/s; one block per row without a queue: 650 us); of 1 part 167 us (6.4
 // TB/s), with both checkpoints 212 us (6.4 TB/s); 8192 x 4096 of 1 part 46 us (5.8
 // TB/s), with both checkpoints 58 us (5.8 TB/s: 36 million instructions, 58 % of
 // the issue slots at 16 warps per SM), of 4095 columns 110 us (8 accesses where
-// an aligned row takes one). One row of 7168 columns of 8 parts: 4.9 us on the
-// device.
+// an aligned row takes one). Wide rows of 1 part with both checkpoints: 5461 x
+// 12288 263 us and 2048 x 32768 171 us (floor 99; 8192 x 8192 takes 111). One row
+// of 7168 columns of 8 parts: 4.9 us on the device.
 #include "layers/layers_common.cuh"
 #include "layers/layers_internal.h"
 
@@ -135,8 +139,8 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
 // Through the warps' queues of K items. KEEP: the column factors stay in
 // registers (they do not depend on the row, and two chunks leave room for them).
 // The bound of one block per SM keeps the compiler from saving registers that
-// nothing else would use: 8192 x 4096 with both checkpoints takes 58 us with 95
-// registers and 70 with 82.
+// nothing else would use: 8192 x 4096 with both checkpoints takes 58 us with 105
+// registers, and took 70 with 82 where 95 took 58.
 template <class T, int C, int K, bool KEEP, bool ODD, bool FULL = false>
 __global__ void __launch_bounds__(C == 2 ? 512 : 1024, 1) block_norm_queue_kernel(const NormParams p)
 {

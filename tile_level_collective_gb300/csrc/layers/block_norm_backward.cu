@@ -20,7 +20,7 @@
 // Each block writes its column sums as one partial row, and a second launch
 // adds the partial rows in order (about 4 us).
 //
-// Measured on GB300 (bf16, both launches; of 6.68 TB/s copied): 8192 x 4096
+// Measured on GB300 (bf16, both launches; of 6.79 TB/s copied): 8192 x 4096
 // from checkpoints 71 us (4.8 TB/s), from matrices 77 us (5.2 TB/s), from
 // checkpoints of 4095 columns 99 us; 16384 x 8192 from checkpoints 237 us (5.7
 // TB/s); f32 8192 x 4096 136 us (5.9 TB/s). With 16-bit elements and codes
@@ -627,7 +627,12 @@ __global__ void __launch_bounds__(kSumThreads) norm_backward_sum_kernel(const No
 }
 
 // The queue form: two chunks per thread and 512 threads on an SM; wider rows
-// leave no room for a row of copies ahead. (Two rows ahead of 16-bit elements:
+// leave no room for a row of copies ahead. They take four chunks in 1,024
+// threads, whose five arrays of the row do not fit the registers: 1.8 to 4.6 KB
+// of each thread's are spilled, and 5461 x 12288 from checkpoints takes 1,970 us,
+// 2048 x 32768 1,240 (floor 99; 8192 x 8192 takes 130). A gate for each element,
+// or one matrix beside one checkpoint, goes without the queue too (8192 x 4096:
+// 265 and 120 us). (Two rows ahead of 16-bit elements:
 // 8192 x 4096 from matrices 81 us instead of 77; 16384 x 8192 from checkpoints
 // the same; issuing all of a row's copies during its exchange: 8192 x 4096 from
 // checkpoints 74 us instead of 71.)

@@ -5,7 +5,7 @@
 // holds 8 columns; a warp covers 256 columns of one row, so a block's largest
 // magnitude is two lane exchanges away and nothing is read twice.
 //
-// Measured on GB300 (of 6.68 TB/s copied): 16384 x 8192 bf16 kept in 64 us (6.3
+// Measured on GB300 (of 6.79 TB/s copied): 16384 x 8192 bf16 kept in 64 us (6.3
 // TB/s), restored in 60 us (6.8 TB/s); with one 256-column unit per warp instead
 // of four, and integer conversions, 105 and 147 us. At 8191 columns 96 and 85 us:
 // each run is put together from the two aligned words it lies across, with

@@ -34,14 +34,17 @@
 // 2's first stages are on their way before the barriers in front of it.
 //
 // Measured on GB300 (bf16, of 6.79 TB/s copied): 64 tokens x 128 experts of 4096
-// x 1536 772 us (6.2 TB/s); 32 tokens 660 us; 1 token, 8 of 64 experts of 7168 x
-// 2048, 129 us (5.5 TB/s); 1 token, 8 of 128 of 4096 x 1536, 72 us (4.2 TB/s).
-// With one rounded activation in place of two parts: 749, 651, 129 and 71 us; the
-// second part passes L2 with every tile of weights and takes a stage of the
-// ring. What a call costs beside its stream of weights is about 25 us at 1 token
-// and 60 us at 64: four grid barriers (five with more than 8 tokens) of 1.2 us,
-// the latency of the first copies of either phase (3 us each), the choice (2
-// us), the epilogues, and at 64 tokens the partial tiles and both parts.
+// x 1536 751 to 780 us from box to box (6.3 to 6.1 TB/s); 32 tokens 642 us; 1
+// token, 8 of 64 experts of 7168 x 2048, 128 us (5.5 TB/s); 1 token, 8 of 128 of
+// 4096 x 1536, 71 us (4.2 TB/s); 64 tokens x 16 experts of 1024 x 512 38 us
+// (floor 8: nearly every tile is in parts). With one rounded activation in
+// place of two parts 64 tokens took 729 us where these took 751, 32 tokens 632
+// and one token the same: half of that is the ring's stage that the second part
+// takes, half its passing L2 with every tile of weights. What a call costs
+// beside its stream of weights is 25 us at 1 token and 50 to 80 us at 64: four
+// grid barriers (five with more than 8 tokens) of 1.2 us, the latency of the
+// first copies of either phase (3 us each), the choice (2 us), the epilogues,
+// and at 64 tokens the partial tiles and both parts.
 // Stages of 128 rows (two per tile of gate and up rows) took 829 us at 64 tokens
 // when these took 756, as the tokens' elements then pass L2 twice as often;
 // boxes without promotion to 256 bytes in L2 872 us; stages of 128 elements of
