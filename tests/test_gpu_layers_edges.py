@@ -446,3 +446,27 @@ def test_alignments_that_no_kernel_needs_cost_nothing(odd):
 
         times.append(device_us(step))
     assert times[1] <= 1.4 * times[0], times
+
+
+# ---- factors that are not finite ----------------------------------------------------------
+
+@pytest.mark.parametrize("cols, lead", [(96, 0), (1000, 0), (1003, 0), (515, 1), (9000, 0), (9001, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_block_norm_infinite_gates_reach_only_their_rows(dtype, cols, lead):
+    """An infinite gate makes its row infinite, whose statistic is then 0 at
+    every width: nothing past the row's end takes part."""
+    rows, t = 5, DT[dtype]
+    g = gen(cols)
+    boxes = [Box(rows, cols, t, 0, lead) for _ in range(4)]
+    part, x, out, normed = (b.view for b in boxes)
+    for v in (part, x):
+        v.copy_(rnd(g, (rows, cols), torch.float32).abs() + 1)
+    gate = torch.ones(rows, 1, dtype=t, device="cuda")
+    gate[2] = float("inf")
+    rstd = torch.empty(2, rows, device="cuda")
+    P.block_norm([part], x, out, normed, gate=gate, rstd=rstd)
+    assert bool(torch.isinf(out[2]).all()) and float(rstd[1, 2]) == 0
+    others = [0, 1, 3, 4]
+    assert bool(torch.isfinite(out[others]).all()) and bool((rstd[:, others] > 0).all())
+    P.block_norm([part], x, out, normed, post_norm=False, rstd=rstd, residual_scale=float("inf"))
+    assert bool(torch.isinf(out).all()) and bool((rstd[1] == 0).all())

@@ -95,7 +95,8 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
         sums.end(total);
         ra = 1.0f / sqrtf(total[0] * k.inv_cols + k.eps);
     }
-    const Pair scale = both(ra * row_gate), keep = both(k.residual_scale);
+    // (past the row's end 0 times a factor that is not finite would be NaN)
+    const float scale = ra * row_gate;
     Raw8<T, G> s[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -104,7 +105,10 @@ __device__ __forceinline__ void finish_row(const NormParams& p, int64_t row, F8 
         const F8 r = x[i].expand();
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const Pair n = mul2(mul2(a[i].p[j], scale), KEEP ? gw[KEEP ? i : 0].p[j] : w.p[j]);
+            const bool lo = mask[i] >> (2 * j / G) & 1, hi = mask[i] >> ((2 * j + 1) / G) & 1;
+            const Pair scales = pair(lo ? scale : 0.0f, hi ? scale : 0.0f);
+            const Pair keep = pair(lo ? k.residual_scale : 0.0f, hi ? k.residual_scale : 0.0f);
+            const Pair n = mul2(mul2(a[i].p[j], scales), KEEP ? gw[KEEP ? i : 0].p[j] : w.p[j]);
             a[i].p[j] = fma2(keep, r.p[j], n);
         }
         s[i] = round8<T, G>(a[i]);
