@@ -34,7 +34,7 @@
 // 2's first stages are on their way before the barriers in front of it.
 //
 // Measured on GB300 (bf16, of 6.79 TB/s copied): 64 tokens x 128 experts of 4096
-// x 1536 751 to 780 us from box to box (6.3 to 6.1 TB/s); 32 tokens 642 us; 1
+// x 1536 751 to 780 us from GPU to GPU (6.3 to 6.1 TB/s); 32 tokens 642 us; 1
 // token, 8 of 64 experts of 7168 x 2048, 128 us (5.5 TB/s); 1 token, 8 of 128 of
 // 4096 x 1536, 71 us (4.2 TB/s); 64 tokens x 16 experts of 1024 x 512 38 us
 // (floor 8: nearly every tile is in parts). With one rounded activation in
