@@ -158,12 +158,12 @@ typedef struct {
  *   norm  = sqrt(sum of g^2 over every element of every gradient)
  *   scale = max_norm / (norm + 1e-6) if that is below 1, else 1
  *   g'    = scale * g, rounded once
- * result ([2] floats) receives norm and scale. Up to 32 squares
- * are added in binary32, scaled where that would overflow or underflow, and
- * everything else in binary64: the norm is finite whenever its value fits. With scale 1 gradients in
- * place are not written, and those with an `out` are copied. A norm that is
- * infinite or NaN has scale 1: the caller tells from result[0]. max_norm > 0;
- * infinity asks for the norm alone. Gradients and outs must not overlap one
+ * result ([2] floats) receives norm and scale. Up to 32 squares are added in
+ * binary32, scaled where that would overflow or underflow, and everything else
+ * in binary64: the norm is finite whenever its value fits. With scale 1
+ * gradients in place are not written, and those with an `out` are copied. A norm
+ * that is infinite (one that binary32 cannot hold is) or NaN has scale 1: the
+ * caller tells from result[0]. max_norm > 0; infinity asks for the norm alone. Gradients and outs must not overlap one
  * another, but for an out that is exactly its own gradient (same pitch).
  * More than PTOC_CLIP_MAX_GRADIENTS, or more than 2^45 elements in all, are
  * PTOC_ERR_UNSUPPORTED. count == 0 has norm 0.

@@ -313,8 +313,9 @@ __device__ __forceinline__ void norm_of(const ClipParams<N>& p, double (&sums)[k
     if (threadIdx.x == 0) {
         for (int w = 1; w < used / 32; ++w) sum += sums[w];
         const double root = sqrt(sum), ratio = (double)p.max_norm / (root + 1e-6);
+        // (finite is what the caller reads: a root beyond binary32 is an infinite norm)
         answer[0] = (float)root;
-        answer[1] = isfinite(root) && ratio < 1.0 ? (float)ratio : 1.0f;
+        answer[1] = isfinite(answer[0]) && ratio < 1.0 ? (float)ratio : 1.0f;
     }
     __syncthreads();
     norm = answer[0];
