@@ -4,8 +4,8 @@ import pytest
 import torch
 
 import tile_level_collective_gb300 as P
-from test_gpu_dense import check_clip
-from test_gpu_layers import DT
+from test_gpu_dense import F64, act64, check_clip
+from test_gpu_layers import DT, TINY, U, close
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,67 @@ def test_clip_largest_norm():
     """The largest norms that binary32 holds are finite, and limited."""
     check_clip([torch.full((2,), 2.4e38, device="cuda")], None, 1e30)
     check_clip([torch.full((3,), 1.9e38, device="cuda")], [torch.empty(3, device="cuda")], 1e30)
+
+
+# ---- the activations --------------------------------------------------------------------------
+
+# An activation is off by at most this part of its value (see the header).
+ACT_REL = 2.0 ** -19
+
+
+def picked(gates, dt, hidden):
+    """[n, hidden] rows whose first product with a unit vector is the gate."""
+    w = torch.zeros(gates.numel(), hidden, dtype=dt, device="cuda")
+    w[:, 0] = gates
+    return w
+
+
+GATES = {torch.float16: (-5.5, 2.0 ** 13), torch.bfloat16: (-12.0, 1.0)}       # the lowest gate, and u, which keeps h normal
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("tokens,odd", [(5, 0), (5, 1), (100, 0), (100, 1), (150, 0)])
+def test_activation_tail(dtype, act, tokens, odd):
+    """h one by one, at gates down to where it is nearly zero: relative to itself."""
+    dt = DT[dtype]
+    low, up = GATES[dt]
+    width = 512 + odd
+    g = torch.linspace(low, -0.5, width, device="cuda").to(dt)
+    w_in = torch.cat([picked(g, dt, width), picked(torch.full_like(g, up), dt, width)])
+    w_out = torch.eye(width, dtype=dt, device="cuda")
+    x = torch.zeros(tokens, width, dtype=dt, device="cuda")
+    x[:, 0] = 1
+    y = torch.empty_like(x)
+    f = P.GatedFfn(w_in, w_out, act)
+    f(x, y, workspace=f.workspace(tokens))
+    want = (act64(g.to(F64), act)[0] * up).expand(tokens, width)
+    # one rounding (two where h enters as one number: the second one is exact), and the activation's arithmetic
+    close(y, want, (U[dt] + 2 * ACT_REL) * want.abs(), act)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("tokens,odd", [(5, 0), (5, 1), (100, 0), (150, 0)])
+def test_slope_tail(dtype, act, tokens, odd):
+    """dg and du one by one, as dx and as a weight's gradient shows them."""
+    dt = DT[dtype]
+    low, up = GATES[dt]
+    width = 512 + odd
+    g = torch.linspace(low, -3.0, width, device="cuda").to(dt)
+    pre = torch.cat([g, torch.full_like(g, up)]).expand(tokens, -1).contiguous()
+    dy = torch.full((tokens, width), 1.0, dtype=dt, device="cuda")
+    eye, none = torch.eye(width, dtype=dt, device="cuda"), torch.zeros(width, width, dtype=dt, device="cuda")
+    x = torch.zeros(tokens, width, dtype=dt, device="cuda")
+    x[0, 0] = 1                                           # d_w_in's first column is the first token's dg and du
+    a, slope = act64(g.to(F64), act)
+    for gate in (True, False):
+        f = P.GatedFfn(torch.cat([eye, none] if gate else [none, eye]), eye, act)
+        dx, dw = torch.empty_like(x), torch.empty_like(f.w_in)
+        f.backward(x, pre, dy, d_x=dx, d_w_in=dw, workspace=f.backward_workspace(tokens))
+        # act' is a sum of two terms of opposite signs, which below -3 add to 2.1 times it at most
+        d = slope * up if gate else a
+        bound = (U[dt] + 4 * ACT_REL) * d.abs() + (TINY if dt == torch.float16 else 0)
+        close(dx, d.expand(tokens, width), bound, "dg" if gate else "du")
+        both = torch.cat([slope * up, a])
+        close(dw[:, 0], both, (U[dt] + 4 * ACT_REL) * both.abs() + (TINY if dt == torch.float16 else 0), "d_w_in")

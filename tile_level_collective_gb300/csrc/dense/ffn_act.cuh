@@ -1,4 +1,7 @@
-// The activations of a gated block and their slopes, in binary32.
+// The activations of a gated block and their slopes, in binary32. Against 64 bits, over
+// all f16 and bf16 gates: silu is off by at most 18 units of 2^-24 of its value down to
+// -16 and 64 down to -80 (the exponential's argument is rounded), gelu by 10 at any
+// gate; the slopes by as much of their two terms.
 #pragma once
 
 #include "ptoc_dense.h"
@@ -10,20 +13,41 @@ struct Act {
     float value, slope;
 };
 
-// The Gaussian distribution function and exp(-g^2 / 2): erfc by formula 7.1.26 of
-// Abramowitz and Stegun's Handbook of Mathematical Functions, t (a1 + t (a2 + ..))
-// exp(-x^2) with t = 1 / (1 + p x), which is off by at most 1.5e-7. (By the
-// library's function dg, du and dx of 1003 tokens of 2048 x 5000 took 92 us, where
-// silu's take 75.)
+// Phi(-|g|) / exp(-g^2 / 2), a polynomial in t = 1 / (1 + 0.35 |g|): the function is
+// near 0.4 / |g| far out, so that t takes out what falls and the rest is smooth. The
+// coefficients are a fit of ours for the least largest relative error over |g| <= 16
+// (weighted least squares, the weights taken from the errors until these are level):
+// 3.3e-8 of the value. Their magnitudes add to 1.1 where the sum is 0.14 to 0.5, and
+// six are above zero: the sum's own roundings stay at 2e-7 of it.
+__device__ __forceinline__ float tail_ratio(float a)
+{
+    const float t = __fdividef(1.0f, fmaf(0.35f, a, 1.0f));
+    float p = fmaf(-0.029164927f, t, 0.144065766f);
+    p = fmaf(p, t, -0.255912333f);
+    p = fmaf(p, t, 0.159405142f);
+    p = fmaf(p, t, -0.0232724566f);
+    p = fmaf(p, t, 0.105578549f);
+    p = fmaf(p, t, 0.119814523f);
+    p = fmaf(p, t, 0.139864475f);
+    p = fmaf(p, t, 0.139621243f);
+    return p * t;
+}
+
+// The Gaussian distribution function, to 2^-20 of its value in both tails (the lower
+// one is what gelu leaves of a gate, and its relative error is that of h), and e =
+// exp(-g^2 / 2), as 2^-z with z = (|g| sqrt(log2(e) / 2))^2 in two parts: rounded to one,
+// it would cost g^2 2^-24 of the value. Beyond 16 both are zero in binary32.
+// 8192 tokens of 4096 x 12288 take 1279 us forward where silu takes 1245; dg, du, h and
+// dx of 1003 tokens of 2048 x 5000 77 us, silu's 73, by the library's function 92.
 __device__ __forceinline__ float gauss(float g, float& e)
 {
-    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(g), 1.0f));
-    e = __expf(-0.5f * g * g);
-    float p = fmaf(1.061405429f, t, -1.453152027f);
-    p = fmaf(p, t, 1.421413741f);
-    p = fmaf(p, t, -0.284496736f);
-    p = fmaf(p, t, 0.254829592f);
-    const float tail = 0.5f * p * t * e;
+    constexpr float kRoot = 0.849321800f, kRootRest = 1.76990603e-8f;
+    const float a = fminf(fabsf(g), 16.0f);
+    const float r = a * kRoot, r_rest = fmaf(a, kRootRest, fmaf(a, kRoot, -r));
+    const float z = r * r, z_rest = fmaf(2.0f * r, r_rest, fmaf(r, r, -z));
+    e = exp2f(-z);
+    e = fmaf(e * -0.693147181f, z_rest, e);
+    const float tail = tail_ratio(a) * e;
     return g < 0.0f ? tail : 1.0f - tail;
 }
 
