@@ -45,7 +45,9 @@ typedef struct {
  * then rstd) may be null. Statistics are binary32 (deviations from the mean,
  * not differences of squares) and, like y, of s before its rounding. PTOC_F32,
  * PTOC_F16 and PTOC_BF16; each output is rounded once. A row that holds an
- * infinity or a NaN is NaN in y. out may be exactly x (same pointer and
+ * infinity or a NaN is NaN in y; a finite one whose squared deviations add to
+ * more than binary32 holds (a spread of 1e17 at the least) has rstd 0, and y is
+ * the bias (NaN where the sum of s leaves binary32 too). out may be exactly x (same pointer and
  * pitch); other overlaps of an output are PTOC_ERR_ALIAS. cols above
  * PTOC_NORM_MAX_COLS is PTOC_ERR_UNSUPPORTED. An empty matrix is PTOC_OK
  * without a launch.

@@ -5,7 +5,7 @@ import torch
 
 import tile_level_collective_gb300 as P
 from test_gpu_dense import F64, act64, check_clip
-from test_gpu_layers import DT, TINY, U, close
+from test_gpu_layers import DT, E, TINY, U, close
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,25 @@ def test_slope_tail(dtype, act, tokens, odd):
         close(dx, d.expand(tokens, width), bound, "dg" if gate else "du")
         both = torch.cat([slope * up, a])
         close(dw[:, 0], both, (U[dt] + 4 * ACT_REL) * both.abs() + (TINY if dt == torch.float16 else 0), "d_w_in")
+
+
+# ---- rows at the end of binary32 -----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [1024, 1001, 8192, 16384])
+def test_layer_norm_warps_far_apart(dtype, cols):
+    """Rows whose warps' means are far apart, up to deviations whose squares binary32 cannot add: those
+    have a standard deviation of infinity, so that rstd is 0 and y the bias."""
+    dt = DT[dtype]
+    x = torch.zeros(3, cols, dtype=dt, device="cuda")
+    # a sum of squared deviations of 2.56e38 (cols / 4 times the square), and larger ones
+    x[0, :cols // 2], x[1, :cols // 2], x[2, cols // 2:] = 2.5e17 * (16384 / cols) ** 0.5, 1e19, -1e19
+    y, stats, bias = torch.empty_like(x), torch.empty(2, 3, device="cuda"), torch.full((cols,), 0.5, dtype=dt, device="cuda")
+    for rows in (x, x[:1]):
+        P.layer_norm([rows], y[:len(rows)], bias=bias, stats=stats[:, :len(rows)].contiguous())
+        s = x[:1].to(F64)
+        d = s - s.mean()
+        want = d / d.square().mean().sqrt()
+        # sums of a warp's equal values, and of the warps: as in norm_want
+        close(y[:1], want + 0.5, 256 * E * want.abs() + U[dt] * (want + 0.5).abs())
+        assert bool((y[1:len(rows)] == 0.5).all())
