@@ -104,17 +104,18 @@ typedef struct {
  * not kept. dtype is PTOC_F16 or PTOC_BF16 (others: PTOC_ERR_UNSUPPORTED). Sums
  * are binary32. h is taken from g and u before their rounding and enters the
  * second product rounded to dtype, as a tensor core reads it; up to 64 tokens as
- * two numbers of dtype whose sum keeps 16 (bf16) or 22 (f16) significant bits. y
- * and pre are rounded once. An infinity or a NaN in x stays with its token, and
- * an f16 h beyond 65504 becomes infinite. Outputs must not overlap anything
- * (PTOC_ERR_ALIAS). Tokens above PTOC_FFN_MAX_TOKENS, hidden or inter above
- * PTOC_FFN_MAX_WIDTH are PTOC_ERR_UNSUPPORTED; tokens == 0 is PTOC_OK without a
- * launch.
+ * two numbers of dtype whose sum keeps 16 (bf16) or 22 (f16) significant bits, or in
+ * binary32. y and pre are rounded once. An infinity or a NaN in x stays with its
+ * token, and an f16 h beyond 65504 becomes infinite unless it enters in binary32.
+ * Outputs must not overlap anything (PTOC_ERR_ALIAS). Tokens above
+ * PTOC_FFN_MAX_TOKENS, hidden or inter above PTOC_FFN_MAX_WIDTH are
+ * PTOC_ERR_UNSUPPORTED; tokens == 0 is PTOC_OK without a launch.
  * 16-byte aligned matrices and pitches with hidden and inter multiples of 8 take
  * the tensor cores, in two launches; their waits for copies are bounded by
  * PTOC_WAIT_NS (ptoc.h) and counted by ptoc_wait_faults if they give up (part of
  * the outputs is then missing). Others take plain kernels, a hundred times slower
- * for long batches. A workspace serves all calls of up to its tokens.
+ * for long batches; h is binary32 there up to 64 tokens. A workspace serves all calls
+ * of up to its tokens.
  */
 size_t ptoc_gated_ffn_workspace(int64_t tokens, int64_t hidden, int64_t inter);
 ptoc_status ptoc_gated_ffn(const ptoc_matrix* x, const ptoc_gated_ffn_params* params, const ptoc_matrix* y,
@@ -130,11 +131,11 @@ ptoc_status ptoc_gated_ffn(const ptoc_matrix* x, const ptoc_gated_ffn_params* pa
  *   d_w_in  = [dg, du]^T x                 [2 * inter, hidden]
  *   d_w_out = dy^T (act(g) * u)            [hidden, inter]
  * dx, d_w_in and d_w_out have the call's dtype; each may be null. dg, du and
- * act(g) * u enter the second products rounded to dtype (dg and du in dx's, up to
- * 64 tokens, as two numbers); beyond f16's range they become infinite. Outputs must
- * not overlap anything. Types, limits, waits and forms as ptoc_gated_ffn; up to
- * three launches (five of the plain kernels). With tokens == 0 the gradients of the
- * weights are set to zero.
+ * act(g) * u enter the second products rounded to dtype (up to 64 tokens dg and du
+ * in dx's as two numbers of it, or in binary32); where they are rounded, what is
+ * beyond f16's range becomes infinite. Outputs must not overlap anything. Types,
+ * limits, waits and forms as ptoc_gated_ffn; up to three launches (five of the plain
+ * kernels). With tokens == 0 the gradients of the weights are set to zero.
  */
 size_t ptoc_gated_ffn_backward_workspace(int64_t tokens, int64_t hidden, int64_t inter);
 ptoc_status ptoc_gated_ffn_backward(const ptoc_matrix* x, const ptoc_matrix* pre, const ptoc_gated_ffn_params* params,

@@ -4,8 +4,8 @@ import pytest
 import torch
 
 import tile_level_collective_gb300 as P
-from test_gpu_dense import F64, act64, check_clip
-from test_gpu_layers import DT, E, TINY, U, close
+from test_gpu_dense import F64, act64, box, check_clip, ffn_inputs, product, rounded
+from test_gpu_layers import DT, E, TINY, U, Box, close, rnd
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,57 @@ def test_layer_norm_warps_far_apart(dtype, cols):
         # sums of a warp's equal values, and of the warps: as in norm_want
         close(y[:1], want + 0.5, 256 * E * want.abs() + U[dt] * (want + 0.5).abs())
         assert bool((y[1:len(rows)] == 0.5).all())
+
+
+# ---- numbers that a second product takes in two parts ------------------------------------------------
+
+# A number of the type and what it leaves, rounded again: relative to the number.
+PARTS = {torch.float16: 2.0 ** -22, torch.bfloat16: 2.0 ** -16}
+
+
+def own_rounding(got, want, dt, what):
+    """The error of a result that is rounded once, against that of rounding the 64-bit one: a second
+    rounding of every operand would make it 1.4 times as much."""
+    once = float((want.to(dt).to(F64) - want).norm())
+    off = float((got.to(F64) - want).norm())
+    assert off <= 1.1 * once, "%s: %.3g times a rounding" % (what, off / once)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("tokens,hidden,inter,pad", [(1, 4096, 1000, 0), (8, 512, 520, 0), (9, 512, 520, 8), (37, 264, 1000, 0),
+                                                     (64, 256, 512, 0), (1, 2049, 333, 0), (8, 512, 520, 1), (40, 255, 401, 0),
+                                                     (64, 256, 512, 3)])
+def test_few_tokens_are_rounded_once(dtype, act, tokens, hidden, inter, pad):
+    """Up to 64 tokens h, dg and du reach y and dx in more bits than the type has, at any width and pitch."""
+    dt = DT[dtype]
+    x, w_in, w_out, g = ffn_inputs(tokens, hidden, inter, dt, tokens + hidden)
+    x, w_in, w_out = box(x, pad), box(w_in, pad), box(w_out, pad)
+    f = P.GatedFfn(w_in.view, w_out.view, act)
+    y = Box(tokens, hidden, dt, pad)
+    f(x.view, y.view, workspace=f.workspace(tokens))
+    pre, dy = box(rnd(g, (tokens, 2 * inter), dt), pad), box(rnd(g, (tokens, hidden), dt), pad)
+    dx = Box(tokens, hidden, dt, pad)
+    f.backward(x.view, pre.view, dy.view, d_x=dx.view, workspace=f.backward_workspace(tokens))
+
+    x, w_in, w_out, pre, dy = (b.view.to(F64) for b in (x, w_in, w_out, pre, dy))
+    gu, err = product(x, w_in.t())
+    a, slope = act64(gu[:, :inter], act)
+    u = gu[:, inter:]
+    h = a * u
+    err_h = (slope.abs() * err[:, :inter] + err[:, :inter] ** 2) * u.abs() + a.abs() * err[:, inter:] \
+        + 2 * ACT_REL * h.abs() + 1.2 * err[:, :inter] * err[:, inter:]
+    want, bound = product(h, w_out.t(), err_h + PARTS[dt] * h.abs() + 2.0 ** -36)
+    close(y.view, want, rounded(want, bound, dt), "y")
+    own_rounding(y.view, want, dt, "y")
+
+    dh, err = product(dy, w_out)
+    a, slope = act64(pre[:, :inter], act)
+    u = pre[:, inter:]
+    # act' is a sum of two terms of at most 1.2 together
+    d = torch.cat([dh * u * slope, dh * a], 1)
+    err_d = torch.cat([err * (u * slope).abs() + 4 * ACT_REL * (dh.abs() + err) * u.abs() * 1.2,
+                       err * a.abs() + 2 * ACT_REL * (dh.abs() + err) * a.abs()], 1)
+    want, bound = product(d, w_in, err_d + PARTS[dt] * d.abs() + 2.0 ** -36)
+    close(dx.view, want, rounded(want, bound, dt), "dx")
+    own_rounding(dx.view, want, dt, "dx")

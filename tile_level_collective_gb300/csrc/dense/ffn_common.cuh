@@ -10,6 +10,10 @@ namespace ptoc {
 // Up to this many tokens the products with weights take the form that streams them.
 constexpr int64_t kFewTokens = 128;
 
+// Up to this many tokens h, and dg and du on their way to dx, are kept in more bits
+// than the type has: in two numbers of it, or in binary32.
+constexpr int64_t kPartsTokens = 64;
+
 // The forward pass' workspace holds h: of up to 64 tokens both parts, of 8, 16, 32
 // or 64 rows each; of up to 128 tokens 128 rows. What serves more tokens serves
 // fewer.
@@ -19,7 +23,7 @@ inline int64_t few_rows(int64_t tokens)
     while (rows < tokens) rows *= 2;
     return rows;
 }
-inline int64_t few_parts(int64_t tokens) { return tokens <= 64 ? 2 : 1; }
+inline int64_t few_parts(int64_t tokens) { return tokens <= kPartsTokens ? 2 : 1; }
 
 // The backward pass' workspace, in elements: dg's rows (all parts), du's `plane`
 // elements after them, and h.

@@ -75,7 +75,7 @@ constexpr uint32_t kSharedMost = 113 * 1024;         // two blocks to an SM
 // Numbers that stand for an element of h, dg or du. With two, 128 tokens would have 48 KB
 // to a stage, 32 of them tokens.
 template <int NT>
-constexpr int kParts = NT <= 64 ? 2 : 1;
+constexpr int kParts = NT <= kPartsTokens ? 2 : 1;
 template <int FORM, int NT>
 constexpr int kColumns = kSecond<FORM> ? kParts<NT> * NT : NT < 16 ? 16 : NT;
 template <int FORM, int NT>

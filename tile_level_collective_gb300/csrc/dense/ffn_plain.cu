@@ -1,6 +1,8 @@
 // The gated feed-forward block and its backward pass on the CUDA cores, for
 // operands at any address and pitch: every product is one kernel that reads
-// both operands element by element.
+// both operands element by element. Up to kPartsTokens tokens h, dg and du stay in
+// binary32, where the tensor cores take them as two numbers of the type; with more
+// they are rounded to the type, as there.
 #include "dense/ffn_act.cuh"
 #include "dense/ffn_common.cuh"
 #include "layers/layers_common.cuh"
@@ -20,8 +22,9 @@ struct Operand {
 };
 
 // result(m, n) = sum_k a(m, k) b(n, k), summed over up to two pairs of operands
-// of the same depth. MODE 0: stored; 1: a and b[0] give g, a and b[1] u, and the
-// epilogue stores h (and pre); 2: dh, from which the epilogue stores dg, du and h.
+// of the same depth: A's elements are of TA, B's and all others of T. MODE 0: stored;
+// 1: a and b[0] give g, a and b[1] u, and the epilogue stores h (and pre); 2: dh, from
+// which the epilogue stores dg, du and h. D: the elements of d (MODE 2: h's are T's).
 struct PlainParams {
     Operand a[2], b[2];
     int32_t pairs;
@@ -49,7 +52,7 @@ __device__ __forceinline__ void load_tile(float (&to)[kStep][kTile + 4], const O
     }
 }
 
-template <class T, int MODE, int ACT>
+template <class TA, class T, class D, int MODE, int ACT>
 __global__ void __launch_bounds__(kThreads) ffn_plain_kernel(const PlainParams p)
 {
     pdl_enter();
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(kThreads) ffn_plain_kernel(const PlainParams p
     float acc[kB][4][4] = {};
     for (int pair = 0; pair < (MODE == 1 ? 1 : p.pairs); ++pair)
         for (int64_t k0 = 0; k0 < p.k; k0 += kStep) {
-            load_tile<T>(as, p.a[pair], m0, k0, p.m, p.k);
+            load_tile<TA>(as, p.a[pair], m0, k0, p.m, p.k);
 #pragma unroll
             for (int q = 0; q < kB; ++q) load_tile<T>(bs[q], p.b[MODE == 1 ? q : pair], n0, k0, p.n, p.k);
             __syncthreads();
@@ -81,54 +84,55 @@ __global__ void __launch_bounds__(kThreads) ffn_plain_kernel(const PlainParams p
         for (int j = 0; j < 4; ++j) {
             const int64_t m = m0 + ty + i, n = n0 + tx + j;
             if (m >= p.m || n >= p.n) continue;
-            T* d = (T*)p.d + m * p.ld_d + n;
+            D* d = (D*)p.d + m * p.ld_d + n;
             T* pre = (T*)p.pre + m * p.ld_pre + n;
             if constexpr (MODE == 0) {
-                *d = from_f32<T>(acc[0][i][j]);
+                *d = from_f32<D>(acc[0][i][j]);
             } else if constexpr (MODE == 1) {
                 const float g = acc[0][i][j], u = acc[kB - 1][i][j];
-                *d = from_f32<T>(act_value<ACT>(g) * u);
+                *d = from_f32<D>(act_value<ACT>(g) * u);
                 if (p.pre) pre[0] = from_f32<T>(g), pre[p.inter] = from_f32<T>(u);
             } else {
                 const float dh = acc[0][i][j], u = to_f32(pre[p.inter]);
                 const Act a = act_both<ACT>(to_f32(pre[0]));
-                d[0] = from_f32<T>(dh * u * a.slope);
-                d[p.plane] = from_f32<T>(dh * a.value);
+                d[0] = from_f32<D>(dh * u * a.slope);
+                d[p.plane] = from_f32<D>(dh * a.value);
                 ((T*)p.h)[m * p.ld_d + n] = from_f32<T>(a.value * u);
             }
         }
 }
 
-template <class T, int MODE, int ACT>
+template <class TA, class T, class D, int MODE, int ACT>
 cudaError_t run(PlainParams& p, cudaStream_t s)
 {
     p.tiles_n = (p.n + kTile - 1) / kTile;
     const int64_t tiles = (p.m + kTile - 1) / kTile * p.tiles_n;
-    return launch_kernel(ffn_plain_kernel<T, MODE, ACT>, dim3((unsigned)tiles), kThreads, 0, s, p);
+    return launch_kernel(ffn_plain_kernel<TA, T, D, MODE, ACT>, dim3((unsigned)tiles), kThreads, 0, s, p);
 }
 
-template <class T, int MODE>
+template <class T, class D, int MODE>
 cudaError_t run(PlainParams& p, int act, cudaStream_t s)
 {
-    return act == PTOC_ACT_SILU ? run<T, MODE, PTOC_ACT_SILU>(p, s) : run<T, MODE, PTOC_ACT_GELU>(p, s);
+    return act == PTOC_ACT_SILU ? run<T, T, D, MODE, PTOC_ACT_SILU>(p, s) : run<T, T, D, MODE, PTOC_ACT_GELU>(p, s);
 }
 
 // A result of one product.
-template <class T>
+template <class TA, class T>
 cudaError_t product(Operand a, Operand b, int64_t m, int64_t n, int64_t k, void* d, int64_t ld, cudaStream_t s)
 {
     PlainParams p = {};
     p.a[0] = a, p.b[0] = b, p.pairs = 1;
     p.m = m, p.n = n, p.k = k;
     p.d = d, p.ld_d = ld;
-    return run<T, 0, 0>(p, s);
+    return run<TA, T, T, 0, 0>(p, s);
 }
 
-template <class T>
+// W: the elements of h (its rows take as many bytes of the workspace as two parts).
+template <class T, class W>
 cudaError_t forward(const FfnParams& q, cudaStream_t s)
 {
     const int64_t ip = padded_inter(q.inter);
-    T* h = (T*)q.ws;
+    W* h = (W*)q.ws;
     PlainParams p = {};
     p.a[0] = Operand{q.x, q.ld_x, 1};
     p.b[0] = Operand{q.w_in, q.ld_in, 1};
@@ -136,25 +140,27 @@ cudaError_t forward(const FfnParams& q, cudaStream_t s)
     p.m = q.tokens, p.n = q.inter, p.k = q.hidden;
     p.d = h, p.ld_d = ip;
     p.pre = q.pre, p.ld_pre = q.ld_pre, p.inter = q.inter;
-    const cudaError_t e = run<T, 1>(p, q.act, s);
+    const cudaError_t e = run<T, W, 1>(p, q.act, s);
     if (e != cudaSuccess) return e;
-    return product<T>(Operand{h, ip, 1}, Operand{q.w_out, q.ld_out, 1}, q.tokens, q.hidden, q.inter, q.y, q.ld_y, s);
+    return product<W, T>(Operand{h, ip, 1}, Operand{q.w_out, q.ld_out, 1}, q.tokens, q.hidden, q.inter, q.y, q.ld_y, s);
 }
 
-template <class T>
+// W: the elements of dg and du.
+template <class T, class W>
 cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
 {
     const BackLayout l = back_layout(q.tokens, q.inter);
-    const int64_t ip = l.ld;
-    T *dg = (T*)q.ws, *du = dg + l.plane, *h = dg + l.h;
+    const int64_t ip = l.ld, plane = l.plane * (int64_t)sizeof(T) / (int64_t)sizeof(W);
+    W *dg = (W*)q.ws, *du = dg + plane;
+    T* h = (T*)q.ws + l.h;
     PlainParams p = {};
     p.a[0] = Operand{q.dy, q.ld_dy, 1};
     p.b[0] = Operand{q.w_out, 1, q.ld_out};
     p.pairs = 1;
     p.m = q.tokens, p.n = q.inter, p.k = q.hidden;
-    p.d = dg, p.ld_d = ip, p.plane = l.plane, p.h = h;
+    p.d = dg, p.ld_d = ip, p.plane = plane, p.h = h;
     p.pre = (void*)q.pre, p.ld_pre = q.ld_pre, p.inter = q.inter;
-    cudaError_t e = run<T, 2>(p, q.act, s);
+    cudaError_t e = run<T, W, 2>(p, q.act, s);
     const T* w_up = (const T*)q.w_in + q.inter * q.ld_in;
     if (e == cudaSuccess && q.dx) {
         PlainParams r = {};
@@ -163,16 +169,30 @@ cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
         r.pairs = 2;
         r.m = q.tokens, r.n = q.hidden, r.k = q.inter;
         r.d = q.dx, r.ld_d = q.ld_dx;
-        e = run<T, 0, 0>(r, s);
+        e = run<W, T, T, 0, 0>(r, s);
     }
     const Operand x{q.x, 1, q.ld_x};
     if (e == cudaSuccess && q.d_in)
-        e = product<T>(Operand{dg, 1, ip}, x, q.inter, q.hidden, q.tokens, q.d_in, q.ld_din, s);
+        e = product<W, T>(Operand{dg, 1, ip}, x, q.inter, q.hidden, q.tokens, q.d_in, q.ld_din, s);
     if (e == cudaSuccess && q.d_in)
-        e = product<T>(Operand{du, 1, ip}, x, q.inter, q.hidden, q.tokens, (T*)q.d_in + q.inter * q.ld_din, q.ld_din, s);
+        e = product<W, T>(Operand{du, 1, ip}, x, q.inter, q.hidden, q.tokens, (T*)q.d_in + q.inter * q.ld_din, q.ld_din,
+                          s);
     if (e == cudaSuccess && q.d_out)
-        e = product<T>(Operand{q.dy, 1, q.ld_dy}, Operand{h, 1, ip}, q.hidden, q.inter, q.tokens, q.d_out, q.ld_dout, s);
+        e = product<T, T>(Operand{q.dy, 1, q.ld_dy}, Operand{h, 1, ip}, q.hidden, q.inter, q.tokens, q.d_out, q.ld_dout,
+                          s);
     return e;
+}
+
+template <class T>
+cudaError_t forward(const FfnParams& q, cudaStream_t s)
+{
+    return q.tokens <= kPartsTokens ? forward<T, float>(q, s) : forward<T, T>(q, s);
+}
+
+template <class T>
+cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
+{
+    return q.tokens <= kPartsTokens ? backward<T, float>(q, s) : backward<T, T>(q, s);
 }
 
 }  // namespace
