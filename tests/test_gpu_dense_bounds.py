@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import tile_level_collective_gb300 as P
-from test_gpu_dense import F64, act64, box, check_clip, ffn_inputs, product, rounded
+from test_gpu_dense import F64, act64, box, check_clip, ffn_back_want, ffn_inputs, ffn_want, product, rounded
 from test_gpu_layers import DT, E, TINY, U, Box, close, rnd
 
 pytestmark = pytest.mark.gpu
@@ -169,3 +169,50 @@ def test_few_tokens_are_rounded_once(dtype, act, tokens, hidden, inter, pad):
     want, bound = product(d, w_in, err_d + PARTS[dt] * d.abs() + 2.0 ** -36)
     close(dx.view, want, rounded(want, bound, dt), "dx")
     own_rounding(dx.view, want, dt, "dx")
+
+
+# ---- gradients along the gradient --------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("tokens,hidden,inter", [(40, 64, 96), (100, 64, 96), (200, 136, 96), (40, 65, 97)])
+def test_gated_ffn_gradient_along_itself(act, tokens, hidden, inter):
+    """The library's forward pass in f16 along each of its own gradients: the loss sum(y dy) changes by
+    the gradient times the way, and by nothing near a gradient that is zero, negated or doubled."""
+    dt, part = torch.float16, 2.0 ** -4
+    x, w_in, w_out, g = ffn_inputs(tokens, hidden, inter, dt, 9)
+    dy = rnd(g, (tokens, hidden), dt)
+    f = P.GatedFfn(w_in, w_out, act)
+    ws = f.workspace(tokens)
+    pre, y = torch.empty(tokens, 2 * inter, dtype=dt, device="cuda"), torch.empty_like(x)
+    f(x, y, pre=pre, workspace=ws)
+    got = dict(d_x=torch.empty_like(x), d_w_in=torch.empty_like(w_in), d_w_out=torch.empty_like(w_out))
+    f.backward(x, pre, dy, **got, workspace=f.backward_workspace(tokens))
+    bounds = ffn_back_want(x, pre, dy, w_in, w_out, act, dt)
+    y_bound = float((ffn_want(x, w_in, w_out, act, dt)["y"][1] * dy.to(F64).abs()).sum())
+    for t, name in ((x, "d_x"), (w_in, "d_w_in"), (w_out, "d_w_out")):
+        d = got[name].to(F64)
+        v = d * (float(t.to(F64).norm()) / float(d.norm()))
+        base, change, way = t.clone(), [], []
+        for h in (part, 2 * part):
+            ends = []
+            for sign in (h, -h):
+                t.copy_((base.to(F64) + sign * v).to(dt))
+                f(x, y, workspace=ws)
+                ends.append((t.to(F64), float((y.to(F64) * dy.to(F64)).sum())))
+            change.append(ends[0][1] - ends[1][1])
+            way.append(ends[0][0] - ends[1][0])
+        t.copy_(base)
+        want = [float((d * m).sum()) for m in way]
+        # the cube's part of a difference, which a way twice as long has eight times
+        cubic = (change[1] - 2 * change[0] - (want[1] - 2 * want[0])) / 6
+        off = abs(change[0] - want[0] - cubic)
+        # roundings of y at the four ends (the far two count a third) and of the gradient; the kept g and u are
+        # rounded too, which moves the gradient by what three roundings of dg and du do at most; the way is
+        # 1/16 of the tensor's norm, so that the fifth power's part (4/16^4) and that of the square, which the ends'
+        # own roundings leave (U a 1/16), stay below a hundredth
+        bound = 4 * y_bound + 4 * float((bounds[name][1] * way[0].abs()).sum()) + 0.1 * abs(cubic) + 0.01 * abs(want[0])
+        assert bound < abs(want[0]) / 4, name
+        assert off <= bound, name
+        for wrong in (0.0, -1.0, 2.0):
+            far = (change[1] - 2 * change[0] - wrong * (want[1] - 2 * want[0])) / 6
+            assert abs(change[0] - wrong * want[0] - far) > bound, name
