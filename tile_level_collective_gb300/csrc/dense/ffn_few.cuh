@@ -157,7 +157,9 @@ __global__ void __launch_bounds__(kThreads, 2) ffn_few_kernel(const __grid_const
     const int first = (int)((int64_t)p.depth * rank / p.split), last = (int)((int64_t)p.depth * (rank + 1) / p.split);
 
     // A second product reads its weights before it waits: the launch before it
-    // in the stream is the first product, which waited for everything before. A
+    // in the stream is the first product, which waited for everything before. (The
+    // header forbids other threads to put a launch that writes weights between the
+    // two: one that releases its dependents early would not be waited for.) A
     // warp of its own starts these copies while another one allocates.
     auto weights = [&](int x, uint32_t slot) {
         const uint32_t dst = ring + slot * kStage;

@@ -5,7 +5,9 @@ backward pass, and the global norm of the gradients with clipping.
 The C names take the C arguments; ``layer_norm``, ``layer_norm_backward``,
 ``GatedFfn`` and ``Gradients`` infer sizes, pitches and types from torch tensors
 and refuse (ValueError) what the C calls cannot describe. Outputs and workspaces
-belong to the caller; nothing is allocated on the device in a call.
+belong to the caller; nothing is allocated on the device in a call. While a call
+is being made, no other thread may put work on its stream that writes its tensors
+or uses its workspace (a call is several launches).
 
     import torch, tile_level_collective_gb300 as ptoc
 
