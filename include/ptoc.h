@@ -91,14 +91,20 @@
  *                        L2 for its first tile before it waits for the previous
  *                        kernel of the stream, so that back-to-back calls keep
  *                        DRAM busy across the boundary between them.
- *   PTOC_WAIT_NS=<ns>    the bound on one wait of the staged and tensor forms
- *                        for a copy to land (1 ns to 60 s; default 2 s). A
- *                        block whose wait runs out stores nothing more,
- *                        counts a fault (ptoc_wait_faults), waits (bounded,
- *                        2 s) for its own copies in flight and returns, so
- *                        part of that call's result is missing. Copies of
- *                        valid memory land in microseconds; tiny bounds serve
- *                        to exercise the detection path.
+ *   PTOC_WAIT_NS=<ns>    the bound on one wait of the staged and tensor forms,
+ *                        of ptoc_moe_few_tokens (ptoc_layers.h) and of
+ *                        ptoc_gated_ffn and its backward pass (ptoc_dense.h)
+ *                        for a copy to land (1 ns to 60 s; default 2 s; in
+ *                        the last two also for products, and for the blocks
+ *                        of a cluster, which give up together). A block whose
+ *                        wait runs out stores nothing more (of the gated block
+ *                        with more than 128 tokens, and of its weights'
+ *                        gradients: nothing but tiles whose products were
+ *                        already done), counts a fault (ptoc_wait_faults),
+ *                        waits (bounded, 2 s) for its own copies in flight and
+ *                        returns, so part of that call's result is missing.
+ *                        Copies of valid memory land in microseconds; tiny
+ *                        bounds serve to exercise the detection path.
  */
 #ifndef PTOC_H
 #define PTOC_H
@@ -387,14 +393,15 @@ ptoc_status ptoc_signal_reset(const ptoc_group* signals, cudaStream_t stream);
 /*
  * ptoc_wait_faults - failure detection for the waits inside the library's
  * kernels (no counterpart in the pages). Every wait of the staged and tensor
- * reduction forms, and of ptoc_moe_few_tokens (ptoc_layers.h), on a copy is
- * bounded (2 s, or PTOC_WAIT_NS); a block whose wait gives up stores nothing
- * more (of ptoc_moe_few_tokens: none of its tiles) and counts one fault on its
- * device. *count receives the faults counted
- * on the current device since the previous call, and the count restarts at
- * zero. 0 means every tile of every earlier call was stored. The
- * read is a synchronous copy on the legacy default stream: call it when the
- * device is idle (after cudaDeviceSynchronize) to include every earlier call.
+ * reduction forms, of ptoc_moe_few_tokens (ptoc_layers.h) and of ptoc_gated_ffn
+ * and ptoc_gated_ffn_backward (ptoc_dense.h) is bounded (2 s, or PTOC_WAIT_NS);
+ * a block whose wait gives up stores nothing more (of ptoc_moe_few_tokens: none
+ * of its tiles; of the gated block: see PTOC_WAIT_NS) and counts one fault on its
+ * device. *count receives the faults counted on the current device since the
+ * previous call, and the count restarts at zero. 0 means every tile of every
+ * earlier call was stored. The read is a synchronous copy on the legacy default
+ * stream: call it when the device is idle (after cudaDeviceSynchronize) to
+ * include every earlier call.
  * The credit barrier reports its own waits through its status array.
  */
 ptoc_status ptoc_wait_faults(uint32_t* count);

@@ -13,7 +13,7 @@
  * two captured graphs) need one each. Results do not depend on scheduling: the
  * same call on the same GPU gives the same bits.
  *
- * A call is up to five launches. Until it has returned, no other thread may put
+ * A call may be several launches. Until it has returned, no other thread may put
  * work on its stream that writes its operands or uses its workspace: such work
  * could come between two of them. (It would also be too late to be waited for: up
  * to 128 tokens the second launch of ptoc_gated_ffn and of its backward pass reads
