@@ -95,11 +95,20 @@ typedef enum {
 #define PTOC_FFN_MAX_TOKENS 4194304
 #define PTOC_FFN_MAX_WIDTH 262144
 
-/* The block's weights, in the call's dtype. */
+/* The block's weights, in the call's dtype, and how many numbers of it what passes
+ * between the products takes. One is what a tensor core reads: an output has the
+ * error of two roundings (2.35e-3 of its norm in bf16, 2.9e-4 in f16). Two, the
+ * second one what the first left, keep 16 (bf16) or 22 (f16, in steps of 2^-24 at the
+ * least) significant bits: y and all gradients have the error of their own rounding
+ * (1.65e-3, 2.1e-4), at any number of tokens, width and pitch, for 1.35 times the time
+ * forward and 1.6 to 1.9 times backward (2.4 times below 128 tokens). A call with
+ * parts = 2 needs twice the bytes of workspace that the functions below state. An
+ * infinity in the weights, x or dy meets both numbers there, and may come out as NaN. */
 typedef struct {
     ptoc_matrix w_in;            /* [2 * inter, hidden]: gate rows, then up rows */
     ptoc_matrix w_out;           /* [hidden, inter] */
     int32_t act;                 /* ptoc_act */
+    int32_t parts;               /* 2; or 1 (or 0), where up to 64 tokens y and dx have 2 all the same */
 } ptoc_gated_ffn_params;
 
 /*
@@ -110,9 +119,9 @@ typedef struct {
  * pre ([tokens, 2 * inter]: g, then u) is what the backward pass reads; null:
  * not kept. dtype is PTOC_F16 or PTOC_BF16 (others: PTOC_ERR_UNSUPPORTED). Sums
  * are binary32. h is taken from g and u before their rounding and enters the
- * second product rounded to dtype, as a tensor core reads it; up to 64 tokens as
- * two numbers of dtype whose sum keeps 16 (bf16) or 22 (f16) significant bits, or in
- * binary32. y and pre are rounded once. An infinity or a NaN in x stays with its
+ * second product rounded to dtype, as a tensor core reads it; with two parts, and up
+ * to 64 tokens, as two numbers of dtype whose sum keeps 16 (bf16) or 22 (f16)
+ * significant bits, or in binary32. y and pre are rounded once. An infinity or a NaN in x stays with its
  * token, and an f16 h beyond 65504 becomes infinite unless it enters in binary32.
  * Outputs must not overlap anything (PTOC_ERR_ALIAS). Tokens above
  * PTOC_FFN_MAX_TOKENS, hidden or inter above PTOC_FFN_MAX_WIDTH are
@@ -121,7 +130,7 @@ typedef struct {
  * the tensor cores, in two launches; their waits for copies are bounded by
  * PTOC_WAIT_NS (ptoc.h) and counted by ptoc_wait_faults if they give up (part of
  * the outputs is then missing). Others take plain kernels, a hundred times slower
- * for long batches; h is binary32 there up to 64 tokens. A workspace serves all calls
+ * for long batches; two parts are binary32 there. A workspace serves all calls
  * of up to its tokens.
  */
 size_t ptoc_gated_ffn_workspace(int64_t tokens, int64_t hidden, int64_t inter);
@@ -138,8 +147,8 @@ ptoc_status ptoc_gated_ffn(const ptoc_matrix* x, const ptoc_gated_ffn_params* pa
  *   d_w_in  = [dg, du]^T x                 [2 * inter, hidden]
  *   d_w_out = dy^T (act(g) * u)            [hidden, inter]
  * dx, d_w_in and d_w_out have the call's dtype; each may be null. dg, du and
- * act(g) * u enter the second products rounded to dtype (up to 64 tokens dg and du
- * in dx's as two numbers of it, or in binary32); where they are rounded, what is
+ * act(g) * u enter the second products rounded to dtype (with two parts, and of up to
+ * 64 tokens dg and du in dx's, as two numbers of it or in binary32); what is
  * beyond f16's range becomes infinite. Outputs must not overlap anything. Types,
  * limits, waits and forms as ptoc_gated_ffn; up to three launches (five of the plain
  * kernels). With tokens == 0 the gradients of the weights are set to zero.

@@ -2,6 +2,7 @@
 and every refusal. Each case here breaks a rule or is empty, so none can reach a
 launch. Device addresses are fake and never dereferenced."""
 import ctypes
+import functools
 import os
 import re
 import subprocess
@@ -314,3 +315,24 @@ def test_gradient_layouts():
                                                                      (70, 70, 4, 64), (1, 1, 1, 1)]
     assert rows([wide, t(4, 64), wide], [t(4, 64), wide, t(4, 90)[:, :64]]) == [(70, 64, 4, 64), (64, 70, 4, 64),
                                                                                 (70, 90, 4, 64)]
+
+
+def test_gated_ffn_parts():
+    """Two numbers for what passes between the products: the binding's choice, other numbers, and twice the workspace."""
+    two = fp(parts=2)
+    for call, need in ((ffn, P.ptoc_gated_ffn_workspace(8, 64, 32)),
+                       (functools.partial(fb, dx=m(3)), P.ptoc_gated_ffn_backward_workspace(8, 64, 32))):
+        assert call(q=fp(parts=3)) == BAD and call(q=fp(parts=-1)) == BAD
+        assert call(q=two, nbytes=2 * need - 1) == BAD
+        # the workspace is as long as that: its second half is not another operand's
+        assert call(q=two, nbytes=2 * need, ws=at(0) - 2 * need + 256, x=m(0)) == ALIAS
+    w_in, w_out = t(64, 64), t(64, 32)
+    one = P.GatedFfn(w_in, w_out)
+    both = P.GatedFfn(w_in, w_out, parts=2)
+    assert P.ptoc_gated_ffn_params.from_buffer_copy(one._params()).parts == 1
+    assert P.ptoc_gated_ffn_params.from_buffer_copy(both._params()).parts == 2
+    for name in ("workspace", "backward_workspace"):
+        assert getattr(both, name)(8).numel() == 2 * getattr(one, name)(8).numel()
+    for parts in (0, 3, None):
+        with pytest.raises(ValueError, match="parts"):
+            P.GatedFfn(w_in, w_out, parts=parts)

@@ -216,3 +216,137 @@ def test_gated_ffn_gradient_along_itself(act, tokens, hidden, inter):
         for wrong in (0.0, -1.0, 2.0):
             far = (change[1] - 2 * change[0] - wrong * (want[1] - 2 * want[0])) / 6
             assert abs(change[0] - wrong * want[0] - far) > bound, name
+
+
+# ---- two parts where the caller asks for them --------------------------------------------------------------
+
+TWO_SHAPES = [  # tokens, hidden, inter, pad: streamed and not, both widths of tiles, any pitch and width
+    (1, 520, 512, 0), (37, 264, 1000, 0), (64, 256, 512, 8), (65, 256, 512, 0), (128, 520, 264, 0), (130, 264, 200, 0),
+    (300, 1000, 600, 8), (1300, 2056, 136, 0), (140, 136, 8200, 0), (8, 512, 520, 1), (70, 255, 401, 0), (150, 64, 64, 3)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("tokens,hidden,inter,pad", TWO_SHAPES)
+def test_two_parts(dtype, act, tokens, hidden, inter, pad):
+    """At any number of tokens, y and all three gradients have the error of their own rounding."""
+    dt = DT[dtype]
+    x, w_in, w_out, g = ffn_inputs(tokens, hidden, inter, dt, tokens + hidden)
+    x, w_in, w_out = box(x, pad), box(w_in, pad), box(w_out, pad)
+    f = P.GatedFfn(w_in.view, w_out.view, act, parts=2)
+    pre, dy = box(rnd(g, (tokens, 2 * inter), dt), pad), box(rnd(g, (tokens, hidden), dt), pad)
+    got = dict(y=Box(tokens, hidden, dt, pad), d_x=Box(tokens, hidden, dt, pad), d_w_in=Box(2 * inter, hidden, dt, pad),
+               d_w_out=Box(hidden, inter, dt, pad))
+    kept = Box(tokens, 2 * inter, dt, pad)
+    ws, bws = f.workspace(tokens), f.backward_workspace(tokens)
+    grads = {k: got[k].view for k in ("d_x", "d_w_in", "d_w_out")}
+    for k in range(2):                                     # what a workspace held does not matter
+        ws.fill_(255), bws.fill_(255)
+        f(x.view, got["y"].view, pre=kept.view if k else None, workspace=ws)
+        f.backward(x.view, pre.view, dy.view, **grads, workspace=bws)
+        again = [b.view.clone() for b in got.values()]
+        if k:
+            assert all(torch.equal(a, b) for a, b in zip(again, first))
+        first = again
+    for name, v in grads.items():                          # asked for alone: the same bits
+        one = torch.empty_like(v)
+        f.backward(x.view, pre.view, dy.view, **{name: one}, workspace=bws)
+        assert torch.equal(one, v), name
+    assert all(b.outside_intact() for b in (kept, *got.values())) and P.ptoc_wait_faults() == 0
+
+    low = 2.0 ** -25 if dt == torch.float16 else 2.0 ** -130       # half a step of the second number
+    x, w_in, w_out, pre, dy = (b.view.to(F64) for b in (x, w_in, w_out, pre, dy))
+    gu, err = product(x, w_in.t())
+    close(kept.view, gu, rounded(gu, err, dt), "pre")
+    a, slope = act64(gu[:, :inter], act)
+    u, eg, eu = gu[:, inter:], err[:, :inter], err[:, inter:]
+    h = a * u
+    err_h = (slope.abs() * eg + eg * eg) * u.abs() + a.abs() * eu + 2 * ACT_REL * h.abs() + 1.2 * eg * eu
+    want = dict(y=product(h, w_out.t(), err_h + PARTS[dt] * h.abs() + low))
+    dh, err = product(dy, w_out)
+    a, slope = act64(pre[:, :inter], act)
+    u = pre[:, inter:]
+    d, h = torch.cat([dh * u * slope, dh * a], 1), a * u
+    err_d = torch.cat([err * (u * slope).abs() + 4 * ACT_REL * (dh.abs() + err) * u.abs() * 1.2,
+                       err * a.abs() + 2 * ACT_REL * (dh.abs() + err) * a.abs()], 1) + PARTS[dt] * d.abs() + low
+    want["d_x"], want["d_w_in"] = product(d, w_in, err_d), product(d.t(), x, err_d.t())
+    v, e = product(h.t(), dy, ((2 * ACT_REL + PARTS[dt]) * h.abs() + low).t())
+    want["d_w_out"] = v.t(), e.t()
+    for name, (v, e) in want.items():
+        close(got[name].view, v, rounded(v, e, dt), name)
+        if v.numel() >= 2000:
+            own_rounding(got[name].view, v, dt, name)
+
+
+@pytest.mark.parametrize("tokens", [3, 70, 300])
+def test_two_parts_rows_stay_apart(tokens):
+    """An infinity or a NaN in a token's row changes no other row, and an h beyond f16 is infinite."""
+    for dt in (torch.bfloat16, torch.float16):
+        x, w_in, w_out, _ = ffn_inputs(tokens, 136, 200, dt, 5)
+        f = P.GatedFfn(w_in, w_out, parts=2)
+        ws = f.workspace(tokens)
+        clean, y = torch.empty_like(x), torch.empty_like(x)
+        f(x, clean, workspace=ws)
+        x[1, 3], x[2, 100] = float("inf"), float("nan")
+        if dt == torch.float16:
+            x[0] *= 300
+        f(x, y, workspace=ws)
+        assert not bool(torch.isfinite(y[1:3]).any()) and (dt == torch.bfloat16 or not bool(torch.isfinite(y[0]).all()))
+        assert torch.equal(y[3:], clean[3:])
+
+
+@pytest.mark.parametrize("tokens", [40, 200])
+def test_two_parts_captured_and_on_streams(tokens):
+    """Overlapping calls with a workspace each, eager and replayed, give the bits of one call; so does a call
+    after one whose waits gave up."""
+    dt, jobs = torch.bfloat16, []
+    for k in range(3):
+        x, w_in, w_out, g = ffn_inputs(tokens, 512, 776, dt, k)
+        f = P.GatedFfn(w_in, w_out, parts=2)
+        pre, dy = torch.empty(tokens, 1552, dtype=dt, device="cuda"), rnd(g, (tokens, 512), dt)
+        out = [torch.empty_like(v) for v in (x, x, w_in, w_out)]
+        spaces = f.workspace(tokens), f.backward_workspace(tokens)
+
+        def run(f=f, x=x, pre=pre, dy=dy, out=out, spaces=spaces):
+            f(x, out[0], pre=pre, workspace=spaces[0])
+            f.backward(x, pre, dy, d_x=out[1], d_w_in=out[2], d_w_out=out[3], workspace=spaces[1])
+        run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        jobs.append((run, graph, out, [v.clone() for v in out], torch.cuda.Stream()))
+    for i in range(6):
+        for run, graph, out, _, stream in jobs:
+            with torch.cuda.stream(stream):
+                for v in out:
+                    v.zero_()
+                graph.replay() if i & 1 else run()
+    torch.cuda.synchronize()
+    for _, _, out, want, _ in jobs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    assert P.ptoc_wait_faults() == 0
+
+
+def test_two_parts_waits_that_give_up(monkeypatch):
+    dt = torch.bfloat16
+    x, w_in, w_out, g = ffn_inputs(150, 2048, 1000, dt, 3)
+    f = P.GatedFfn(w_in, w_out, parts=2)
+    ws, bws = f.workspace(150), f.backward_workspace(150)
+    y, pre, dy = torch.empty_like(x), torch.empty(150, 2000, dtype=dt, device="cuda"), rnd(g, (150, 2048), dt)
+    out = [y, *(torch.empty_like(v) for v in (x, w_in, w_out))]
+
+    def run():
+        f(x, y, pre=pre, workspace=ws)
+        f.backward(x, pre, dy, d_x=out[1], d_w_in=out[2], d_w_out=out[3], workspace=bws)
+        torch.cuda.synchronize()
+
+    run()
+    want = [v.clone() for v in out]
+    monkeypatch.setenv("PTOC_WAIT_NS", "1")
+    for _ in range(3):
+        run()
+    assert P.ptoc_wait_faults() > 0
+    monkeypatch.delenv("PTOC_WAIT_NS")
+    run()
+    assert P.ptoc_wait_faults() == 0 and all(torch.equal(a, b) for a, b in zip(out, want))

@@ -38,6 +38,7 @@ ptoc_status check_ffn(const ptoc_gated_ffn_params* q, int64_t tokens, int64_t hi
     if (dtype != PTOC_F16 && dtype != PTOC_BF16) return PTOC_ERR_UNSUPPORTED;
     if (!q || tokens < 0 || hidden < 1 || inter < 1) return PTOC_ERR_INVALID_ARG;
     if (q->act != PTOC_ACT_SILU && q->act != PTOC_ACT_GELU) return PTOC_ERR_INVALID_ARG;
+    if (q->parts < 0 || q->parts > 2) return PTOC_ERR_INVALID_ARG;
     if (tokens > PTOC_FFN_MAX_TOKENS || hidden > PTOC_FFN_MAX_WIDTH || inter > PTOC_FFN_MAX_WIDTH)
         return PTOC_ERR_UNSUPPORTED;
     o.matrix(false, &q->w_in, 2 * inter, hidden, 2);
@@ -218,7 +219,7 @@ extern "C" ptoc_status ptoc_gated_ffn(const ptoc_matrix* x, const ptoc_gated_ffn
     o.matrix(true, y, tokens, hidden, 2);
     if (pre) o.matrix(true, pre, tokens, 2 * inter, 2);
     if (!o.ok) return PTOC_ERR_INVALID_ARG;
-    const size_t need = ptoc_gated_ffn_workspace(tokens, hidden, inter);
+    const size_t need = ptoc_gated_ffn_workspace(tokens, hidden, inter) * (params->parts == 2 ? 2 : 1);
     if (need > 0) {
         if (!workspace || workspace_bytes < need || !aligned(workspace, kWsAlign)) return PTOC_ERR_INVALID_ARG;
         o.add(true, workspace, (int64_t)need);
@@ -242,6 +243,7 @@ extern "C" ptoc_status ptoc_gated_ffn(const ptoc_matrix* x, const ptoc_gated_ffn
     p.hidden = hidden;
     p.inter = inter;
     p.act = params->act;
+    p.parts = params->parts;
     p.vec = o.vec;
     return status_of(launch_ffn(p, dtype, stream));
 }
@@ -270,7 +272,7 @@ extern "C" ptoc_status ptoc_gated_ffn_backward(const ptoc_matrix* x, const ptoc_
     if (d_w_in) o.matrix(true, d_w_in, 2 * inter, hidden, 2);
     if (d_w_out) o.matrix(true, d_w_out, hidden, inter, 2);
     if (!o.ok) return PTOC_ERR_INVALID_ARG;
-    const size_t need = ptoc_gated_ffn_backward_workspace(tokens, hidden, inter);
+    const size_t need = ptoc_gated_ffn_backward_workspace(tokens, hidden, inter) * (params->parts == 2 ? 2 : 1);
     if (need > 0) {
         if (!workspace || workspace_bytes < need || !aligned(workspace, kWsAlign)) return PTOC_ERR_INVALID_ARG;
         o.add(true, workspace, (int64_t)need);
@@ -301,6 +303,7 @@ extern "C" ptoc_status ptoc_gated_ffn_backward(const ptoc_matrix* x, const ptoc_
     p.hidden = hidden;
     p.inter = inter;
     p.act = params->act;
+    p.parts = params->parts;
     p.vec = o.vec;
     return status_of(launch_ffn_backward(p, dtype, stream));
 }

@@ -59,6 +59,7 @@ struct FfnParams {
     char* ws;
     int64_t tokens, hidden, inter;
     int32_t act, vec;                    // vec: every matrix can be addressed in 16-byte words
+    int32_t parts;                       // 2: two numbers for h at any number of tokens
 };
 
 struct FfnBackParams {
@@ -69,6 +70,7 @@ struct FfnBackParams {
     char* ws;
     int64_t tokens, hidden, inter;
     int32_t act, vec;
+    int32_t parts;                       // 2: two numbers for dg, du and h in every product
 };
 
 // Rows of the workspace's activations begin at multiples of 16 bytes.

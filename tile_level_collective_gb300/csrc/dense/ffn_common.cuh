@@ -41,6 +41,18 @@ inline BackLayout back_layout(int64_t tokens, int64_t inter)
     return l;
 }
 
+// The same where every product takes two numbers for each (at most twice the bytes
+// of the above): planes of dg, du and h, and planes of their second numbers.
+inline BackLayout parts_layout(int64_t tokens, int64_t inter)
+{
+    BackLayout l;
+    l.ld = padded_inter(inter);
+    l.plane = l.ld * tokens;
+    l.h = 2 * l.plane;
+    l.elements = 6 * l.plane;
+    return l;
+}
+
 // Any address and pitch.
 cudaError_t launch_ffn_plain(const FfnParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_ffn_backward_plain(const FfnBackParams& p, int dtype, cudaStream_t s);

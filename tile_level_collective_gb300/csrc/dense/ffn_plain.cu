@@ -1,8 +1,8 @@
 // The gated feed-forward block and its backward pass on the CUDA cores, for
 // operands at any address and pitch: every product is one kernel that reads
-// both operands element by element. Up to kPartsTokens tokens h, dg and du stay in
-// binary32, where the tensor cores take them as two numbers of the type; with more
-// they are rounded to the type, as there.
+// both operands element by element. Where the tensor cores take h, dg and du as two
+// numbers of the type (up to kPartsTokens tokens, or where the caller asks for it)
+// they stay in binary32; elsewhere they are rounded to the type, as there.
 #include "dense/ffn_act.cuh"
 #include "dense/ffn_common.cuh"
 #include "layers/layers_common.cuh"
@@ -24,7 +24,7 @@ struct Operand {
 // result(m, n) = sum_k a(m, k) b(n, k), summed over up to two pairs of operands
 // of the same depth: A's elements are of TA, B's and all others of T. MODE 0: stored;
 // 1: a and b[0] give g, a and b[1] u, and the epilogue stores h (and pre); 2: dh, from
-// which the epilogue stores dg, du and h. D: the elements of d (MODE 2: h's are T's).
+// which the epilogue stores dg, du and h. D: the elements of d, H: of MODE 2's h.
 struct PlainParams {
     Operand a[2], b[2];
     int32_t pairs;
@@ -52,7 +52,7 @@ __device__ __forceinline__ void load_tile(float (&to)[kStep][kTile + 4], const O
     }
 }
 
-template <class TA, class T, class D, int MODE, int ACT>
+template <class TA, class T, class D, class H, int MODE, int ACT>
 __global__ void __launch_bounds__(kThreads) ffn_plain_kernel(const PlainParams p)
 {
     pdl_enter();
@@ -97,34 +97,35 @@ __global__ void __launch_bounds__(kThreads) ffn_plain_kernel(const PlainParams p
                 const Act a = act_both<ACT>(to_f32(pre[0]));
                 d[0] = from_f32<D>(dh * u * a.slope);
                 d[p.plane] = from_f32<D>(dh * a.value);
-                ((T*)p.h)[m * p.ld_d + n] = from_f32<T>(a.value * u);
+                ((H*)p.h)[m * p.ld_d + n] = from_f32<H>(a.value * u);
             }
         }
 }
 
-template <class TA, class T, class D, int MODE, int ACT>
+template <class TA, class T, class D, class H, int MODE, int ACT>
 cudaError_t run(PlainParams& p, cudaStream_t s)
 {
     p.tiles_n = (p.n + kTile - 1) / kTile;
     const int64_t tiles = (p.m + kTile - 1) / kTile * p.tiles_n;
-    return launch_kernel(ffn_plain_kernel<TA, T, D, MODE, ACT>, dim3((unsigned)tiles), kThreads, 0, s, p);
+    return launch_kernel(ffn_plain_kernel<TA, T, D, H, MODE, ACT>, dim3((unsigned)tiles), kThreads, 0, s, p);
 }
 
-template <class T, class D, int MODE>
+template <class T, class D, class H, int MODE>
 cudaError_t run(PlainParams& p, int act, cudaStream_t s)
 {
-    return act == PTOC_ACT_SILU ? run<T, T, D, MODE, PTOC_ACT_SILU>(p, s) : run<T, T, D, MODE, PTOC_ACT_GELU>(p, s);
+    return act == PTOC_ACT_SILU ? run<T, T, D, H, MODE, PTOC_ACT_SILU>(p, s)
+                                : run<T, T, D, H, MODE, PTOC_ACT_GELU>(p, s);
 }
 
 // A result of one product.
-template <class TA, class T>
+template <class TA, class T, class TB = T>
 cudaError_t product(Operand a, Operand b, int64_t m, int64_t n, int64_t k, void* d, int64_t ld, cudaStream_t s)
 {
     PlainParams p = {};
     p.a[0] = a, p.b[0] = b, p.pairs = 1;
     p.m = m, p.n = n, p.k = k;
     p.d = d, p.ld_d = ld;
-    return run<TA, T, T, 0, 0>(p, s);
+    return run<TA, TB, T, T, 0, 0>(p, s);
 }
 
 // W: the elements of h (its rows take as many bytes of the workspace as two parts).
@@ -140,19 +141,21 @@ cudaError_t forward(const FfnParams& q, cudaStream_t s)
     p.m = q.tokens, p.n = q.inter, p.k = q.hidden;
     p.d = h, p.ld_d = ip;
     p.pre = q.pre, p.ld_pre = q.ld_pre, p.inter = q.inter;
-    const cudaError_t e = run<T, W, 1>(p, q.act, s);
+    const cudaError_t e = run<T, W, W, 1>(p, q.act, s);
     if (e != cudaSuccess) return e;
     return product<W, T>(Operand{h, ip, 1}, Operand{q.w_out, q.ld_out, 1}, q.tokens, q.hidden, q.inter, q.y, q.ld_y, s);
 }
 
-// W: the elements of dg and du.
-template <class T, class W>
+// W: the elements of dg and du; H: of h.
+template <class T, class W, class H>
 cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
 {
-    const BackLayout l = back_layout(q.tokens, q.inter);
-    const int64_t ip = l.ld, plane = l.plane * (int64_t)sizeof(T) / (int64_t)sizeof(W);
+    // (a plane of two parts, or of one and its second one, has the bytes of binary32)
+    constexpr bool kAll = sizeof(H) == 4;
+    const BackLayout l = kAll ? parts_layout(q.tokens, q.inter) : back_layout(q.tokens, q.inter);
+    const int64_t ip = l.ld, plane = kAll ? l.plane : l.plane * (int64_t)sizeof(T) / (int64_t)sizeof(W);
     W *dg = (W*)q.ws, *du = dg + plane;
-    T* h = (T*)q.ws + l.h;
+    H* h = kAll ? (H*)(du + plane) : (H*)((T*)q.ws + l.h);
     PlainParams p = {};
     p.a[0] = Operand{q.dy, q.ld_dy, 1};
     p.b[0] = Operand{q.w_out, 1, q.ld_out};
@@ -160,7 +163,7 @@ cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
     p.m = q.tokens, p.n = q.inter, p.k = q.hidden;
     p.d = dg, p.ld_d = ip, p.plane = plane, p.h = h;
     p.pre = (void*)q.pre, p.ld_pre = q.ld_pre, p.inter = q.inter;
-    cudaError_t e = run<T, W, 2>(p, q.act, s);
+    cudaError_t e = run<T, W, H, 2>(p, q.act, s);
     const T* w_up = (const T*)q.w_in + q.inter * q.ld_in;
     if (e == cudaSuccess && q.dx) {
         PlainParams r = {};
@@ -169,7 +172,7 @@ cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
         r.pairs = 2;
         r.m = q.tokens, r.n = q.hidden, r.k = q.inter;
         r.d = q.dx, r.ld_d = q.ld_dx;
-        e = run<W, T, T, 0, 0>(r, s);
+        e = run<W, T, T, T, 0, 0>(r, s);
     }
     const Operand x{q.x, 1, q.ld_x};
     if (e == cudaSuccess && q.d_in)
@@ -178,7 +181,7 @@ cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
         e = product<W, T>(Operand{du, 1, ip}, x, q.inter, q.hidden, q.tokens, (T*)q.d_in + q.inter * q.ld_din, q.ld_din,
                           s);
     if (e == cudaSuccess && q.d_out)
-        e = product<T, T>(Operand{q.dy, 1, q.ld_dy}, Operand{h, 1, ip}, q.hidden, q.inter, q.tokens, q.d_out, q.ld_dout,
+        e = product<T, T, H>(Operand{q.dy, 1, q.ld_dy}, Operand{h, 1, ip}, q.hidden, q.inter, q.tokens, q.d_out, q.ld_dout,
                           s);
     return e;
 }
@@ -186,13 +189,14 @@ cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
 template <class T>
 cudaError_t forward(const FfnParams& q, cudaStream_t s)
 {
-    return q.tokens <= kPartsTokens ? forward<T, float>(q, s) : forward<T, T>(q, s);
+    return q.parts == 2 || q.tokens <= kPartsTokens ? forward<T, float>(q, s) : forward<T, T>(q, s);
 }
 
 template <class T>
 cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
 {
-    return q.tokens <= kPartsTokens ? backward<T, float>(q, s) : backward<T, T>(q, s);
+    if (q.parts == 2) return backward<T, float, float>(q, s);
+    return q.tokens <= kPartsTokens ? backward<T, float, T>(q, s) : backward<T, T, T>(q, s);
 }
 
 }  // namespace

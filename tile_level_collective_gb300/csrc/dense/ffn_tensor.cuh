@@ -8,6 +8,14 @@
 //   kBackX    dx = dg w_gate + du w_up
 //   kGrad     the same, d_w_in = [dg, du]^T x and d_w_out = dy^T h (over the tokens), those that are asked for
 //
+// h, dg and du pass between the products in PARTS numbers of the type: one, rounded as
+// a tensor core reads it, or where the caller asks for it two, the second one what
+// the first left, as further planes of the contraction. One makes the error of a
+// result sqrt(2) times that of its own rounding (2.35e-3 of the norm where that is
+// 1.65e-3, bf16); two make the products that read them twice as long (8192 tokens of
+// 4096 x 12288 1620 us forward where one takes 1210, 4680 backward where one takes
+// 2520; 512 tokens 133 and 100, 324 and 205).
+//
 // Two SMs (a cluster of two blocks) work on one tile of 256 rows x BN columns:
 // each holds 128 rows of A and half of B's columns in shared memory, and the
 // mma (cta_group::2, issued by the first block) reads both halves, so that a
@@ -71,7 +79,7 @@ constexpr bool kBByRows = PRODUCT >= kBackIn;
 // A result and its operands.
 struct Problem {
     CUtensorMap a, b;
-    CUtensorMap out;                        // the result; kIn: h; kBackIn: dg, du and h, its planes
+    CUtensorMap out;                        // the result; kIn: h; kBackIn: dg, du and h, its planes (PARTS times)
     int64_t rows, cols;                     // of the result (d_w_in: of one plane)
     uint32_t tiles_m, tiles_n;              // tiles_m: of all planes
     uint32_t plane_tiles;                   // tile rows of a plane
@@ -83,6 +91,7 @@ struct ProductParams {
     CUtensorMap pre_out;                    // kIn: g and u, its planes
     const void* pre;                        // kBackIn (read); kIn: null where pre is not kept
     int64_t ld_pre, inter;                  // inter: from g to u in a row of pre
+    int32_t parts;                          // of what kOut, kBackX and kGrad read
     uint32_t tiles;                         // of all problems
     uint32_t rounds;                        // kGrad: see Order
     uint64_t wait_ns;
@@ -229,11 +238,26 @@ struct Tile {
         plane = m >= q.plane_tiles;         // (there are two at most)
         m -= plane * q.plane_tiles;
     }
-    // The stages of a tile of a problem.
+    // The stages of a tile of a problem: of the planes of its contraction, which are
+    // dg and du in dx, and the parts.
     static __device__ __forceinline__ uint32_t stages(const ProductParams& p, uint32_t which)
     {
-        const bool planes = PRODUCT == kBackX || (PRODUCT == kGrad && which == 0);
-        return (uint32_t)p.q[which].depth * (planes ? 2u : 1u);
+        const bool two = PRODUCT == kBackX || (PRODUCT == kGrad && which == 0);
+        const uint32_t planes = PRODUCT == kIn || PRODUCT == kBackIn ? 1u : (uint32_t)p.parts * (two ? 2u : 1u);
+        return (uint32_t)p.q[which].depth * planes;
+    }
+    // The planes of A and of B in plane n of the contraction. (What has parts lies
+    // as dg, du, h and then their second parts.)
+    __device__ __forceinline__ int plane_a(int n) const
+    {
+        if (PRODUCT == kOut) return n;
+        if (PRODUCT == kBackX || (PRODUCT == kGrad && which == 0)) return n + (n >> 1);
+        return PRODUCT == kGrad && which == 1 ? (int)plane + 3 * n : 0;
+    }
+    __device__ __forceinline__ int plane_b(int n) const
+    {
+        if (PRODUCT == kBackX || (PRODUCT == kGrad && which == 0)) return n & 1;
+        return PRODUCT == kGrad && which == 2 ? 3 * n : 0;
     }
 };
 
@@ -252,6 +276,18 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* v)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         v[2 * i] = Raw8<T, 8>::widen(u[i] & 0xffffu), v[2 * i + 1] = Raw8<T, 8>::widen_high(u[i]);
+}
+
+// What eight elements leave of the values they stand for, rounded (nothing of one
+// that is not finite): f16 in steps of 2^-24 at the least.
+template <class T>
+__device__ __forceinline__ uint4 rest8(const float* v, const uint4& w)
+{
+    float high[8], rest[8];
+    unpack8<T>(w, high);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rest[i] = v[i] - high[i], rest[i] = isfinite(rest[i]) ? rest[i] : 0.0f;
+    return pack8<T>(rest);
 }
 
 // A drain warp's two buffers of 32 rows x 32 columns, a row to a lane, in the
@@ -329,7 +365,7 @@ struct DrainBuffers {
 
 // A warp's part of a tile: rows row0 to row0 + 31 (of plane `plane`), the
 // accumulator's columns from `acc` on, which are the result's from col0 on.
-template <class T, int PRODUCT, int ACT, int BN>
+template <class T, int PRODUCT, int ACT, int BN, int PARTS>
 __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf, uint32_t acc, int64_t row0,
                                       int64_t plane, int64_t col0, const Problem& q)
 {
@@ -340,7 +376,7 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
         if (col0 + c >= q.cols) break;
         const int x = (int)(col0 + c), y = (int)row0;
         if constexpr (PRODUCT == kIn) {
-            uint4 h[4], g[4], u[4];
+            uint4 h[4], rest[4], g[4], u[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float vg[16], vu[16], vh[16];
@@ -350,11 +386,13 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     h[2 * k + i] = pack8<T>(vh + 8 * i);
+                    if constexpr (PARTS == 2) rest[2 * k + i] = rest8<T>(vh + 8 * i, h[2 * k + i]);
                     g[2 * k + i] = pack8<T>(vg + 8 * i);
                     u[2 * k + i] = pack8<T>(vu + 8 * i);
                 }
             }
             buf.put(h, &q.out, x, y, 0);
+            if constexpr (PARTS == 2) buf.put(rest, &q.out, x, y, 1);
             if (p.pre) {
                 buf.put(g, &p.pre_out, x, y, 0);
                 buf.put(u, &p.pre_out, x, y, 1);
@@ -364,26 +402,54 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
             float dh[32];
             load_columns(acc + c, acc + c + 16, *(float(*)[16])dh, *(float(*)[16])(dh + 16));
             buf.fetched();
-            uint4 dg[4], du[4], h[4];
+            if constexpr (PARTS == 1) {
+                uint4 dg[4], du[4], h[4];
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                float g[8], u[8], vg[8], vu[8], vh[8];
-                unpack8<T>(buf.get(0, w), g);
-                unpack8<T>(buf.get(1, w), u);
+                for (int w = 0; w < 4; ++w) {
+                    float g[8], u[8], vg[8], vu[8], vh[8];
+                    unpack8<T>(buf.get(0, w), g);
+                    unpack8<T>(buf.get(1, w), u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float d = dh[8 * w + i];
-                    const Act a = act_both<ACT>(g[i]);
-                    vg[i] = d * u[i] * a.slope;
-                    vu[i] = d * a.value;
-                    vh[i] = a.value * u[i];
+                    for (int i = 0; i < 8; ++i) {
+                        const float d = dh[8 * w + i];
+                        const Act a = act_both<ACT>(g[i]);
+                        vg[i] = d * u[i] * a.slope;
+                        vu[i] = d * a.value;
+                        vh[i] = a.value * u[i];
+                    }
+                    dg[w] = pack8<T>(vg), du[w] = pack8<T>(vu), h[w] = pack8<T>(vh);
                 }
-                dg[w] = pack8<T>(vg), du[w] = pack8<T>(vu), h[w] = pack8<T>(vh);
+                __syncwarp();
+                buf.put(dg, &q.out, x, y, 0);
+                buf.put(du, &q.out, x, y, 1);
+                buf.put(h, &q.out, x, y, 2);
+            } else {
+                // one result at a time: six of them do not fit into registers
+                uint4 wg[4], wu[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) wg[w] = buf.get(0, w), wu[w] = buf.get(1, w);
+                __syncwarp();
+#pragma unroll 1
+                for (int r = 0; r < 3; ++r) {
+                    uint4 high[4], rest[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        float g[8], u[8], v[8];
+                        unpack8<T>(wg[w], g);
+                        unpack8<T>(wu[w], u);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float d = dh[8 * w + i];
+                            const Act a = act_both<ACT>(g[i]);
+                            v[i] = r == 0 ? d * u[i] * a.slope : r == 1 ? d * a.value : a.value * u[i];
+                        }
+                        high[w] = pack8<T>(v);
+                        rest[w] = rest8<T>(v, high[w]);
+                    }
+                    buf.put(high, &q.out, x, y, r);
+                    buf.put(rest, &q.out, x, y, 3 + r);
+                }
             }
-            __syncwarp();
-            buf.put(dg, &q.out, x, y, 0);
-            buf.put(du, &q.out, x, y, 1);
-            buf.put(h, &q.out, x, y, 2);
             if (c + kChunk < kColumns) buf.template fetch<T>(p, row0, col0 + c + kChunk);
         } else {
             float v[32];
@@ -396,7 +462,7 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
     }
 }
 
-template <class T, int PRODUCT, int ACT, int BN>
+template <class T, int PRODUCT, int ACT, int BN, int PARTS>
 __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_constant__ ProductParams p)
 {
     extern __shared__ unsigned char raw[];
@@ -446,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
             const Problem& q = p.q[PRODUCT == kGrad ? tile.which : 0];
             const bool by_rows = PRODUCT == kGrad && tile.which > 0;
             const uint32_t stages = tile.stages(p, PRODUCT == kGrad ? tile.which : 0);
-            const int plane_m = (int)tile.plane, m0 = (int)(tile.m * 2 * kRows + rank * kRows);
+            const int m0 = (int)(tile.m * 2 * kRows + rank * kRows);
             const int n0 = PRODUCT == kIn ? (int)tile.n * (BN / 2) : (int)tile.n * BN + (int)rank * (BN / 2);
             int k = 0, plane = 0;
             for (uint32_t it = 0; it < stages; ++it, ++u) {
@@ -458,15 +524,15 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
                         // the first block expects the bytes of both
                         if (rank == 0) bar_expect(&sh.full[slot], 2 * kStage);
                         if (by_rows) {
-                            pair_copy(at, &q.a, m0, k, plane_m, bar);
-                            pair_copy(at + kABytes / 2, &q.a, m0 + 64, k, plane_m, bar);
+                            pair_copy(at, &q.a, m0, k, tile.plane_a(plane), bar);
+                            pair_copy(at + kABytes / 2, &q.a, m0 + 64, k, tile.plane_a(plane), bar);
                         } else {
-                            pair_copy(at, &q.a, k, m0, plane, bar);
+                            pair_copy(at, &q.a, k, m0, tile.plane_a(plane), bar);
                         }
                     } else if constexpr (kB) {
 #pragma unroll
                         for (int c = 0; c < BN / 2; c += 64)
-                            pair_copy(at + kABytes + c * 128, &q.b, n0 + c, k, plane, bar);
+                            pair_copy(at + kABytes + c * 128, &q.b, n0 + c, k, tile.plane_b(plane), bar);
                     } else {
                         pair_copy(at + kABytes, &q.b, k, n0, PRODUCT == kIn ? (int)rank : 0, bar);
                     }
@@ -474,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
                 __syncwarp();
                 if (++slot == kRing) slot = 0, turn ^= 1;
                 k += kDepth;
-                if (PRODUCT >= kBackX && k >= q.depth * kDepth) k = 0, ++plane;
+                if (PRODUCT != kIn && PRODUCT != kBackIn && k >= q.depth * kDepth) k = 0, ++plane;
             }
         }
         if (lane == 0) sh.sent[warp >> 1] = u;
@@ -536,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
             if (!__all_sync(0xffffffffu, wait(sh, &sh.acc_full[b], n >> 1 & 1, p.wait_ns))) break;
             __syncwarp();
             fence_after();
-            drain<T, PRODUCT, ACT, BN>(p, buf, tmem + b * BN + ((uint32_t)(warp & 3) << 21) + half * kHalf, row0,
+            drain<T, PRODUCT, ACT, BN, PARTS>(p, buf, tmem + b * BN + ((uint32_t)(warp & 3) << 21) + half * kHalf, row0,
                                        tile.plane, col0, p.q[PRODUCT == kGrad ? tile.which : 0]);
             __syncwarp();
             fence_before();
@@ -589,14 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
 
 // ---- host side ------------------------------------------------------------------------
 
-template <class T, int PRODUCT, int ACT, int BN>
+template <class T, int PRODUCT, int ACT, int BN, int PARTS>
 cudaError_t launch_product(ProductParams& p, cudaStream_t s)
 {
     // (at most 2^14 x 2^12 to a problem: the limits of the sizes)
     p.tiles = 0;
     for (const Problem& q : p.q) p.tiles += q.tiles_m * q.tiles_n;
     const int64_t tiles = p.tiles;
-    auto kernel = ffn_product_kernel<T, PRODUCT, ACT, BN>;
+    auto kernel = ffn_product_kernel<T, PRODUCT, ACT, BN, PARTS>;
     static std::atomic<uint64_t> done{0};
     const int most = sm_count() / 2 < kClusters ? sm_count() / 2 : kClusters;
     cudaLaunchConfig_t cfg = {};
@@ -636,9 +702,10 @@ bool encode(CUtensorMap* map, const Matrix& m, int box_cols, int box_rows)
 }
 
 // out = a b: A's rows are the result's, or (a_by_rows) both have the tokens as rows.
+// out_planes: of which the result's tiles are a plane's each.
 template <class T, int PRODUCT, int BN>
 bool add_problem(ProductParams& p, int which, const Matrix& a, const Matrix& b, const Matrix& out,
-                 bool a_by_rows = false)
+                 bool a_by_rows = false, int out_planes = 1)
 {
     const int64_t depth = a_by_rows ? a.rows : a.cols;
     const int64_t columns = PRODUCT == kIn ? BN / 2 : BN;
@@ -646,7 +713,7 @@ bool add_problem(ProductParams& p, int which, const Matrix& a, const Matrix& b, 
     q.rows = out.rows;
     q.cols = out.cols;
     q.plane_tiles = (uint32_t)((q.rows + 2 * kRows - 1) / (2 * kRows));
-    q.tiles_m = q.plane_tiles * (uint32_t)(a_by_rows ? a.planes : 1);
+    q.tiles_m = q.plane_tiles * (uint32_t)out_planes;
     q.tiles_n = (uint32_t)((q.cols + columns - 1) / columns);
     q.depth = (int32_t)((depth + kDepth - 1) / kDepth);
     p.wait_ns = copy_wait_ns();
@@ -654,7 +721,7 @@ bool add_problem(ProductParams& p, int which, const Matrix& a, const Matrix& b, 
            encode<T>(&q.b, b, 64, kBByRows<PRODUCT> ? kDepth : BN / 2) && encode<T>(&q.out, out, kChunk, 32);
 }
 
-template <class T, int PRODUCT, int ACT, int BN>
+template <class T, int PRODUCT, int ACT, int BN, int PARTS>
 cudaError_t product_of(ProductParams& p, const Matrix& a, const Matrix& b, const Matrix& out, cudaStream_t s)
 {
     if (!add_problem<T, PRODUCT, BN>(p, 0, a, b, out)) return cudaErrorNotSupported;
@@ -662,14 +729,14 @@ cudaError_t product_of(ProductParams& p, const Matrix& a, const Matrix& b, const
         const Matrix pre{p.pre, 2, out.rows, out.cols, p.ld_pre, p.inter};
         if (!encode<T>(&p.pre_out, pre, kChunk, 32)) return cudaErrorNotSupported;
     }
-    return launch_product<T, PRODUCT, ACT, BN>(p, s);
+    return launch_product<T, PRODUCT, ACT, BN, PARTS>(p, s);
 }
 
 // The width of the tiles: the one with the least waves of clusters times cycles
 // of a stage, which were measured (narrower tiles have more bytes to copy for a
 // product): 1500 x 7168 x 2048 96 us for h and y in 3 waves of 128 columns, 106 in
 // 2 of 256; 2048 x 4096 x 12288 338 in 11 of 256, 360 in 21 of 128.
-template <class T, int PRODUCT, int ACT>
+template <class T, int PRODUCT, int ACT, int PARTS>
 cudaError_t product(ProductParams& p, const Matrix& a, const Matrix& b, const Matrix& out, cudaStream_t s)
 {
     const int64_t rows = (out.rows + 2 * kRows - 1) / (2 * kRows);
@@ -680,16 +747,16 @@ cudaError_t product(ProductParams& p, const Matrix& a, const Matrix& b, const Ma
     };
     const int64_t wide = cost(256, kStageCycles), middle = cost(128, 310), narrow = cost(64, 260);
     if constexpr (PRODUCT == kOut)
-        if (narrow < middle && narrow < wide) return product_of<T, PRODUCT, ACT, 64>(p, a, b, out, s);
-    if (middle < wide) return product_of<T, PRODUCT, ACT, 128>(p, a, b, out, s);
-    return product_of<T, PRODUCT, ACT, 256>(p, a, b, out, s);
+        if (narrow < middle && narrow < wide) return product_of<T, PRODUCT, ACT, 64, PARTS>(p, a, b, out, s);
+    if (middle < wide) return product_of<T, PRODUCT, ACT, 128, PARTS>(p, a, b, out, s);
+    return product_of<T, PRODUCT, ACT, 256, PARTS>(p, a, b, out, s);
 }
 
-template <class T, int ACT>
+template <class T, int ACT, int PARTS>
 cudaError_t forward(const FfnParams& q, cudaStream_t s)
 {
     const Matrix x = stacked(q.x, 1, q.tokens, q.hidden, q.ld_x);
-    const Matrix h = stacked(q.ws, 1, q.tokens, q.inter, padded_inter(q.inter));
+    const Matrix h = stacked(q.ws, PARTS, q.tokens, q.inter, padded_inter(q.inter));
     const Matrix y = stacked(q.y, 1, q.tokens, q.hidden, q.ld_y);
     const Matrix w_in = stacked(q.w_in, 2, q.inter, q.hidden, q.ld_in);
     const Matrix w_out = stacked(q.w_out, 1, q.hidden, q.inter, q.ld_out);
@@ -697,52 +764,72 @@ cudaError_t forward(const FfnParams& q, cudaStream_t s)
     memset(&p, 0, sizeof(p));
     p.pre = q.pre, p.ld_pre = q.ld_pre;
     p.inter = q.inter;
-    const cudaError_t e = product<T, kIn, ACT>(p, x, w_in, h, s);
-    return e == cudaSuccess ? product<T, kOut, 0>(p, h, w_out, y, s) : e;
+    p.parts = PARTS;
+    const cudaError_t e = product<T, kIn, ACT, PARTS>(p, x, w_in, h, s);
+    return e == cudaSuccess ? product<T, kOut, 0, 1>(p, h, w_out, y, s) : e;
 }
 
-template <class T, int ACT>
+template <class T, int ACT, int PARTS>
 cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
 {
-    const BackLayout l = back_layout(q.tokens, q.inter);
+    // with two parts the weights' gradients read both, which few:: does not keep
+    const bool streamed = PARTS == 1 && q.tokens <= kFewTokens;
+    const BackLayout l = PARTS == 1 ? back_layout(q.tokens, q.inter) : parts_layout(q.tokens, q.inter);
     T* d = (T*)q.ws;
     const Matrix x = stacked(q.x, 1, q.tokens, q.hidden, q.ld_x), dy = stacked(q.dy, 1, q.tokens, q.hidden, q.ld_dy);
-    const Matrix d_gu{d, 2, q.tokens, q.inter, l.ld, l.plane}, h = stacked(d + l.h, 1, q.tokens, q.inter, l.ld);
+    // two parts: dg, du, h and then their second parts, seen as planes from dg and from h on
+    const Matrix d_gu{d, PARTS == 1 ? 2 : 5, q.tokens, q.inter, l.ld, l.plane};
+    const Matrix h{d + l.h, PARTS == 1 ? 1 : 4, q.tokens, q.inter, l.ld, l.plane};
     ProductParams p;
     memset(&p, 0, sizeof(p));
+    p.parts = PARTS;
     cudaError_t e;
     const Matrix w_in = stacked(q.w_in, 2, q.inter, q.hidden, q.ld_in);
     const Matrix d_x = stacked(q.dx, 1, q.tokens, q.hidden, q.ld_dx);
-    if (q.tokens <= kFewTokens) {
+    if (streamed) {
         e = few::backward<T, ACT>(q, s);
     } else {
         const Matrix w_out = stacked(q.w_out, 1, q.hidden, q.inter, q.ld_out);
         p.pre = q.pre, p.ld_pre = q.ld_pre;
         p.inter = q.inter;
-        e = product<T, kBackIn, ACT>(p, dy, w_out, stacked(d, 3, q.tokens, q.inter, l.ld), s);
+        e = product<T, kBackIn, ACT, PARTS>(p, dy, w_out, stacked(d, 3 * PARTS, q.tokens, q.inter, l.ld), s);
         if (e == cudaSuccess && q.dx && !q.d_in && !q.d_out)
-            e = product<T, kBackX, 0>(p, d_gu, w_in, d_x, s);
+            e = product<T, kBackX, 0, 1>(p, d_gu, w_in, d_x, s);
     }
     if (e != cudaSuccess || (!q.d_in && !q.d_out)) return e;
     memset(&p, 0, sizeof(p));
+    p.parts = PARTS;
     const Matrix d_in = stacked(q.d_in, 2, q.inter, q.hidden, q.ld_din);
     const Matrix d_out = stacked(q.d_out, 1, q.hidden, q.inter, q.ld_dout);
-    if ((q.dx && q.tokens > kFewTokens && !add_problem<T, kGrad, 256>(p, 0, d_gu, w_in, d_x)) ||
-        (q.d_in && !add_problem<T, kGrad, 256>(p, 1, d_gu, x, d_in, true)) ||
+    if ((q.dx && !streamed && !add_problem<T, kGrad, 256>(p, 0, d_gu, w_in, d_x)) ||
+        (q.d_in && !add_problem<T, kGrad, 256>(p, 1, d_gu, x, d_in, true, 2)) ||
         (q.d_out && !add_problem<T, kGrad, 256>(p, 2, dy, h, d_out, true)))
         return cudaErrorNotSupported;
     // cycles of a tile: its stages, or what its drain takes
-    const int64_t deep = 2 * p.q[0].depth * kStageCycles, depth = q.d_in ? p.q[1].depth : p.q[2].depth;
+    const int64_t deep = 2 * PARTS * p.q[0].depth * kStageCycles;
+    const int64_t depth = PARTS * (q.d_in ? p.q[1].depth : p.q[2].depth);
     const int64_t flat = depth * kStageCycles > kDrainCycles ? depth * kStageCycles : kDrainCycles;
     p.rounds = (uint32_t)((deep + flat / 2) / flat);
-    return launch_product<T, kGrad, 0, 256>(p, s);
+    return launch_product<T, kGrad, 0, 256, 1>(p, s);
+}
+
+template <class T, int ACT>
+cudaError_t forward(const FfnParams& q, cudaStream_t s)
+{
+    // few:: has two parts up to kPartsTokens
+    if (q.tokens <= (q.parts == 2 ? kPartsTokens : kFewTokens)) return few::forward<T, ACT>(q, s);
+    return q.parts == 2 ? forward<T, ACT, 2>(q, s) : forward<T, ACT, 1>(q, s);
+}
+
+template <class T, int ACT>
+cudaError_t backward(const FfnBackParams& q, cudaStream_t s)
+{
+    return q.parts == 2 ? backward<T, ACT, 2>(q, s) : backward<T, ACT, 1>(q, s);
 }
 
 template <class T>
 cudaError_t forward(const FfnParams& q, cudaStream_t s)
 {
-    if (q.tokens <= kFewTokens)
-        return q.act == PTOC_ACT_SILU ? few::forward<T, PTOC_ACT_SILU>(q, s) : few::forward<T, PTOC_ACT_GELU>(q, s);
     return q.act == PTOC_ACT_SILU ? forward<T, PTOC_ACT_SILU>(q, s) : forward<T, PTOC_ACT_GELU>(q, s);
 }
 

@@ -41,7 +41,7 @@ class ptoc_layer_norm_params(ctypes.Structure):
 
 
 class ptoc_gated_ffn_params(ctypes.Structure):
-    _fields_ = [("w_in", ptoc_matrix), ("w_out", ptoc_matrix), ("act", _i32)]
+    _fields_ = [("w_in", ptoc_matrix), ("w_out", ptoc_matrix), ("act", _i32), ("parts", _i32)]
 
 
 class ptoc_gradient(ctypes.Structure):
@@ -129,10 +129,10 @@ def ptoc_clip_gradients(grads, max_norm, result, workspace, workspace_bytes, str
 # ---- layer norm over torch tensors --------------------------------------------------
 
 _norm_bytes = struct.Struct("PPif").pack
-_ffn_bytes = struct.Struct("PqPqi4x").pack
+_ffn_bytes = struct.Struct("PqPqii").pack
 _gradient_bytes = struct.Struct("PPqqqqi4x").pack
 assert struct.calcsize("PPif") == ctypes.sizeof(ptoc_layer_norm_params)
-assert struct.calcsize("PqPqi4x") == ctypes.sizeof(ptoc_gated_ffn_params)
+assert struct.calcsize("PqPqii") == ctypes.sizeof(ptoc_gated_ffn_params)
 assert struct.calcsize("PPqqqqi4x") == ctypes.sizeof(ptoc_gradient)
 
 
@@ -221,15 +221,19 @@ class GatedFfn:
     """A gated feed-forward block over given weights: ``w_in`` [2 * inter,
     hidden] (gate rows, then up rows) and ``w_out`` [hidden, inter], in float16
     or bfloat16, with rows at any pitch. ``act`` is "silu" or "gelu". The weights
-    are used in place, where they are at each call."""
+    are used in place, where they are at each call. ``parts`` = 2: what passes
+    between the products (act(g) * u, and the gradients of g and u) is held in two
+    numbers of the weights' dtype instead of one, at up to twice the time."""
 
-    def __init__(self, w_in, w_out, act="silu"):
+    def __init__(self, w_in, w_out, act="silu", parts=1):
         if w_in.dim() != 2 or w_out.dim() != 2 or w_in.shape != (2 * w_out.shape[1], w_out.shape[0]):
             raise ValueError("GatedFfn: expected w_in [2 * inter, hidden] and w_out [hidden, inter]")
         if act not in ACTIVATIONS:
             raise ValueError("GatedFfn: act is one of %s" % sorted(ACTIVATIONS))
+        if parts not in (1, 2):
+            raise ValueError("GatedFfn: parts is 1 or 2")
         self.hidden, self.inter = w_out.shape
-        self.w_in, self.w_out, self.act = w_in, w_out, act
+        self.w_in, self.w_out, self.act, self.parts = w_in, w_out, act, parts
         self.dtype, self.device = w_in.dtype, w_in.device
         self.code = _code(self.dtype)
         if self.code not in (F16, BF16):
@@ -242,24 +246,26 @@ class GatedFfn:
         """The C parameters. The weights may have got other storage since the
         last call."""
         at = (self.w_in.data_ptr(), self.w_out.data_ptr(), self.w_in.stride(), self.w_out.stride(), self.w_in.shape,
-              self.w_out.shape, self.w_in.dtype, self.w_out.dtype, self.act)
+              self.w_out.shape, self.w_in.dtype, self.w_out.dtype, self.act, self.parts)
         if at != self._at:
             dtype, device = self._kind
             for t, rows, cols, what in ((self.w_in, 2 * self.inter, self.hidden, "w_in"),
                                         (self.w_out, self.hidden, self.inter, "w_out")):
                 _matrix(t, rows, cols, dtype, device, what)
             self._packed = _ffn_bytes(at[0], _pitch(self.w_in, 2 * self.inter, self.hidden, "w_in"), at[1],
-                                      _pitch(self.w_out, self.hidden, self.inter, "w_out"), ACTIVATIONS[self.act])
+                                      _pitch(self.w_out, self.hidden, self.inter, "w_out"), ACTIVATIONS[self.act],
+                                      self.parts)
             self._at = at
         return self._packed
 
     def workspace(self, tokens):
         """A workspace tensor for calls of up to `tokens` tokens."""
-        return _workspace(ptoc_gated_ffn_workspace(tokens, self.hidden, self.inter), self.device)
+        return _workspace(self.parts * ptoc_gated_ffn_workspace(tokens, self.hidden, self.inter), self.device)
 
     def backward_workspace(self, tokens):
         """A workspace tensor for backward passes of up to `tokens` tokens."""
-        return _workspace(ptoc_gated_ffn_backward_workspace(tokens, self.hidden, self.inter), self.device)
+        return _workspace(self.parts * ptoc_gated_ffn_backward_workspace(tokens, self.hidden, self.inter),
+                          self.device)
 
     def _tokens(self, x):
         kind = _first(x, "x")
