@@ -8,10 +8,10 @@
 // columns; wider rows take four chunks per thread.
 //
 // Measured on GB300 (bf16, of 6.8 TB/s copied): 8192 x 4096 with a residual 46 us
-// (5.8 TB/s; straight from memory 57), 16384 x 8192 167 us (6.4 TB/s), of 8 parts
-// 443 us (6.7 TB/s); without a residual 31 and 113 us (4.7 TB/s: 16 warps per SM
-// issue in 60 % of the slots); 8192 x 4095 66 us; 4096 x 16384 115 us. One row of
-// 7168 columns of 8 parts: 7 us on the device.
+// (5.8 TB/s; straight from memory 57), 16384 x 8192 163 us (6.6 TB/s), of 8 parts
+// 441 us (6.7 TB/s); without a residual 31 and 112 us (4.7 TB/s: latency at 16
+// warps per SM, which issue in 61 % of the slots); 8192 x 4095 66 us; 4096 x 16384
+// 100 us. One row of 7168 columns of 8 parts: 4.6 us in a graph.
 #include "layers/layers_common.cuh"
 #include "dense/dense_internal.h"
 #include "host/host_checks.h"

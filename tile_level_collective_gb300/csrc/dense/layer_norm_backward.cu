@@ -11,7 +11,7 @@
 // Measured on GB300 (bf16, both launches, of 6.8 TB/s copied): 16384 x 8192 with
 // du 181 us (5.9 TB/s; straight from memory 243), without 160; 8192 x 4096 56 and
 // 50 us; f32 88 and 70 us (6.1 TB/s); 8192 x 4095 63 and 56 us. With 16-bit elements
-// half of the issue slots at 16 warps per SM, which 125 registers allow. Wide
+// latency at 16 warps per SM, which 125 registers allow: half of the issue slots. Wide
 // rows: 4096 x 16384 184 us.
 #include "layers/layers_common.cuh"
 #include "dense/dense_internal.h"
