@@ -336,3 +336,16 @@ def test_gated_ffn_parts():
     for parts in (0, 3, None):
         with pytest.raises(ValueError, match="parts"):
             P.GatedFfn(w_in, w_out, parts=parts)
+
+
+def test_header_offsets_match(tmp_path):
+    """Members whose place a size does not tell."""
+    src, exe = tmp_path / "o.c", tmp_path / "o"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "ptoc_dense.h"\nint main(void) {\n'
+                   'printf("%d %d %d\\n", (int)offsetof(ptoc_gated_ffn_params, act), '
+                   '(int)offsetof(ptoc_gated_ffn_params, parts), (int)offsetof(ptoc_gradient, dtype)); return 0; }\n')
+    subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), "-I",
+                    cuda_include(), "-o", str(exe), str(src)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True).stdout.split()
+    assert [int(v) for v in out] == [P.ptoc_gated_ffn_params.act.offset, P.ptoc_gated_ffn_params.parts.offset,
+                                     P.ptoc_gradient.dtype.offset]
