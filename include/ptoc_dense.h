@@ -54,9 +54,9 @@ typedef struct {
  * PTOC_F16 and PTOC_BF16; each output is rounded once. A row that holds an
  * infinity or a NaN is NaN in y; a finite one whose squared deviations add to
  * more than binary32 holds (a spread of 1e17 at the least) has rstd 0, and y is
- * the bias (NaN where the sum of s leaves binary32 too). out may be exactly x (same pointer and
- * pitch); other overlaps of an output are PTOC_ERR_ALIAS. cols above
- * PTOC_NORM_MAX_COLS is PTOC_ERR_UNSUPPORTED. An empty matrix is PTOC_OK
+ * the bias (NaN where the sum of s leaves binary32 too). out may be exactly x
+ * (same pointer and pitch); other overlaps of an output are PTOC_ERR_ALIAS. cols
+ * above PTOC_NORM_MAX_COLS is PTOC_ERR_UNSUPPORTED. An empty matrix is PTOC_OK
  * without a launch.
  */
 ptoc_status ptoc_layer_norm(const ptoc_group* parts, int64_t ld_parts, const ptoc_matrix* x,
@@ -121,10 +121,10 @@ typedef struct {
  * are binary32. h is taken from g and u before their rounding and enters the
  * second product rounded to dtype, as a tensor core reads it; with two parts, and up
  * to 64 tokens, as two numbers of dtype whose sum keeps 16 (bf16) or 22 (f16)
- * significant bits, or in binary32. y and pre are rounded once. An infinity or a NaN in x stays with its
- * token, and an f16 h beyond 65504 becomes infinite unless it enters in binary32.
- * Outputs must not overlap anything (PTOC_ERR_ALIAS). Tokens above
- * PTOC_FFN_MAX_TOKENS, hidden or inter above PTOC_FFN_MAX_WIDTH are
+ * significant bits, or in binary32. y and pre are rounded once. An infinity or a
+ * NaN in x stays with its token, and an f16 h beyond 65504 becomes infinite unless
+ * it enters in binary32. Outputs must not overlap anything (PTOC_ERR_ALIAS). Tokens
+ * above PTOC_FFN_MAX_TOKENS, hidden or inter above PTOC_FFN_MAX_WIDTH are
  * PTOC_ERR_UNSUPPORTED; tokens == 0 is PTOC_OK without a launch.
  * 16-byte aligned matrices and pitches with hidden and inter multiples of 8 take
  * the tensor cores, in two launches; their waits for copies are bounded by
@@ -149,9 +149,10 @@ ptoc_status ptoc_gated_ffn(const ptoc_matrix* x, const ptoc_gated_ffn_params* pa
  * dx, d_w_in and d_w_out have the call's dtype; each may be null. dg, du and
  * act(g) * u enter the second products rounded to dtype (with two parts, and of up to
  * 64 tokens dg and du in dx's, as two numbers of it or in binary32); what is
- * beyond f16's range becomes infinite. Outputs must not overlap anything. Types,
- * limits, waits and forms as ptoc_gated_ffn; up to three launches (five of the plain
- * kernels). With tokens == 0 the gradients of the weights are set to zero.
+ * beyond f16's range becomes infinite unless it enters in binary32. Outputs must not
+ * overlap anything. Types, limits, waits and forms as ptoc_gated_ffn; up to three
+ * launches (five of the plain kernels). With tokens == 0 the gradients of the
+ * weights are set to zero.
  */
 size_t ptoc_gated_ffn_backward_workspace(int64_t tokens, int64_t hidden, int64_t inter);
 ptoc_status ptoc_gated_ffn_backward(const ptoc_matrix* x, const ptoc_matrix* pre, const ptoc_gated_ffn_params* params,
@@ -184,10 +185,10 @@ typedef struct {
  * in binary64: the norm is finite whenever its value fits. With scale 1
  * gradients in place are not written, and those with an `out` are copied. A norm
  * that is infinite (one that binary32 cannot hold is) or NaN has scale 1: the
- * caller tells from result[0]. max_norm > 0; infinity asks for the norm alone. Gradients and outs must not overlap one
- * another, but for an out that is exactly its own gradient (same pitch).
- * More than PTOC_CLIP_MAX_GRADIENTS, or more than 2^45 elements in all, are
- * PTOC_ERR_UNSUPPORTED. count == 0 has norm 0.
+ * caller tells from result[0]. max_norm > 0; infinity asks for the norm alone.
+ * Gradients and outs must not overlap one another, but for an out that is exactly
+ * its own gradient (same pitch). More than PTOC_CLIP_MAX_GRADIENTS, or more than
+ * 2^45 elements in all, are PTOC_ERR_UNSUPPORTED. count == 0 has norm 0.
  */
 size_t ptoc_clip_gradients_workspace(int32_t count);
 ptoc_status ptoc_clip_gradients(const ptoc_gradient* grads, int32_t count, float max_norm, float* result,

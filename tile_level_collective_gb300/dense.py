@@ -234,7 +234,7 @@ class GatedFfn:
         if parts not in (1, 2):
             raise ValueError("GatedFfn: parts is 1 or 2")
         self.hidden, self.inter = w_out.shape
-        self.w_in, self.w_out, self.act, self.parts = w_in, w_out, act, parts
+        self.w_in, self.w_out, self.act, self.parts = w_in, w_out, act, int(parts)
         self.dtype, self.device = w_in.dtype, w_in.device
         self.code = _code(self.dtype)
         if self.code not in (F16, BF16):
