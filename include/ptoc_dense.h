@@ -118,14 +118,17 @@ typedef struct {
  *   y      = w_out h
  * pre ([tokens, 2 * inter]: g, then u) is what the backward pass reads; null:
  * not kept. dtype is PTOC_F16 or PTOC_BF16 (others: PTOC_ERR_UNSUPPORTED). Sums
- * are binary32. h is taken from g and u before their rounding and enters the
- * second product rounded to dtype, as a tensor core reads it; with two parts, and up
- * to 64 tokens, as two numbers of dtype whose sum keeps 16 (bf16) or 22 (f16)
- * significant bits, or in binary32. y and pre are rounded once. An infinity or a
- * NaN in x stays with its token, and an f16 h beyond 65504 becomes infinite unless
- * it enters in binary32. Outputs must not overlap anything (PTOC_ERR_ALIAS). Tokens
- * above PTOC_FFN_MAX_TOKENS, hidden or inter above PTOC_FFN_MAX_WIDTH are
- * PTOC_ERR_UNSUPPORTED; tokens == 0 is PTOC_OK without a launch.
+ * are binary32. Tensor cores cut them off where others round: in chains of at most
+ * 32768 terms, whose sums are rounded, by 5e-5 of a long sum of random signs and
+ * 2.5e-4 of one of one sign (in proportion less for shorter chains). h is taken from
+ * g and u before their rounding and enters the second product rounded to dtype, as
+ * a tensor core reads it; with two parts, and up to 64 tokens, as two numbers of
+ * dtype whose sum keeps 16 (bf16) or 22 (f16) significant bits, or in binary32. y and
+ * pre are rounded once. An infinity or a NaN in x stays with its token, and an f16 h
+ * beyond 65504 becomes infinite unless it enters in binary32. Outputs must not
+ * overlap anything (PTOC_ERR_ALIAS). Tokens above PTOC_FFN_MAX_TOKENS, hidden or
+ * inter above PTOC_FFN_MAX_WIDTH are PTOC_ERR_UNSUPPORTED; tokens == 0 is PTOC_OK
+ * without a launch.
  * 16-byte aligned matrices and pitches with hidden and inter multiples of 8 take
  * the tensor cores, in two launches; their waits for copies are bounded by
  * PTOC_WAIT_NS (ptoc.h) and counted by ptoc_wait_faults if they give up (part of

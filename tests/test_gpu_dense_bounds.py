@@ -328,12 +328,14 @@ def test_two_parts_captured_and_on_streams(tokens):
     assert P.ptoc_wait_faults() == 0
 
 
-def test_two_parts_waits_that_give_up(monkeypatch):
+@pytest.mark.parametrize("parts,tokens,hidden,inter", [(2, 150, 2048, 1000), (1, 40000, 264, 264), (1, 130, 264, 33000)])
+def test_two_parts_and_long_sums_waits_that_give_up(parts, tokens, hidden, inter, monkeypatch):
+    """With a bound of 1 ns waits on valid copies run out: the calls end, and the next ones are whole."""
     dt = torch.bfloat16
-    x, w_in, w_out, g = ffn_inputs(150, 2048, 1000, dt, 3)
-    f = P.GatedFfn(w_in, w_out, parts=2)
-    ws, bws = f.workspace(150), f.backward_workspace(150)
-    y, pre, dy = torch.empty_like(x), torch.empty(150, 2000, dtype=dt, device="cuda"), rnd(g, (150, 2048), dt)
+    x, w_in, w_out, g = ffn_inputs(tokens, hidden, inter, dt, 3)
+    f = P.GatedFfn(w_in, w_out, parts=parts)
+    ws, bws = f.workspace(tokens), f.backward_workspace(tokens)
+    y, pre, dy = torch.empty_like(x), torch.empty(tokens, 2 * inter, dtype=dt, device="cuda"), rnd(g, (tokens, hidden), dt)
     out = [y, *(torch.empty_like(v) for v in (x, w_in, w_out))]
 
     def run():
@@ -350,3 +352,91 @@ def test_two_parts_waits_that_give_up(monkeypatch):
     monkeypatch.delenv("PTOC_WAIT_NS")
     run()
     assert P.ptoc_wait_faults() == 0 and all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ---- calls at the limits, and several threads' ------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("parts", [1, 2])
+@pytest.mark.parametrize("tokens,hidden,inter", [
+    (3, P.FFN_MAX_WIDTH, 8), (3, 8, P.FFN_MAX_WIDTH), (200, P.FFN_MAX_WIDTH, 8), (200, 8, P.FFN_MAX_WIDTH),
+    (P.FFN_MAX_TOKENS, 8, 8), (100001, 64, 72), (300000, 40, 24), (130, 264, 33000), (500, 33000, 264), (33000, 264, 520),
+    (33000, 1024, 2048)])
+def test_gated_ffn_long_sums(dtype, tokens, hidden, inter, parts):
+    """The widest blocks and the longest batches keep the error of their roundings. (In one chain 2^22
+    tokens lose 4e-3 of the weights' gradients: the tensor cores cut sums off.)"""
+    dt = DT[dtype]
+    x, w_in, w_out, g = ffn_inputs(tokens, hidden, inter, dt, 11)
+    f = P.GatedFfn(w_in, w_out, parts=parts)
+    y, pre, dy = torch.empty_like(x), torch.empty(tokens, 2 * inter, dtype=dt, device="cuda"), rnd(g, (tokens, hidden), dt)
+    f(x, y, pre=pre, workspace=f.workspace(tokens))
+    got = dict(d_x=torch.empty_like(x), d_w_in=torch.empty_like(w_in), d_w_out=torch.empty_like(w_out))
+    f.backward(x, pre, dy, **got, workspace=f.backward_workspace(tokens))
+    assert P.ptoc_wait_faults() == 0
+    x, w_in, w_out, dy = (t.to(F64) for t in (x, w_in, w_out, dy))
+    gu = x @ w_in.t()
+    want = dict(pre=gu, y=(act64(gu[:, :inter], "silu")[0] * gu[:, inter:]) @ w_out.t())
+    p = pre.to(F64)
+    a, slope = act64(p[:, :inter], "silu")
+    dh = dy @ w_out
+    d = torch.cat([dh * p[:, inter:] * slope, dh * a], 1)
+    want.update(d_x=d @ w_in, d_w_in=d.t() @ x, d_w_out=dy.t() @ (a * p[:, inter:]))
+    for name, v in dict(got, y=y, pre=pre).items():
+        once = float((want[name].to(dt).to(F64) - want[name]).norm() / want[name].norm())
+        off = float((v.to(F64) - want[name]).norm() / want[name].norm())
+        # one rounding, and of what enters the product another one (of the same size: independent of it), a tenth
+        # for the few values that a result may have; a chain of 32768 elements (of the two parts 65536) cut off at every
+        # 16th is off by at most 2^-24 for each of its sums on the average, which lie between 0 and the last one
+        roundings = 1.1 * once * (2 ** 0.5 if parts == 1 else 1)
+        assert off <= roundings + 2048 * 2.0 ** -25, "%s: %.3g, %.3g times a rounding" % (name, off, off / once)
+
+
+@pytest.mark.parametrize("shared", [True, False])
+def test_threads_at_once(shared):
+    """Threads that call on one stream, launch between launch, or on a stream each, with tensors and
+    workspaces of their own: the bits of calls one after another."""
+    import threading
+    dt, jobs = torch.bfloat16, []
+    for k, tokens in enumerate((1, 33, 100, 200)):
+        x, w_in, w_out, g = ffn_inputs(tokens, 512, 776, dt, k)
+        f = P.GatedFfn(w_in, w_out, parts=1 + k % 2)
+        pre, dy = torch.empty(tokens, 1552, dtype=dt, device="cuda"), rnd(g, (tokens, 512), dt)
+        out = [torch.empty_like(v) for v in (x, x, w_in, w_out)]
+        spaces = f.workspace(tokens), f.backward_workspace(tokens)
+        result, normed = torch.empty(2, device="cuda"), torch.empty_like(x)
+        grads = P.Gradients(out[2:], [torch.empty_like(v) for v in out[2:]])
+        cs = grads.workspace()
+
+        def run(stream, f=f, x=x, pre=pre, dy=dy, out=out, spaces=spaces, grads=grads, cs=cs, result=result, normed=normed):
+            P.layer_norm([x], normed, stream=stream)
+            f(normed, out[0], pre=pre, workspace=spaces[0], stream=stream)
+            f.backward(normed, pre, dy, d_x=out[1], d_w_in=out[2], d_w_out=out[3], workspace=spaces[1], stream=stream)
+            grads.clip(1.0, result, workspace=cs, stream=stream)
+        jobs.append((run, out + grads.outs + [result, normed, pre]))
+    one = torch.cuda.Stream()
+    for run, _ in jobs:
+        run(one)
+    torch.cuda.synchronize()
+    want = [[v.clone() for v in out] for _, out in jobs]
+    for _, out in jobs:
+        for v in out:
+            v.zero_()
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(run, stream):
+        try:
+            for _ in range(30):
+                run(stream)
+        except Exception as e:                             # shown by the test's thread
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(run, one if shared else torch.cuda.Stream())) for run, _ in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and P.ptoc_wait_faults() == 0
+    for (_, out), ref in zip(jobs, want):
+        assert all(torch.equal(a, b) for a, b in zip(out, ref))

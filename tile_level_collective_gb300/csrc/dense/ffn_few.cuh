@@ -364,8 +364,10 @@ cudaError_t launch(Params& p, int64_t rows, int64_t depth, cudaStream_t s)
     p.rows = (int32_t)rows;
     p.plane_depth = (int32_t)((depth + kDepth - 1) / kDepth);
     p.depth = FORM == kBackX ? 2 * p.plane_depth : p.plane_depth;
-    // as many blocks as run at a time, each with a stage at least
+    // as many blocks as run at a time, each with a stage at least; more where a
+    // block's sums would be longer than a chain (of the widest blocks two chains)
     int64_t split = kSlots / tiles;
+    if (split < (p.depth + kChain - 1) / kChain) split = (p.depth + kChain - 1) / kChain;
     if (split > kMaxSplit) split = kMaxSplit;
     if (split > p.depth) split = p.depth;
     p.split = split < 1 ? 1 : (int32_t)split;

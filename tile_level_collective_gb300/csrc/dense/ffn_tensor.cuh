@@ -140,6 +140,21 @@ __device__ __forceinline__ void bar_less(uint64_t* bar, uint32_t bytes)
                  : "memory");
 }
 
+// Sixteen columns from `lo_at` and from `hi_at` on of this thread's row of tensor memory.
+__device__ __forceinline__ void store_columns(uint32_t lo_at, uint32_t hi_at, const float (&lo)[16], const float (&hi)[16])
+{
+    auto store = [](uint32_t at, const float (&v)[16]) {
+        asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 "
+                     "[%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+                     ::"r"(at), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+                       "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+                     : "memory");
+    };
+    store(lo_at, lo);
+    store(hi_at, hi);
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void remote_write(uint32_t addr, uint32_t v)
 {
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
@@ -240,11 +255,14 @@ struct Tile {
     }
     // The stages of a tile of a problem: of the planes of its contraction, which are
     // dg and du in dx, and the parts.
-    static __device__ __forceinline__ uint32_t stages(const ProductParams& p, uint32_t which)
+    static __host__ __device__ __forceinline__ uint32_t stages(uint32_t depth, uint32_t parts, uint32_t which)
     {
         const bool two = PRODUCT == kBackX || (PRODUCT == kGrad && which == 0);
-        const uint32_t planes = PRODUCT == kIn || PRODUCT == kBackIn ? 1u : (uint32_t)p.parts * (two ? 2u : 1u);
-        return (uint32_t)p.q[which].depth * planes;
+        return depth * (PRODUCT == kIn || PRODUCT == kBackIn ? 1u : two ? 2 * parts : parts);
+    }
+    static __device__ __forceinline__ uint32_t stages(const ProductParams& p, uint32_t which)
+    {
+        return stages((uint32_t)p.q[which].depth, (uint32_t)p.parts, which);
     }
     // The planes of A and of B in plane n of the contraction. (What has parts lies
     // as dg, du, h and then their second parts.)
@@ -259,6 +277,26 @@ struct Tile {
         if (PRODUCT == kBackX || (PRODUCT == kGrad && which == 0)) return n & 1;
         return PRODUCT == kGrad && which == 2 ? 3 * n : 0;
     }
+};
+
+// The sums of a tile deeper than kChain stages are taken at every chain's end and added up in
+// the other accumulator's columns (its drains are then not hidden: about 1 % of its time).
+// Where a tile's sums stand: which accumulator, and how often each was used before.
+// Tiles take the two in turn; a deep one takes the first for all its chains (its sums so far
+// are in the second), and so does the tile after it, which waits until both are read.
+// DEEP: there are such tiles. (The same for all: dx and the weights' gradients of 512 tokens
+// of 4096 x 12288 209 us instead of 205.)
+template <bool DEEP>
+struct Turn {
+    uint32_t b = 0, used[2] = {0, 0};
+    static __device__ __forceinline__ uint32_t chains(uint32_t stages)
+    {
+        return DEEP ? (stages + (uint32_t)kChain - 1) / (uint32_t)kChain : 1u;
+    }
+    __device__ __forceinline__ void begin(uint32_t chains) { b = DEEP && chains > 1 ? 0 : b; }
+    __device__ __forceinline__ uint32_t phase() const { return (b ? used[1] : used[0]) & 1; }
+    __device__ __forceinline__ void next() { ++(b ? used[1] : used[0]); }
+    __device__ __forceinline__ void end(uint32_t chains) { b = DEEP && chains > 1 ? 0 : b ^ 1; }
 };
 
 // Eight neighbouring elements.
@@ -363,10 +401,37 @@ struct DrainBuffers {
     }
 };
 
+// Sixteen columns of an accumulator from `lo_at` and from `hi_at` on; more: and what
+// earlier chains of the tile left, BN columns further on.
+template <int BN, bool DEEP>
+__device__ __forceinline__ void load_sums(uint32_t lo_at, uint32_t hi_at, bool more, float (&lo)[16], float (&hi)[16])
+{
+    load_columns(lo_at, hi_at, lo, hi);
+    if (!DEEP || !more) return;
+    float a[16], b[16];
+    load_columns(lo_at + BN, hi_at + BN, a, b);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) lo[i] += a[i], hi[i] += b[i];
+}
+
+// A chain's sums of a warp's part of a tile, to those of the chains before it.
+template <int PRODUCT, int BN>
+__device__ __forceinline__ void keep_sums(uint32_t acc, bool more)
+{
+    constexpr int kColumns = PRODUCT == kIn ? BN / 4 : BN / 2, kStep = PRODUCT == kIn ? 16 : 32;
+#pragma unroll 1
+    for (int c = 0; c < kColumns; c += kStep) {
+        const uint32_t lo_at = acc + c, hi_at = lo_at + (PRODUCT == kIn ? BN / 2 : 16);
+        float lo[16], hi[16];
+        load_sums<BN, true>(lo_at, hi_at, more, lo, hi);
+        store_columns(lo_at + BN, hi_at + BN, lo, hi);
+    }
+}
+
 // A warp's part of a tile: rows row0 to row0 + 31 (of plane `plane`), the
-// accumulator's columns from `acc` on, which are the result's from col0 on.
-template <class T, int PRODUCT, int ACT, int BN, int PARTS>
-__device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf, uint32_t acc, int64_t row0,
+// accumulator's columns from `acc` on, which are the result's from col0 on. more: see load_sums.
+template <class T, int PRODUCT, int ACT, int BN, int PARTS, bool DEEP>
+__device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf, uint32_t acc, bool more, int64_t row0,
                                       int64_t plane, int64_t col0, const Problem& q)
 {
     if (row0 >= q.rows) return;
@@ -380,7 +445,7 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 float vg[16], vu[16], vh[16];
-                load_columns(acc + c + 16 * k, acc + BN / 2 + c + 16 * k, vg, vu);
+                load_sums<BN, DEEP>(acc + c + 16 * k, acc + BN / 2 + c + 16 * k, more, vg, vu);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) vh[i] = act_value<ACT>(vg[i]) * vu[i];
 #pragma unroll
@@ -400,7 +465,7 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
         } else if constexpr (PRODUCT == kBackIn) {
             // (the first chunk's g and u are on their way already)
             float dh[32];
-            load_columns(acc + c, acc + c + 16, *(float(*)[16])dh, *(float(*)[16])(dh + 16));
+            load_sums<BN, DEEP>(acc + c, acc + c + 16, more, *(float(*)[16])dh, *(float(*)[16])(dh + 16));
             buf.fetched();
             if constexpr (PARTS == 1) {
                 uint4 dg[4], du[4], h[4];
@@ -453,7 +518,7 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
             if (c + kChunk < kColumns) buf.template fetch<T>(p, row0, col0 + c + kChunk);
         } else {
             float v[32];
-            load_columns(acc + c, acc + c + 16, *(float(*)[16])v, *(float(*)[16])(v + 16));
+            load_sums<BN, DEEP>(acc + c, acc + c + 16, more, *(float(*)[16])v, *(float(*)[16])(v + 16));
             uint4 w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = pack8<T>(v + 8 * i);
@@ -462,7 +527,7 @@ __device__ __forceinline__ void drain(const ProductParams& p, DrainBuffers& buf,
     }
 }
 
-template <class T, int PRODUCT, int ACT, int BN, int PARTS>
+template <class T, int PRODUCT, int ACT, int BN, int PARTS, bool DEEP>
 __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_constant__ ProductParams p)
 {
     extern __shared__ unsigned char raw[];
@@ -552,61 +617,79 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
     }
 
     if (warp == 1 && rank == 0) {
-        uint32_t n = 0, slot = 0, turn = 0, t;
+        uint32_t slot = 0, turn = 0, t;
         bool ok = true, ready = false;      // ready: the next stage is known to have landed
+        Turn<DEEP> acc;
         const uint64_t desc_b = operand_at<kB>(ring + kABytes, 0);
-        for (; ok && order.tile(p, n, t); ++n) {
-            const uint32_t b = n & 1, d = tmem + b * BN;
+        for (uint32_t i = 0; ok && order.tile(p, i, t); ++i) {
             const uint32_t which = PRODUCT == kGrad ? Tile<PRODUCT>(p, t).which : 0;
             const bool by_rows = PRODUCT == kGrad && which > 0;
             const uint32_t stages = Tile<PRODUCT>::stages(p, which);
             const uint64_t desc_a = by_rows ? operand_by_rows(ring) : operand(ring);
             const uint32_t step_a = (by_rows ? 2048 : 32) >> 4, kind = kKind | (uint32_t)by_rows << 15;
-            ok = __all_sync(0xffffffffu, wait(sh, &sh.acc_empty[b], (n >> 1 & 1) ^ 1, p.wait_ns));
-            if (!ok) break;
-            fence_after();
-            for (uint32_t it = 0; it < stages; ++it) {
-                if (!ready) {
-                    ok = __all_sync(0xffffffffu, wait(sh, &sh.full[slot], turn, p.wait_ns));
-                    if (!ok) break;
-                }
+            const uint32_t chains = acc.chains(stages);
+            acc.begin(chains);
+            for (uint32_t it = 0; ok && it < stages; acc.next()) {
+                const uint32_t d = tmem + acc.b * BN, chain = DEEP ? min(stages - it, (uint32_t)kChain) : stages;
+                ok = __all_sync(0xffffffffu, wait(sh, &sh.acc_empty[acc.b], acc.phase() ^ 1, p.wait_ns));
+                if (!ok) break;
                 fence_after();
-                const uint64_t a = desc_a + slot * (kStage >> 4), w = desc_b + slot * (kStage >> 4);
-                if (elect_one()) {
+                for (uint32_t j = 0; j < chain; ++j, ++it) {
+                    if (!ready) {
+                        ok = __all_sync(0xffffffffu, wait(sh, &sh.full[slot], turn, p.wait_ns));
+                        if (!ok) break;
+                    }
+                    fence_after();
+                    const uint64_t a = desc_a + slot * (kStage >> 4), w = desc_b + slot * (kStage >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kDepth / 16; ++k)
-                        pair_mma(d, a + k * step_a, w + k * ((kB ? 2048 : 32) >> 4), kind, it > 0 || k > 0);
-                    pair_commit(&sh.empty[slot]);
+                        for (int k = 0; k < kDepth / 16; ++k)
+                            pair_mma(d, a + k * step_a, w + k * ((kB ? 2048 : 32) >> 4), kind, j > 0 || k > 0);
+                        pair_commit(&sh.empty[slot]);
+                    }
+                    __syncwarp();
+                    if (++slot == kRing) slot = 0, turn ^= 1;
+                    // asked while the products queue up: a wait after them takes longer than the queue lasts
+                    ready = __all_sync(0xffffffffu, landed(smem_u32(&sh.full[slot]), turn));
                 }
+                if (ok && elect_one()) pair_commit(&sh.acc_full[acc.b]);
                 __syncwarp();
-                if (++slot == kRing) slot = 0, turn ^= 1;
-                // asked while the products queue up: a wait after them takes longer than the queue lasts
-                ready = __all_sync(0xffffffffu, landed(smem_u32(&sh.full[slot]), turn));
             }
-            if (ok && elect_one()) pair_commit(&sh.acc_full[b]);
-            __syncwarp();
+            acc.end(chains);
         }
     }
 
     if (warp >= 4) {
-        uint32_t n = 0, t;
+        uint32_t t;
+        bool ok = true;
+        Turn<DEEP> acc;
         const int half = (warp - 4) >> 2;
         DrainBuffers buf{ring + kRing * kStage + (uint32_t)(warp - 4) * 2 * kBuffer, (uint32_t)lane};
-        for (; order.tile(p, n, t); ++n) {
-            const uint32_t b = n & 1;
+        for (uint32_t i = 0; ok && order.tile(p, i, t); ++i) {
             const Tile<PRODUCT> tile(p, t);
+            const Problem& q = p.q[PRODUCT == kGrad ? tile.which : 0];
             const int64_t row0 = (int64_t)tile.m * 2 * kRows + rank * kRows + (warp & 3) * 32;
             constexpr int kHalf = PRODUCT == kIn ? BN / 4 : BN / 2;
             const int64_t col0 = (int64_t)tile.n * 2 * kHalf + half * kHalf;
+            const uint32_t chains = acc.chains(DEEP ? tile.stages(p, PRODUCT == kGrad ? tile.which : 0) : 0);
             if constexpr (PRODUCT == kBackIn) buf.template fetch<T>(p, row0, col0);
-            if (!__all_sync(0xffffffffu, wait(sh, &sh.acc_full[b], n >> 1 & 1, p.wait_ns))) break;
-            __syncwarp();
-            fence_after();
-            drain<T, PRODUCT, ACT, BN, PARTS>(p, buf, tmem + b * BN + ((uint32_t)(warp & 3) << 21) + half * kHalf, row0,
-                                       tile.plane, col0, p.q[PRODUCT == kGrad ? tile.which : 0]);
-            __syncwarp();
-            fence_before();
-            if (lane == 0) remote_arrive(in_block(smem_u32(&sh.acc_empty[b]), 0));
+            acc.begin(chains);
+            for (uint32_t k = 0; k < chains; ++k, acc.next()) {
+                ok = __all_sync(0xffffffffu, wait(sh, &sh.acc_full[acc.b], acc.phase(), p.wait_ns));
+                if (!ok) break;
+                __syncwarp();
+                fence_after();
+                const uint32_t at = tmem + acc.b * BN + ((uint32_t)(warp & 3) << 21) + half * kHalf;
+                if (k + 1 < chains) {
+                    if constexpr (DEEP) keep_sums<PRODUCT, BN>(at, k > 0);
+                } else {
+                    drain<T, PRODUCT, ACT, BN, PARTS, DEEP>(p, buf, at, k > 0, row0, tile.plane, col0, q);
+                }
+                __syncwarp();
+                fence_before();
+                if (lane == 0) remote_arrive(in_block(smem_u32(&sh.acc_empty[acc.b]), 0));
+            }
+            acc.end(chains);
         }
         if constexpr (PRODUCT == kBackIn) buf.fetched();
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -655,14 +738,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_product_kernel(const __grid_c
 
 // ---- host side ------------------------------------------------------------------------
 
-template <class T, int PRODUCT, int ACT, int BN, int PARTS>
-cudaError_t launch_product(ProductParams& p, cudaStream_t s)
+template <class T, int PRODUCT, int ACT, int BN, int PARTS, bool DEEP>
+cudaError_t launch_tiles(ProductParams& p, cudaStream_t s)
 {
     // (at most 2^14 x 2^12 to a problem: the limits of the sizes)
     p.tiles = 0;
     for (const Problem& q : p.q) p.tiles += q.tiles_m * q.tiles_n;
     const int64_t tiles = p.tiles;
-    auto kernel = ffn_product_kernel<T, PRODUCT, ACT, BN, PARTS>;
+    auto kernel = ffn_product_kernel<T, PRODUCT, ACT, BN, PARTS, DEEP>;
     static std::atomic<uint64_t> done{0};
     const int most = sm_count() / 2 < kClusters ? sm_count() / 2 : kClusters;
     cudaLaunchConfig_t cfg = {};
@@ -679,6 +762,23 @@ cudaError_t launch_product(ProductParams& p, cudaStream_t s)
     cfg.numAttrs = programmatic_launch() ? 2 : 1;
     return launch_shared((const void*)kernel, (int)kSharedBytes<BN>, done,
                          [&] { return cudaLaunchKernelEx(&cfg, kernel, p); });
+}
+
+template <int PRODUCT>
+bool deep(const ProductParams& p)
+{
+    for (uint32_t i = 0; i < 3; ++i)
+        if (p.q[i].tiles_m && Tile<PRODUCT>::stages((uint32_t)p.q[i].depth, (uint32_t)p.parts, i) > kChain) return true;
+    return false;
+}
+
+// (deep tiles are always of 256 columns)
+template <class T, int PRODUCT, int ACT, int BN, int PARTS>
+cudaError_t launch_product(ProductParams& p, cudaStream_t s)
+{
+    if constexpr (BN == 256)
+        if (deep<PRODUCT>(p)) return launch_tiles<T, PRODUCT, ACT, BN, PARTS, true>(p, s);
+    return launch_tiles<T, PRODUCT, ACT, BN, PARTS, false>(p, s);
 }
 
 // A matrix as an operand or a result: `planes` of [rows, cols], `plane` elements apart.
@@ -745,6 +845,8 @@ cudaError_t product(ProductParams& p, const Matrix& a, const Matrix& b, const Ma
         const int64_t tiles = rows * ((out.cols + columns - 1) / columns);
         return (tiles + kClusters - 1) / kClusters * cycles;
     };
+    if (Tile<PRODUCT>::stages((uint32_t)((a.cols + kDepth - 1) / kDepth), (uint32_t)p.parts, 0) > kChain)
+        return product_of<T, PRODUCT, ACT, 256, PARTS>(p, a, b, out, s);
     const int64_t wide = cost(256, kStageCycles), middle = cost(128, 310), narrow = cost(64, 260);
     if constexpr (PRODUCT == kOut)
         if (narrow < middle && narrow < wide) return product_of<T, PRODUCT, ACT, 64, PARTS>(p, a, b, out, s);
