@@ -13,8 +13,8 @@
 // the first left, as further planes of the contraction. One makes the error of a
 // result sqrt(2) times that of its own rounding (2.35e-3 of the norm where that is
 // 1.65e-3, bf16); two make the products that read them twice as long (8192 tokens of
-// 4096 x 12288 1620 us forward where one takes 1210, 4680 backward where one takes
-// 2520; 512 tokens 133 and 100, 324 and 205).
+// 4096 x 12288 1660 us forward where one takes 1230, 4870 backward where one takes
+// 2590; 512 tokens 133 and 99, 331 and 207).
 //
 // Two SMs (a cluster of two blocks) work on one tile of 256 rows x BN columns:
 // each holds 128 rows of A and half of B's columns in shared memory, and the
